@@ -16,6 +16,12 @@
  *                              column-wise after a 16-point random-sign Hadamard
  *                              transform, optionally with an FP8 1x128 row-wise
  *                              output in the same call
+ * and serve attention from a KV cache held in NVFP4:
+ *   mxq_add_rmsnorm_quant_fp8  residual addition + RMS norm -> FP8 1x128 (the
+ *                              quantized input of a projection)
+ *   mxq_rope_append_nvfp4      rotary positions on Q and K, then K and V into a paged
+ *                              NVFP4 cache
+ *   mxq_attention_nvfp4        causal attention of ragged queries over that cache
  *
  * Conventions shared by every entry point
  *  - Pointers named *_bf16 / codes / scales / workspace are DEVICE pointers; the
@@ -388,6 +394,173 @@ mxq_status mxq_group_rht_quant_nvfp4_noalloc(const uint16_t* x_bf16, int64_t k,
                                              const mxq_nvfp4_out* rowwise,
                                              const mxq_nvfp4_out* columnwise,
                                              const mxq_fp8_out* fp8_rowwise, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Residual addition + RMS norm -> FP8 1x128: the quantizer in front of a W8A8
+ * projection, with the norm that feeds it in the same pass.  For each row:
+ *   z_i = BF16(x_i + res_i)  (nearest-even; z_i = x_i without a residual)
+ *   r   = F(1 / sqrt(sum_i z_i^2 / n + eps)), the sum and everything inside in
+ *         binary64, rounded once to binary32
+ *   y_i = fl(fl(z_i * r) * w_i)                       (FP32; no round to BF16)
+ * and then, per group of 128 consecutive y, exactly as mxq_quant_fp8_1x128
+ * (a = max |y| without NaNs, s = fl(max(a, F(1e-10)) * F(1/448)), rounded up to a
+ * power of two with MXQ_FP8_UE8M0, q = E4M3(fl(y / s)), 0x7F for a NaN).  The squares
+ * are exact and n <= 32768 of them are summed in 53 bits, so the order of the sum can
+ * change r only where the exact value lies within 2^-37 (relative) of a binary32
+ * rounding border.
+ *
+ *   x_bf16        [m][ldx] BF16;  residual [m][ld_res] BF16, or NULL
+ *   residual_out  [m][ld_res_out] BF16: z.  Required with a residual, NULL without;
+ *                 may be the residual or x itself (same pointer and stride), and
+ *                 must not overlap an input in any other way
+ *   weight_bf16   [n] BF16;  eps >= 0, finite
+ *   y_bf16        [m][ld_y] BF16(y) as well (a router's input), or NULL
+ *   q_e4m3, ldq, scales, scale strides: as mxq_quant_fp8_1x128
+ * Requirements: n % 128 == 0, n <= MXQ_RMSNORM_MAX_N (else MXQ_ERR_UNSUPPORTED); BF16
+ * strides multiples of 8, ldq of 16; pointers 16-byte aligned, scales 4-byte
+ * aligned; options in {0, MXQ_FP8_UE8M0}.  m == 0 is a successful no-op.
+ * ------------------------------------------------------------------------- */
+#define MXQ_RMSNORM_MAX_N 32768
+mxq_status mxq_add_rmsnorm_quant_fp8(const uint16_t* x_bf16, int64_t ldx, const uint16_t* residual, int64_t ld_res,
+                                     uint16_t* residual_out, int64_t ld_res_out, const uint16_t* weight_bf16,
+                                     float eps, int64_t m, int64_t n, uint32_t options,
+                                     uint16_t* y_bf16, int64_t ld_y, uint8_t* q_e4m3, int64_t ldq,
+                                     float* scales, int64_t scale_stride_row, int64_t scale_stride_group,
+                                     void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged KV cache in NVFP4.  Token t of a sequence lives in page block_table[t /
+ * page_size] of the sequence, at row t % page_size; the row of K (or V) of one head
+ * is head_dim/2 bytes of E2M1 codes (element 2i in the low nibble of byte i) and
+ * head_dim/16 E4M3 block scales, and its values are
+ *   E2M1value(code) * E4M3value(scale) * global[head]
+ * with one FP32 tensor scale per head (caller-supplied, fixed while rows written
+ * with it are in use; positive, finite and normal).  A row's codes start at
+ *   codes + page * code_stride_page + head * code_stride_head + row * code_stride_token
+ * (bytes), its scales likewise with the scale strides; K and V share the strides, so
+ * [page][head][row] and [page][row][head] orders and caches interleaved with other
+ * arrays are all expressed by them.
+ * Requirements: head_dim 64 or 128; page_size a power of two, 16 .. 2^20 (else
+ * MXQ_ERR_UNSUPPORTED); strides >= 0, code strides multiples of 16, scale strides of
+ * head_dim/16 (else MXQ_ERR_MISALIGNED); codes 16-byte, scales 8-byte, globals 4-byte
+ * aligned; rows of different (page, head, row) do not overlap.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    const float* k_global;           /* device [kv_heads] */
+    const float* v_global;           /* device [kv_heads] */
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int64_t code_stride_page;
+    int64_t code_stride_head;
+    int64_t code_stride_token;
+    int64_t scale_stride_page;
+    int64_t scale_stride_head;
+    int64_t scale_stride_token;
+} mxq_nvfp4_kv;
+
+/* Rotary positions.  Pair i (0 <= i < rot_dim/2) of a head turns by the angle
+ *   theta = fl64(position * inv_freq[i]),
+ * so a table of inverse frequencies in binary64 expresses every scaling of them for
+ * long contexts; cos and sin are formed in binary64 (error below 2^-50) and
+ *   c = F(factor * cos(theta)),  s = F(factor * sin(theta))   (one round to binary32).
+ * Pair i is elements (i, i + rot_dim/2) of the head, or (2i, 2i + 1) with
+ * MXQ_ROPE_INTERLEAVED; with (a, b) its BF16 values the rotated pair is
+ *   BF16(fl(fl(a c) - fl(b s))),  BF16(fl(fl(b c) + fl(a s))).
+ * Elements from rot_dim on stay as they are.  rot_dim: a multiple of 16, at most
+ * head_dim; 0 rotates nothing (inv_freq may then be NULL). */
+enum { MXQ_ROPE_INTERLEAVED = 1u };
+typedef struct {
+    const double* inv_freq;          /* device [rot_dim / 2] */
+    int32_t  rot_dim;
+    uint32_t flags;                  /* 0 or MXQ_ROPE_INTERLEAVED */
+    double   factor;                 /* on cos and sin (1 for plain frequencies) */
+} mxq_rope;
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions on Q and K, then K (rotated) and V appended to the cache.
+ * For every token t: q_out[t] = rope(q[t]) and, unless slots[t] is negative or not
+ * below num_pages * page_size (such a token is padding: nothing of the cache is
+ * written for it), row slots[t] % page_size of page slots[t] / page_size gets the
+ * row-wise NVFP4 encode of mxq_group_rht_quant_nvfp4 with the tensor scale g =
+ * global[head]: per 1x16 block a = max |y|, t = fl(fl(a * F(1/6)) / g),
+ * sc = E4M3(min(t, 448)); d = fl(E4M3(sc) * g), codes E2M1(fl(y / d)); a block with a
+ * NaN gets scale 0x7F and zero codes, one with sc == 0 zero codes.
+ *
+ *   q        [tokens][ld_q] BF16, head h of a token at h * head_dim; q_out the same
+ *            with ld_q_out (q_out = q with the same stride works in place; no other
+ *            overlap).  q_heads may be 0 (q, q_out then NULL)
+ *   k, v     [tokens][ld_k] / [ld_v] BF16, kv_heads heads of head_dim
+ *   positions  device int32[tokens];  slots  device int64[tokens], distinct where
+ *            they are not padding
+ *   k_values, v_values  [tokens][kv_heads][head_dim] BF16(E2M1 * E4M3 * global), the
+ *            values the cache stands for (products of the first two exact, one FP32
+ *            round by global, one to BF16), written for every token, padding
+ *            included; or NULL
+ * Requirements: strides multiples of 8 and at least heads * head_dim; BF16 pointers
+ * 16-byte aligned, positions 4-, slots and inv_freq 8-byte aligned; at least one cached
+ * head.  tokens == 0 is a successful no-op.
+ * ------------------------------------------------------------------------- */
+mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, uint16_t* q_out, int64_t ld_q_out,
+                                 const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v, int64_t tokens,
+                                 const int32_t* positions, const int64_t* slots, const mxq_rope* rope,
+                                 const mxq_nvfp4_kv* cache, uint16_t* k_values, uint16_t* v_values, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Causal attention of ragged queries over the paged NVFP4 cache.  Sequence b has
+ * seq_lens[b] cached tokens (its new ones included: append first) and the queries
+ * q[q_starts[b]] .. q[q_starts[b + 1] - 1], the last of them at position
+ * seq_lens[b] - 1; one query per sequence is a decoding step, more are a draft, a
+ * chunk or a whole prompt.  Query head h reads cached head h / (q_heads / kv_heads).
+ * The query at position p sees token t iff
+ *   t <= p  and  (window == 0 or t > p - window or t < sinks)
+ * and out = softmax(softmax_scale * q . k) . v over the tokens it sees, with FP32 (or
+ * wider) scores, maxima, sums and accumulators; 0 (and lse = -inf) where it sees none.
+ * What a query does not see never reaches its output, whatever it holds (NaN scales
+ * included).  A NaN K row it sees makes its output NaN; a NaN V block it sees makes
+ * at least that block's 16 elements NaN.
+ *
+ *   q        [total_q][ld_q] BF16, head h at h * head_dim; out alike with ld_out;
+ *            must not overlap
+ *   lse      [total_q][q_heads] FP32: the natural logarithm of the sum of exponentials
+ *            (to join parts of a softmax), or NULL
+ *   block_table  device int32 [batch][ld_table], table_pages entries of each row;
+ *   seq_lens device int32[batch]; q_starts device int32[batch + 1], ascending
+ *   max_q_len    at least the longest query run: later queries of a longer one are
+ *                left unwritten.  max_seq_len: an estimate of the longest cached
+ *                length, which sizes the split over the cache (longer sequences are
+ *                still right, only slower)
+ * Values read on the device are bounded there: a length above table_pages * page_size
+ * is read as that and a negative one as 0; rows outside [0, total_q) are not touched;
+ * a page number outside [0, num_pages) gives no access, and queries that see one of its
+ * tokens come out NaN.  Rows of q that belong to no sequence leave out and lse as they
+ * were.
+ *
+ * workspace: device memory of mxq_attention_nvfp4_workspace_size(...) bytes for the
+ * same shape (0: none needed, may be NULL), 256-byte aligned, any contents: the call's
+ * kernels meet through it in stream order and keep nothing in it between calls.  Calls
+ * that share it must be ordered.
+ * Requirements: q_heads a multiple of kv_heads; 1 <= batch <= 65535; ld_q, ld_out
+ * multiples of 8 and at least q_heads * head_dim; q, out 16-byte aligned, the others
+ * 4-byte; softmax_scale > 0 and finite; window, sinks >= 0; total_q * q_heads < 2^31.
+ * total_q == 0 or max_q_len == 0 is a successful no-op.
+ * ------------------------------------------------------------------------- */
+size_t mxq_attention_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,
+                                          int64_t total_q, int64_t max_q_len, int64_t max_seq_len,
+                                          int32_t window, int32_t sinks);
+
+mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q,
+                               uint16_t* out, int64_t ld_out, float* lse, const mxq_nvfp4_kv* cache,
+                               const int32_t* block_table, int64_t ld_table, int64_t table_pages,
+                               const int32_t* seq_lens, const int32_t* q_starts, int64_t batch,
+                               int64_t max_q_len, int64_t max_seq_len, float softmax_scale,
+                               int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 
 #ifdef __cplusplus

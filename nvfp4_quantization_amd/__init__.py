@@ -1,4 +1,5 @@
-"""mxq: MI355X-native (gfx950) block quantization of BF16 activations.
+"""mxq: MI355X-native (gfx950) block quantization of BF16 activations, and attention
+served from a KV cache in NVFP4.
 
 A thin ctypes binding of the C ABI in include/mxq.h.  The functions here only
 marshal arguments: every step of the quantization runs in the HIP kernels of
@@ -27,7 +28,9 @@ EXPORTED = ("mxq_status_string", "mxq_version", "mxq_quant_fp8_1x128", "mxq_hada
             "mxq_group_rht_quant_nvfp4_workspace_size", "mxq_group_rht_quant_nvfp4",
             "mxq_group_rht_quant_nvfp4_with_amax",
             "mxq_hadamard_quant_nvfp4_workspace_size", "mxq_hadamard_quant_nvfp4", "mxq_swiglu_quant_fp8",
-            "mxq_quant_fp8_blockwise", "mxq_hadamard_quant_fp8_ex", "mxq_group_rht_quant_nvfp4_noalloc")
+            "mxq_quant_fp8_blockwise", "mxq_hadamard_quant_fp8_ex", "mxq_group_rht_quant_nvfp4_noalloc",
+            "mxq_add_rmsnorm_quant_fp8", "mxq_rope_append_nvfp4", "mxq_attention_nvfp4_workspace_size",
+            "mxq_attention_nvfp4")
 MXQ_FP8_UE8M0 = 1
 
 
@@ -101,6 +104,17 @@ def lib() -> ctypes.CDLL:
         L.mxq_group_rht_quant_nvfp4_noalloc.restype = ctypes.c_int
         L.mxq_group_rht_quant_nvfp4_noalloc.argtypes = [p, i64, p, i64, ctypes.c_uint16, ctypes.c_uint32, p,
                                                         p, p, p, p]
+        i32, u32, f32 = ctypes.c_int32, ctypes.c_uint32, ctypes.c_float
+        L.mxq_add_rmsnorm_quant_fp8.restype = ctypes.c_int
+        L.mxq_add_rmsnorm_quant_fp8.argtypes = [p, i64, p, i64, p, i64, p, f32, i64, i64, u32, p, i64, p, i64, p,
+                                                i64, i64, p]
+        L.mxq_rope_append_nvfp4.restype = ctypes.c_int
+        L.mxq_rope_append_nvfp4.argtypes = [p, i64, i32, p, i64, p, i64, p, i64, i64, p, p, p, p, p, p, p]
+        L.mxq_attention_nvfp4_workspace_size.restype = ctypes.c_size_t
+        L.mxq_attention_nvfp4_workspace_size.argtypes = [i32, i32, i32, i64, i64, i64, i64, i32, i32]
+        L.mxq_attention_nvfp4.restype = ctypes.c_int
+        L.mxq_attention_nvfp4.argtypes = [p, i64, i32, i64, p, i64, p, p, p, i64, i64, p, p, i64, i64, i64, f32,
+                                          i32, i32, p, ctypes.c_size_t, p]
         _lib = L
     return _lib
 
@@ -526,3 +540,9 @@ def mxq_group_rht_quant_nvfp4(x: torch.Tensor, split_sections: Sequence[int], rh
     FP8 1x128 row-wise outputs of a BF16 [total_rows][k] tensor."""
     return GroupedNVFP4(x, split_sections, rht_sign_mask, flags, seed, row_offsets, col_offsets, out,
                         workspace)(stream)
+
+
+from .serve import (  # noqa: E402  (the serving calls use the helpers above)
+    MXQ_ROPE_INTERLEAVED, AddRMSNormFP8, AttentionNVFP4, AttentionResult, NVFP4KVCache, RMSNormFP8Result,
+    RopeAppendNVFP4, RopeAppendResult, RopePlan, mxq_add_rmsnorm_quant_fp8, mxq_attention_nvfp4,
+    mxq_attention_nvfp4_workspace_size, mxq_rope_append_nvfp4, rope_plan)

@@ -1,0 +1,211 @@
+// mxq_serve_api.cpp -- the C ABI of the serving calls of include/mxq.h (RMS norm ->
+// FP8, rotary append to the NVFP4 cache, attention over it): argument checks, launch
+// planning and kernel launches.  Host code only; nothing here allocates, synchronizes,
+// memsets or reads the environment.
+#include "mxq.h"
+
+#include <hip/hip_runtime_api.h>
+
+#include <cmath>
+
+#include "mxq_serve.hpp"
+
+namespace {
+
+constexpr int64_t kMaxGridThreads = 0xFFFFFFFFll;    // 1-D grids only; threads per launch < 2^32
+constexpr int64_t kMaxRows = (1ll << 31) - 128;
+constexpr int64_t kMaxElems = 1ll << 40;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// a * b < lim for a, b >= 0 and lim >= 1, without forming the product.
+bool product_below(int64_t a, int64_t b, int64_t lim) { return a == 0 || b <= (lim - 1) / a; }
+
+// A [rows][ld] array whose rows hold len elements spans fewer than kMaxElems.
+bool extent_ok(int64_t rows, int64_t ld, int64_t len) {
+    return len < kMaxElems && product_below(rows - 1, ld, kMaxElems - len);
+}
+
+// The largest index of a [rows][cols] array addressed as r * s_r + c * s_c is below
+// kMaxElems (rows, cols >= 1; s_r, s_c >= 0).
+bool index2_ok(int64_t rows, int64_t s_r, int64_t cols, int64_t s_c) {
+    if (!product_below(rows - 1, s_r, kMaxElems) || !product_below(cols - 1, s_c, kMaxElems)) return false;
+    return (rows - 1) * s_r < kMaxElems - (cols - 1) * s_c;
+}
+
+// The three strides of a cache array: its last row's first byte is below kMaxElems.
+bool index3_ok(int64_t a, int64_t sa, int64_t b, int64_t sb, int64_t c, int64_t sc) {
+    if (!index2_ok(a, sa, b, sb) || !product_below(c - 1, sc, kMaxElems)) return false;
+    return (a - 1) * sa + (b - 1) * sb < kMaxElems - (c - 1) * sc;
+}
+
+mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
+    if (!c || c->num_pages < 0 || c->kv_heads < 1 || c->page_size < 1 || c->head_dim < 1)
+        return MXQ_ERR_INVALID_ARGUMENT;
+    if (!c->k_global || !c->v_global) return MXQ_ERR_INVALID_ARGUMENT;
+    if (c->num_pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
+        return MXQ_ERR_INVALID_ARGUMENT;
+    if (c->head_dim != 64 && c->head_dim != 128) return MXQ_ERR_UNSUPPORTED;
+    if (c->page_size < 16 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1)))
+        return MXQ_ERR_UNSUPPORTED;
+    if (c->num_pages > kMaxRows) return MXQ_ERR_UNSUPPORTED;
+    const int64_t cs[3] = {c->code_stride_page, c->code_stride_head, c->code_stride_token};
+    const int64_t ss[3] = {c->scale_stride_page, c->scale_stride_head, c->scale_stride_token};
+    for (int i = 0; i < 3; ++i) {
+        if (cs[i] < 0 || ss[i] < 0) return MXQ_ERR_INVALID_ARGUMENT;
+        if (cs[i] % 16 != 0 || ss[i] % (c->head_dim / 16) != 0) return MXQ_ERR_MISALIGNED;
+    }
+    if (cs[2] < c->head_dim / 2 || ss[2] < c->head_dim / 16) return MXQ_ERR_INVALID_ARGUMENT;
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 8) || !aligned(c->v_scales, 8) ||
+        !aligned(c->k_global, 4) || !aligned(c->v_global, 4))
+        return MXQ_ERR_MISALIGNED;
+    if (c->num_pages > 0 && (!index3_ok(c->num_pages, cs[0], c->kv_heads, cs[1], c->page_size, cs[2]) ||
+                             !index3_ok(c->num_pages, ss[0], c->kv_heads, ss[1], c->page_size, ss[2])))
+        return MXQ_ERR_UNSUPPORTED;
+    int shift = 4;
+    while ((1 << shift) < c->page_size) ++shift;
+    *out = mxq::KvCache{c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->k_global, c->v_global, c->num_pages,
+                        cs[0], cs[1], cs[2], ss[0], ss[1], ss[2], shift, c->kv_heads, c->head_dim};
+    return MXQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mxq_status mxq_add_rmsnorm_quant_fp8(const uint16_t* x_bf16, int64_t ldx, const uint16_t* residual, int64_t ld_res,
+                                     uint16_t* residual_out, int64_t ld_res_out, const uint16_t* weight_bf16,
+                                     float eps, int64_t m, int64_t n, uint32_t options,
+                                     uint16_t* y_bf16, int64_t ld_y, uint8_t* q_e4m3, int64_t ldq,
+                                     float* scales, int64_t scale_stride_row, int64_t scale_stride_group,
+                                     void* stream) {
+    if (options & ~(uint32_t)MXQ_FP8_UE8M0) return MXQ_ERR_INVALID_ARGUMENT;
+    if (m < 0 || n <= 0 || ldx < n || ldq < n || scale_stride_row < 0 || scale_stride_group < 0)
+        return MXQ_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return MXQ_ERR_INVALID_ARGUMENT;
+    if ((residual != nullptr) != (residual_out != nullptr)) return MXQ_ERR_INVALID_ARGUMENT;
+    if (residual && (ld_res < n || ld_res_out < n)) return MXQ_ERR_INVALID_ARGUMENT;
+    if (y_bf16 && ld_y < n) return MXQ_ERR_INVALID_ARGUMENT;
+    if (n % 128 != 0 || ldx % 8 != 0 || ldq % 16 != 0) return MXQ_ERR_MISALIGNED;
+    if ((residual && (ld_res % 8 != 0 || ld_res_out % 8 != 0)) || (y_bf16 && ld_y % 8 != 0)) return MXQ_ERR_MISALIGNED;
+    if (n > MXQ_RMSNORM_MAX_N) return MXQ_ERR_UNSUPPORTED;
+    if (m == 0) return MXQ_OK;
+    if (!x_bf16 || !weight_bf16 || !q_e4m3 || !scales) return MXQ_ERR_INVALID_ARGUMENT;
+    if (!aligned(x_bf16, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(weight_bf16, 16) ||
+        !aligned(y_bf16, 16) || !aligned(q_e4m3, 16) || !aligned(scales, 4))
+        return MXQ_ERR_MISALIGNED;
+    if (m > kMaxRows || !extent_ok(m, ldx, n) || !extent_ok(m, ldq, n) ||
+        (residual && (!extent_ok(m, ld_res, n) || !extent_ok(m, ld_res_out, n))) || (y_bf16 && !extent_ok(m, ld_y, n)) ||
+        !index2_ok(m, scale_stride_row, n / 128, scale_stride_group))
+        return MXQ_ERR_UNSUPPORTED;
+    if (!product_below(m, 1024, kMaxGridThreads)) return MXQ_ERR_UNSUPPORTED;
+    mxq::RmsNormArgs a{x_bf16, residual, residual_out, weight_bf16, y_bf16, q_e4m3, scales, ldx, ld_res, ld_res_out,
+                       ld_y, ldq, scale_stride_row, scale_stride_group, m, (int32_t)n, eps};
+    return mxq::launch_add_rmsnorm_quant_fp8(a, (options & MXQ_FP8_UE8M0) != 0, static_cast<hipStream_t>(stream)) ==
+                   hipSuccess
+               ? MXQ_OK
+               : MXQ_ERR_HIP;
+}
+
+mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, uint16_t* q_out, int64_t ld_q_out,
+                                 const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v, int64_t tokens,
+                                 const int32_t* positions, const int64_t* slots, const mxq_rope* rope,
+                                 const mxq_nvfp4_kv* cache, uint16_t* k_values, uint16_t* v_values, void* stream) {
+    mxq::KvCache c;
+    const mxq_status st = check_cache(cache, &c);
+    if (st != MXQ_OK) return st;
+    if (!rope || (rope->flags & ~(uint32_t)MXQ_ROPE_INTERLEAVED)) return MXQ_ERR_INVALID_ARGUMENT;
+    if (tokens < 0 || q_heads < 0 || rope->rot_dim < 0 || rope->rot_dim > c.head_dim) return MXQ_ERR_INVALID_ARGUMENT;
+    if (rope->rot_dim % 16 != 0) return MXQ_ERR_MISALIGNED;
+    if (!std::isfinite(rope->factor) || (rope->rot_dim > 0 && !rope->inv_freq)) return MXQ_ERR_INVALID_ARGUMENT;
+    const int64_t qw = (int64_t)q_heads * c.head_dim, kw = (int64_t)c.kv_heads * c.head_dim;
+    if ((q_heads > 0 && (ld_q < qw || ld_q_out < qw)) || ld_k < kw || ld_v < kw) return MXQ_ERR_INVALID_ARGUMENT;
+    if ((q_heads > 0 && (ld_q % 8 != 0 || ld_q_out % 8 != 0)) || ld_k % 8 != 0 || ld_v % 8 != 0)
+        return MXQ_ERR_MISALIGNED;
+    if (tokens == 0) return MXQ_OK;
+    if ((q_heads > 0 && (!q || !q_out)) || !k || !v || !positions || !slots) return MXQ_ERR_INVALID_ARGUMENT;
+    if ((q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(positions, 4) || !aligned(slots, 8) || !aligned(rope->inv_freq, 8) || !aligned(k_values, 16) ||
+        !aligned(v_values, 16))
+        return MXQ_ERR_MISALIGNED;
+    if (q_heads > (1 << 20) || c.kv_heads > (1 << 20) || tokens > kMaxRows ||
+        (q_heads > 0 && (!extent_ok(tokens, ld_q, qw) || !extent_ok(tokens, ld_q_out, qw))) ||
+        !extent_ok(tokens, ld_k, kw) || !extent_ok(tokens, ld_v, kw) || !extent_ok(tokens, kw, kw))
+        return MXQ_ERR_UNSUPPORTED;
+    // at most one 256-thread work-group per 16 * 8 elements of every token
+    const int64_t rows = q_heads + 2ll * c.kv_heads;
+    if (!product_below(tokens, (rows * (c.head_dim / 8) + 255) / 256 * 256, kMaxGridThreads)) return MXQ_ERR_UNSUPPORTED;
+    mxq::RopeAppendArgs a{q, q_out, k, v, ld_q, ld_q_out, ld_k, ld_v, tokens, positions, slots, rope->inv_freq,
+                          rope->factor, rope->rot_dim, q_heads, k_values, v_values, c};
+    return mxq::launch_rope_append_nvfp4(a, (rope->flags & MXQ_ROPE_INTERLEAVED) != 0,
+                                         static_cast<hipStream_t>(stream)) == hipSuccess
+               ? MXQ_OK
+               : MXQ_ERR_HIP;
+}
+
+size_t mxq_attention_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,
+                                          int64_t total_q, int64_t max_q_len, int64_t max_seq_len,
+                                          int32_t window, int32_t sinks) {
+    (void)q_heads, (void)kv_heads, (void)head_dim, (void)batch, (void)total_q, (void)max_q_len, (void)max_seq_len;
+    (void)window, (void)sinks;
+    return 0;
+}
+
+mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q,
+                               uint16_t* out, int64_t ld_out, float* lse, const mxq_nvfp4_kv* cache,
+                               const int32_t* block_table, int64_t ld_table, int64_t table_pages,
+                               const int32_t* seq_lens, const int32_t* q_starts, int64_t batch,
+                               int64_t max_q_len, int64_t max_seq_len, float softmax_scale,
+                               int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    mxq::KvCache c;
+    const mxq_status st = check_cache(cache, &c);
+    if (st != MXQ_OK) return st;
+    if (q_heads < 1 || q_heads % c.kv_heads != 0 || total_q < 0 || batch < 1 || max_q_len < 0 || max_seq_len < 0 ||
+        table_pages < 0 || ld_table < table_pages || window < 0 || sinks < 0)
+        return MXQ_ERR_INVALID_ARGUMENT;
+    if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return MXQ_ERR_INVALID_ARGUMENT;
+    const int64_t width = (int64_t)q_heads * c.head_dim;
+    if (ld_q < width || ld_out < width) return MXQ_ERR_INVALID_ARGUMENT;
+    if (ld_q % 8 != 0 || ld_out % 8 != 0) return MXQ_ERR_MISALIGNED;
+    if (batch > 65535 || !product_below(total_q, q_heads, 1ll << 31) || max_q_len > kMaxRows || max_seq_len > kMaxRows)
+        return MXQ_ERR_UNSUPPORTED;
+    if (total_q == 0 || max_q_len == 0) return MXQ_OK;
+    if (!q || !out || !seq_lens || !q_starts || (table_pages > 0 && !block_table)) return MXQ_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(q_starts, 4))
+        return MXQ_ERR_MISALIGNED;
+    if (!extent_ok(total_q, ld_q, width) || !extent_ok(total_q, ld_out, width) ||
+        !extent_ok(batch, ld_table, table_pages) || table_pages > kMaxRows)
+        return MXQ_ERR_UNSUPPORTED;
+    const size_t need = mxq_attention_nvfp4_workspace_size(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len,
+                                                           max_seq_len, window, sinks);
+    if (need > 0) {
+        if (!workspace) return MXQ_ERR_INVALID_ARGUMENT;
+        if (workspace_bytes < need) return MXQ_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned(workspace, 256)) return MXQ_ERR_MISALIGNED;
+    }
+    mxq::AttnArgs a{};
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.ld_q = ld_q;
+    a.ld_out = ld_out;
+    a.table = block_table;
+    a.ld_table = ld_table;
+    a.seq_lens = seq_lens;
+    a.q_starts = q_starts;
+    a.table_pages = (int32_t)table_pages;
+    a.batch = (int32_t)batch;
+    a.q_heads = q_heads;
+    a.group = q_heads / c.kv_heads;
+    a.total_q = (int32_t)total_q;
+    a.max_q_len = (int32_t)(max_q_len < total_q ? max_q_len : total_q);
+    a.window = window;
+    a.sinks = sinks;
+    a.scale_log2 = softmax_scale * 1.44269504088896341f;
+    a.c = c;
+    return mxq::launch_attention_nvfp4(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
+}
+
+}  // extern "C"
