@@ -1,118 +1,375 @@
-// mxq_attention_nvfp4.hip -- causal attention over the paged NVFP4 cache (gfx950).
+// mxq_attention_nvfp4.hip -- causal attention over the paged NVFP4 cache (gfx950): few
+// query rows per cached head (decoding steps, drafts), and the join of split work.
 //
-// The plain form: one wave per (query, head), 64 cached tokens a step.  Lane i forms the
-// score of token i of the step; the running maximum and sum of the softmax are kept in
-// FP32, and the wave then holds 1 (head_dim 64) or 2 output elements per lane.
-#include "mxq_device.hpp"
-#include "mxq_serve.hpp"
+// The cache is read once, straight into the operands of the matrix instructions: scores
+// S^T = K Q^T and outputs O^T = V^T P^T, 64 cached tokens a step, one wave per step.
+//
+//  * An E2M1 value times its E4M3 block scale has at most six significant bits and lies
+//    in [2^-10, 2688], so the dequantized K and V are exact in FP16: one conversion and
+//    one packed FP16 product per two elements.  Q is BF16 times a power of two per row
+//    (its largest element in [2^14, 2^15)), exact in FP16 but for elements 2^-28 below the
+//    row's largest.  Scores and outputs accumulate in FP32.
+//  * The tensor scales, the softmax scale and Q's power of two are one FP32 factor on the
+//    scores and one on the outputs.
+//  * Softmax: running maximum per row in FP32, raised only when a score exceeds it by more
+//    than 2^kSlack (the outputs are then rescaled); the weights 2^(s - m + kBias) are rounded to
+//    FP16 (nearest-even) for the product with V, their FP32 values are summed.  With
+//    kBias = 9 a weight keeps all 11 bits down to 2^-23 of the row's largest and adds in
+//    down to 2^-33 of it.
+//  * S^T leaves the matrix unit with a query row per lane column and four tokens per lane
+//    register group, which is P^T's operand layout for the second product when score
+//    tile t row 4g + i is token 16 g + 4 t + i: K's rows are loaded in that order, and
+//    the weights never leave their registers.
+//  * V is staged per wave in LDS as it lies in the cache (two codes a byte, a token per
+//    row) and read back transposed (ds_read_b64_tr_b4): a lane gets the 16 tokens of one
+//    output element.  Its scales are staged as FP16, a token pair per dword.
+//
+// A work-group of four waves takes one chunk of one (sequence, cached head, rows of
+// queries) and interleaves its 64-token tiles over the waves; the waves join through LDS.
+#include "mxq_attention_nvfp4.hpp"
 
 namespace mxq {
 
 namespace {
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t m = c & 7u;
-    const float v = m < 2 ? 0.5f * (float)m : __builtin_bit_cast(float, (126u + (m >> 1)) << 23 | (m & 1u) << 22);
-    return (c & 8u) ? -v : v;
+// ---------------------------------------------------------------- a step's loads
+template <int D>
+struct StepRegs {
+    uint32_t k[4][D / 32];            // codes of this lane's K rows (score tile t): D / 4 elements each
+    uint32_t ks[4];                   // their scales (D / 64 bytes)
+    uint4 v[D / 32];                  // V codes on their way to LDS
+    uint32_t vs[D / 64];              // V scales of this lane's token
+    bool ok;                          // the page of this lane's 16 tokens may be read
+};
+
+struct Lane {
+    int lane, g, q, low;              // g = lane / 16, q = (lane / 4) % 4, low = lane % 4
+};
+
+template <int D>
+__device__ __forceinline__ void load_step(const AttnArgs& a, const int32_t* table, int len, int tile, int kvh,
+                                          const Lane& L, StepRegs<D>& s) {
+    const int tg = tile * 64 + 16 * L.q;                    // the lane's 16 tokens
+    int64_t page = 0;
+    s.ok = true;
+    if (tg < len) {
+        const int32_t p = table[tg >> a.c.page_shift];
+        s.ok = (uint32_t)p < (uint32_t)a.c.num_pages;
+        page = s.ok ? p : 0;
+    }
+    const int64_t row = tg & ((1 << a.c.page_shift) - 1);
+    const int64_t oc = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok;
+    const int64_t os = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok;
+    const uint8_t* kc = a.c.kc + oc + L.low * a.c.cs_tok + L.g * (D / 8);
+    const uint8_t* ks = a.c.ks + os + L.low * a.c.ss_tok + L.g * (D / 64);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(kc + 4 * t * a.c.cs_tok);
+            s.k[t][0] = w.x, s.k[t][1] = w.y, s.k[t][2] = w.z, s.k[t][3] = w.w;
+            s.ks[t] = *reinterpret_cast<const uint16_t*>(ks + 4 * t * a.c.ss_tok);
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(kc + 4 * t * a.c.cs_tok);
+            s.k[t][0] = w.x, s.k[t][1] = w.y;
+            s.ks[t] = ks[4 * t * a.c.ss_tok];
+        }
+    }
+    const uint8_t* vc = a.c.vc + oc;
+    const int sw = L.low ^ L.g;                             // 16-byte chunk order of the staging
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+        const int tok = D == 128 ? 4 * j + L.g : 8 * j + 2 * L.g + (sw >> 1);
+        const int chunk = D == 128 ? sw : sw & 1;
+        s.v[j] = *reinterpret_cast<const uint4*>(vc + tok * a.c.cs_tok + 16 * chunk);
+    }
+    const uint8_t* vs = a.c.vs + os + (4 * L.g + L.low) * a.c.ss_tok;
+    if constexpr (D == 128) {
+        const uint2 w = *reinterpret_cast<const uint2*>(vs);
+        s.vs[0] = w.x, s.vs[1] = w.y;
+    } else {
+        s.vs[0] = *reinterpret_cast<const uint32_t*>(vs);
+    }
 }
 
-// The page of token t (-1: none that may be read).
-__device__ __forceinline__ int64_t page_of(const AttnArgs& a, int b, int t) {
-    const int i = t >> a.c.page_shift;
-    if (i >= a.table_pages) return -1;
-    const int32_t p = a.table[(int64_t)b * a.ld_table + i];
-    return p >= 0 && p < a.c.num_pages ? p : -1;
+// ---------------------------------------------------------------- LDS of one wave
+// V codes: load j's 64 x 16 bytes at j * kVJ (64 bytes of padding keep the 16 tokens that
+// a transposing read touches in different banks); V scales as FP16 [D/16][64 tokens].
+constexpr int kVJ = 1024 + 64;
+template <int D>
+struct WaveLds {
+    static constexpr int kScales = (D / 32) * kVJ;
+    static constexpr int kBytes = kScales + (D / 16) * 128;
+};
+// The byte of V's LDS image where token k of lane group G starts its element tile dt.
+template <int D>
+__device__ __forceinline__ int v_addr(int G, int k, int dt) {
+    if constexpr (D == 128) return (k >> 2) * kVJ + 256 * (k & 3) + 64 * G + 16 * ((dt >> 1) ^ (k & 3)) + 8 * (dt & 1);
+    const int g = (k >> 1) & 3;
+    return (k >> 3) * kVJ + 256 * g + 64 * G + 16 * ((2 * (k & 1) + (dt >> 1)) ^ g) + 8 * (dt & 1);
+}
+
+// FP16 scales of this lane's token into LDS; sane: a NaN scale is written as zero.
+template <int D>
+__device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[D / 64], bool valid, const Lane& L) {
+    f16* const p = reinterpret_cast<f16*>(lds + WaveLds<D>::kScales) + 16 * L.q + 4 * L.g + L.low;
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {
+        const f16x2 a = e4m3_pair(vs[w], false), b = e4m3_pair(vs[w], true);
+        const f16 z = (f16)0.0f;
+        p[(4 * w + 0) * 64] = valid ? a.x : z;
+        p[(4 * w + 1) * 64] = valid ? a.y : z;
+        p[(4 * w + 2) * 64] = valid ? b.x : z;
+        p[(4 * w + 3) * 64] = valid ? b.y : z;
+    }
 }
 
 }  // namespace
 
-template <int D>
-__global__ __launch_bounds__(64) void k_attention_plain(const AttnArgs a) {
-    const int lane = (int)threadIdx.x;
-    const int64_t item = blockIdx.x;
-    const int qi = (int)(item / a.q_heads), head = (int)(item % a.q_heads), kvh = head / a.group;
-    // the sequence of query qi
-    int b = -1, start = 0, end = 0;
-    for (int i = 0; i < a.batch; ++i) {
-        const int s = a.q_starts[i], e = a.q_starts[i + 1];
-        if (qi >= s && qi < e) b = i, start = s, end = e;
+template <int D, int NT>
+__global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const AttnArgs a) {
+    constexpr int kWave = WaveLds<D>::kBytes;
+    constexpr int kJoin = (D / 16) * 64 * 16;               // a wave's outputs of one column tile
+    constexpr int kLds = 4 * kWave > 4 * kJoin ? 4 * kWave : 4 * kJoin;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+    __shared__ float2 join[4][NT * 16];
+
+    const int wave = (int)threadIdx.x >> 6;
+    Lane L;
+    L.lane = (int)threadIdx.x & 63;
+    L.g = L.lane >> 4, L.q = (L.lane >> 2) & 3, L.low = L.lane & 3;
+    const int col = L.lane & 15;
+
+    const int split = (int)(blockIdx.x % (unsigned)a.splits);
+    const int unit = (int)(blockIdx.x / (unsigned)a.splits);
+    const int kvh = unit % a.c.kv_heads, bt = unit / a.c.kv_heads;
+    const int b = bt / a.row_tiles, r0 = (bt - b * a.row_tiles) * (NT * 16);
+    const Seq seq = sequence(a, b);
+    const int rows = min(min(seq.nq, a.max_q_len) * a.group - r0, NT * 16);      // of this unit
+    if (rows <= 0) return;
+    const Span span = tile_span(a, seq, r0 / a.group, (r0 + rows - 1) / a.group);
+    const int used = splits_used(a, span.n);
+    if (split >= used) return;
+    const int first = split * a.chunk, last = split == used - 1 ? span.n : first + a.chunk;
+
+    // Q as the second operand of S^T = K Q^T: lane (col, g) holds elements D/4 g .. of row
+    // col, scaled to FP16 by the row's power of two
+    f16x8 q[NT][D / 32];
+    float factor[NT];
+    int pos[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = n * 16 + col;
+        const bool live = r < rows;
+        const int qi = live ? (r0 + r) / a.group : 0, head = kvh * a.group + (live ? r0 + r - qi * a.group : 0);
+        pos[n] = live ? max(seq.len - seq.nq + qi, -1) : -1;
+        const uint16_t* src = a.q + (int64_t)(seq.start + qi) * a.ld_q + (int64_t)head * D + L.g * (D / 4);
+        uint4 w[D / 32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            w[i] = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+            top = absmax_pk(absmax_pk(absmax_pk(absmax_pk(top, w[i].x), w[i].y), w[i].z), w[i].w);
+        }
+        top = fold_pk(top);
+        top = max(top, shfl_xor_u32(top, 16));
+        top = max(top, shfl_xor_u32(top, 32));
+        const float up = q_power(top, factor[n]);
+        factor[n] *= a.scale_log2 * a.c.kg[kvh];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) q[n][i] = q_operand(w[i], up);
     }
-    if (b < 0 || qi - start >= a.max_q_len) return;
-    const int64_t cap = (int64_t)a.table_pages << a.c.page_shift;
-    int64_t len64 = a.seq_lens[b];
-    len64 = len64 < 0 ? 0 : len64 > cap ? cap : len64;
-    const int len = (int)(len64 > 0x7FFFFF00ll ? 0x7FFFFF00ll : len64);
-    const int pos = len - (end - start) + (qi - start);
-    const uint16_t* q = a.q + qi * a.ld_q + (int64_t)head * D;
-    const float kg = a.c.kg[kvh], vg = a.c.vg[kvh];
-    float m = -1e30f, l = 0.0f, o[D / 64] = {};
-    for (int t0 = 0; t0 <= pos; t0 += 64) {
-        if (a.window && t0 >= a.sinks && t0 + 63 <= pos - a.window) continue;
-        const int t = t0 + lane;
-        const bool see = t <= pos && (!a.window || t > pos - a.window || t < a.sinks);
-        float x = -__builtin_inff();
-        int64_t page = -1;
-        if (see) {
-            page = page_of(a, b, t);
-            x = __builtin_nanf("");
-            if (page >= 0) {
-                const int64_t off = t & ((1 << a.c.page_shift) - 1);
-                const uint8_t* kc = a.c.kc + page * a.c.cs_page + kvh * a.c.cs_head + off * a.c.cs_tok;
-                const uint8_t* ks = a.c.ks + page * a.c.ss_page + kvh * a.c.ss_head + off * a.c.ss_tok;
-                float acc = 0.0f;
-                for (int g = 0; g < D / 16; ++g) {
-                    float part = 0.0f;
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t w = kc[g * 8 + i];
-                        const uint32_t qq = *reinterpret_cast<const uint32_t*>(q + g * 16 + 2 * i);
-                        part += e2m1_value(w) * lo_bf16(qq);
-                        part += e2m1_value(w >> 4) * hi_bf16(qq);
+
+    f32x4 o[NT][D / 16];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n] = kFloor;
+        l[n] = 0.0f;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) o[n][dt] = f32x4{0, 0, 0, 0};
+    }
+    uint8_t* const mine = lds + wave * kWave;
+    const int32_t* const table = a.table + (int64_t)b * a.ld_table;
+
+    StepRegs<D> s;
+    int i = first + wave;
+    if (i < last) load_step<D>(a, table, seq.len, span.tile(i), kvh, L, s);
+    while (i < last) {
+        const int tile = span.tile(i), t0 = tile * 64;
+        // V and its scales to LDS; tokens past the sequence or of unreadable pages get
+        // zero scales, so whatever lies there stays out
+        const bool v_valid = s.ok && t0 + 16 * L.q + 4 * L.g + L.low < seq.len;
+        const uint64_t bad = __ballot(!s.ok);
+        bool nan_here = false;
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) nan_here |= has_nan_scale(s.vs[w]);
+        const bool nan_v = __any(nan_here && v_valid);
+        uint32_t vs_keep[D / 64];
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) vs_keep[w] = s.vs[w];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) *reinterpret_cast<uint4*>(mine + j * kVJ + L.lane * 16) = s.v[j];
+        stage_scales<D>(mine, s.vs, v_valid, L);
+
+        // scores of 64 tokens: tile t row 4 g' + i' is token 16 g' + 4 t + i'
+        f32x4 x[NT][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f16x8 k[D / 32];
+            dequant_row<D>(s.k[t], s.ks[t], k);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                x[n][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                    x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[c], q[n][c], x[n][t], 0, 0, 0);
+            }
+        }
+        const int next = i + 4;
+        if (next < last) load_step<D>(a, table, seq.len, span.tile(next), kvh, L, s);
+
+        f16x8 p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            // masks only where an edge crosses the tile (uniform over the wave)
+            const bool edge = t0 + 63 > span.p_lo || (a.window && t0 <= (int64_t)span.p_hi - a.window) || bad != 0;
+            if (edge) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = t0 + 16 * L.g + 4 * t + e;
+                        const bool see = tok <= pos[n] && (!a.window || tok > pos[n] - a.window || tok < a.sinks);
+                        if ((bad >> (4 * L.g)) & 1) x[n][t][e] = __builtin_nanf("");
+                        x[n][t][e] = see ? x[n][t][e] : -__builtin_inff();
                     }
-                    acc += part * e4m3_value(ks[g]);
-                }
-                x = acc * kg * a.scale_log2;
+            }
+            softmax_step<D>(x[n], factor[n], m[n], l[n], o[n], p[n]);
+        }
+
+        if (nan_v) {
+            nan_blocks<D, NT>(mine + WaveLds<D>::kScales, L.g, p, o);
+            uint32_t clean[D / 64];
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) clean[w] = drop_nan_scales(vs_keep[w]);
+            stage_scales<D>(mine, clean, v_valid, L);
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+            const i32x2 c = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                (__attribute__((address_space(3))) i32x2*)(mine + v_addr<D>(L.g, col, dt)));
+            const f16x8* sc = reinterpret_cast<const f16x8*>(mine + WaveLds<D>::kScales + dt * 128 + L.g * 32);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const f16x8 v = e2m1_8(u ? c.y : c.x) * sc[u];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[n][u], o[n][dt], 0, 0, 0);
             }
         }
-        float top = x;
-        for (int i = 1; i < 64; i <<= 1) top = __builtin_fmaxf(top, shfl_xor_f32(top, i));
-        const float m1 = __builtin_fmaxf(m, top);
-        const float keep = __builtin_amdgcn_exp2f(m - m1);
-        const float p = see ? __builtin_amdgcn_exp2f(x - m1) : 0.0f;
-        m = m1;
-        l = l * keep + p;
+        i = next;
+    }
+
+    // join the four waves
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) o[j] *= keep;
-        for (int i = 0; i < 64; ++i) {
-            const float pi = __shfl(p, i, 64);
-            const int64_t pg = __shfl(page, i, 64);
-            if (pi == 0.0f || pg < 0) continue;                    // (uniform) unseen, or a NaN score in l
-            const int64_t off = (t0 + i) & ((1 << a.c.page_shift) - 1);
-            const uint8_t* vc = a.c.vc + pg * a.c.cs_page + kvh * a.c.cs_head + off * a.c.cs_tok;
-            const uint8_t* vs = a.c.vs + pg * a.c.ss_page + kvh * a.c.ss_head + off * a.c.ss_tok;
+    for (int n = 0; n < NT; ++n) {
+        l[n] += shfl_xor_f32(l[n], 16);
+        l[n] += shfl_xor_f32(l[n], 32);
+        if (L.g == 0) join[wave][n * 16 + col] = make_float2(m[n], l[n]);
+    }
+    const float vg = a.c.vg[kvh];
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const int d = lane + 64 * j;
-                const uint32_t c = vc[d >> 1] >> (4 * (d & 1));
-                o[j] += pi * (e2m1_value(c) * e4m3_value(vs[d >> 4]));
-            }
+    for (int n = 0; n < NT; ++n) {
+        __syncthreads();
+        float top = kFloor, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, join[w][n * 16 + col].x);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sum += join[w][n * 16 + col].y * __builtin_amdgcn_exp2f(join[w][n * 16 + col].x - top);
+        const float f = __builtin_amdgcn_exp2f(m[n] - top);
+        f32x4* const all = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) all[(wave * (D / 16) + dt) * 64 + L.lane] = o[n][dt] * f;
+        __syncthreads();
+        const int r = n * 16 + col;
+        const bool live = r < rows;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const int dt = wave * (D / 64) + j;
+            f32x4 v = all[dt * 64 + L.lane];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) v += all[(w * (D / 16) + dt) * 64 + L.lane];
+            if (live) store_rows<D>(a, seq, unit, kvh, split, used, NT * 16, r0 + r, 16 * dt + 4 * L.g, v, top, sum, vg);
         }
     }
-    for (int i = 1; i < 64; i <<= 1) l += shfl_xor_f32(l, i);
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-        const float v = l == 0.0f ? 0.0f : o[j] * vg / l;
-        a.out[qi * a.ld_out + (int64_t)head * D + lane + 64 * j] = (uint16_t)(pack_bf16(v, v) & 0xFFFFu);
-    }
-    if (a.lse && lane == 0)
-        a.lse[item] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994531f;
 }
 
-hipError_t launch_attention_nvfp4(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.total_q * a.q_heads));
-    if (a.c.head_dim == 128)
-        hipLaunchKernelGGL(k_attention_plain<128>, grid, dim3(64), 0, stream, a);
+// Joins the splits of every query row: a wave per row.
+template <int D>
+__global__ __launch_bounds__(256) void k_attention_join(const AttnArgs a) {
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = (int)threadIdx.x & 63;
+    const int tile_rows = a.tile_rows;
+    const int64_t unit = item / tile_rows;
+    const int r = (int)(item - unit * tile_rows);
+    const int kvh = (int)(unit % a.c.kv_heads);
+    const int64_t bt = unit / a.c.kv_heads;
+    const int b = (int)(bt / a.row_tiles), rt = (int)(bt - (int64_t)b * a.row_tiles);
+    if (b >= a.batch) return;
+    const Seq seq = sequence(a, b);
+    const int64_t rows = min((int64_t)seq.nq, (int64_t)a.max_q_len) * a.group;
+    const int64_t r0 = (int64_t)rt * tile_rows;
+    if (r0 + r >= rows) return;
+    const int64_t r1 = min(r0 + tile_rows, rows) - 1;
+    const Span span = tile_span(a, seq, (int)(r0 / a.group), (int)(r1 / a.group));
+    const int used = splits_used(a, span.n);
+    if (used <= 1) return;                                   // written by the first kernel
+    const float2* ml = a.part_ml + (unit * a.splits) * tile_rows + r;
+    const float* po = a.part_o + ((unit * a.splits) * tile_rows + r) * D + lane * (D / 64);
+    float top = kFloor;
+    for (int s = 0; s < used; ++s) top = __builtin_fmaxf(top, ml[(int64_t)s * tile_rows].x);
+    float sum = 0.0f, v[D / 64] = {};
+    for (int s = 0; s < used; ++s) {
+        const float2 e = ml[(int64_t)s * tile_rows];
+        const float f = __builtin_amdgcn_exp2f(e.x - top);
+        sum += e.y * f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) v[j] += po[(int64_t)s * tile_rows * D + j] * f;
+    }
+    const float vg = a.c.vg[kvh], inv = sum == 0.0f ? 0.0f : vg / sum;
+    const int qi = (int)((r0 + r) / a.group), head = kvh * a.group + (int)((r0 + r) - (int64_t)qi * a.group);
+    uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D + lane * (D / 64);
+    if constexpr (D == 128)
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v[0] * inv, v[1] * inv);
     else
-        hipLaunchKernelGGL(k_attention_plain<64>, grid, dim3(64), 0, stream, a);
+        *dst = (uint16_t)(pack_bf16(v[0] * inv, 0.0f) & 0xFFFFu);
+    if (a.lse && lane == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(top, sum);
+}
+
+hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.batch * a.row_tiles * a.c.kv_heads * a.splits));
+    if (a.c.head_dim == 128) {
+        if (a.tile_rows == 16)
+            hipLaunchKernelGGL((k_attention_rows<128, 1>), grid, dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((k_attention_rows<128, 2>), grid, dim3(256), 0, stream, a);
+    } else {
+        if (a.tile_rows == 16)
+            hipLaunchKernelGGL((k_attention_rows<64, 1>), grid, dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((k_attention_rows<64, 2>), grid, dim3(256), 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_attention_join(const AttnArgs& a, hipStream_t stream) {
+    const int64_t items = (int64_t)a.batch * a.row_tiles * a.c.kv_heads * a.tile_rows;
+    const dim3 grid((unsigned)((items + 3) / 4));
+    if (a.c.head_dim == 128)
+        hipLaunchKernelGGL(k_attention_join<128>, grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL(k_attention_join<64>, grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

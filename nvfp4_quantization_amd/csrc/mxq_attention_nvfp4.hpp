@@ -1,0 +1,213 @@
+// mxq_attention_nvfp4.hpp -- what the attention kernels share (gfx950): sequences and the
+// tiles of tokens that a set of query rows sees, dequantization into FP16 operands, one
+// softmax step, and how finished rows are stored.
+#pragma once
+
+#include "mxq_device.hpp"
+#include "mxq_serve.hpp"
+
+namespace mxq {
+
+namespace {
+
+typedef _Float16 f16;
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kFloor = -1e30f;      // the running maximum before any score (finite: no inf - inf)
+constexpr float kBias = 9.0f;         // weights are 2^(s - m + kBias): at most 2^(kSlack + kBias) = 2^14
+constexpr float kSlack = 5.0f;        // how far scores may exceed m before it is raised
+
+// ---------------------------------------------------------------- sequences and tiles
+struct Seq {
+    int len;                          // cached tokens that may be read
+    int start;                        // first query row
+    int nq;                           // queries (their positions end at len - 1)
+};
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+    Seq s;
+    const int64_t cap = min((int64_t)a.table_pages << a.c.page_shift, (int64_t)0x7FFFFF00);
+    s.len = (int)min((int64_t)max(a.seq_lens[b], 0), cap);
+    const int64_t q0 = min(max(a.q_starts[b], 0), a.total_q), q1 = min(max(a.q_starts[b + 1], 0), a.total_q);
+    s.start = (int)q0;
+    s.nq = (int)max(q1 - q0, (int64_t)0);
+    return s;
+}
+
+// The 64-token tiles that queries q_first .. q_last of a sequence see: with a window the
+// tiles of the first `sinks` tokens, then those from the first query's window on.
+struct Span {
+    int head;                         // tiles 0 .. head - 1, then
+    int body;                         // tile body and following ones
+    int n;                            // tiles in all
+    int p_lo, p_hi;                   // positions of the first and last query (>= -1)
+    __device__ __forceinline__ int tile(int i) const { return i < head ? i : body + (i - head); }
+};
+__device__ __forceinline__ Span tile_span(const AttnArgs& a, const Seq& s, int q_first, int q_last) {
+    Span r;
+    r.p_lo = max(s.len - s.nq + q_first, -1);
+    r.p_hi = max(s.len - s.nq + q_last, -1);
+    const int end = (int)(((int64_t)r.p_hi + 64) >> 6);                  // ceil((p_hi + 1) / 64)
+    const int64_t from = a.window ? max((int64_t)r.p_lo - a.window + 1, (int64_t)0) : 0;
+    r.body = (int)(from >> 6);
+    r.head = a.window ? (int)min((min((int64_t)a.sinks, from) + 63) >> 6, (int64_t)r.body) : 0;
+    r.n = r.head + max(end - r.body, 0);
+    return r;
+}
+__device__ __forceinline__ int splits_used(const AttnArgs& a, int tiles) {
+    return max(min((tiles + a.chunk - 1) / a.chunk, a.splits), 1);
+}
+
+// ---------------------------------------------------------------- FP16 operands
+// 8 E2M1 codes of a dword.
+__device__ __forceinline__ f16x8 e2m1_8(uint32_t w) {
+    const f16x2 a = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+    const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+    const f16x2 c = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+    const f16x2 d = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+    return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+// Two E4M3 codes (the low or the high half of w) as FP16 (exact; NaN stays NaN).
+__device__ __forceinline__ f16x2 e4m3_pair(uint32_t w, bool high) {
+    return high ? __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))
+                : __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+}
+// D / 4 elements of a K row (D / 32 dwords) with their D / 64 block scales.
+template <int D>
+__device__ __forceinline__ void dequant_row(const uint32_t (&w)[D / 32], uint32_t scales, f16x8 (&k)[D / 32]) {
+    const f16x2 s = e4m3_pair(scales, false);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        const f16 f = (D == 128 && c >= 2) ? s.y : s.x;
+        k[c] = e2m1_8(w[c]) * f16x8{f, f, f, f, f, f, f, f};
+    }
+}
+// Q's power of two from the BF16 bits of its row's largest magnitude: returns 2^(14 - e) for a
+// largest element in [2^e, 2^(e + 1)), and its inverse.  e is held to [-100, 127], where
+// both are normal; a row below 2^-100 only uses fewer bits, an infinite one stays infinite.
+__device__ __forceinline__ float q_power(uint32_t top, float& inverse) {
+    const int e = min(max((int)(top >> 7) - 127, -100), 127);
+    inverse = __builtin_bit_cast(float, (uint32_t)(e - 14 + 127) << 23);
+    return __builtin_bit_cast(float, (uint32_t)(14 - e + 127) << 23);
+}
+__device__ __forceinline__ f16x8 q_operand(const uint4& w, float up) {
+    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+    f16x8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = (f16)(lo_bf16(p[i]) * up);
+        r[2 * i + 1] = (f16)(hi_bf16(p[i]) * up);
+    }
+    return r;
+}
+
+// A byte of w is an E4M3 NaN (0x7F or 0xFF).
+__device__ __forceinline__ bool has_nan_scale(uint32_t w) {
+    return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+__device__ __forceinline__ uint32_t drop_nan_scales(uint32_t w) {
+    const uint32_t hit = ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+    return w & ~hit;
+}
+
+// ---------------------------------------------------------------- softmax
+// One step of 64 tokens for 16 query rows: raw scores x (lane column = row, 16 tokens a
+// lane) to FP16 weights p, with the row's maximum, its lane's share of the sum and, when
+// the maximum is raised, the outputs.  factor > 0 turns raw scores into base-2 exponents.
+// The four lanes of a row always hold the same m.
+template <int D>
+__device__ __forceinline__ void softmax_step(f32x4 (&x)[4], float factor, float& m, float& l, f32x4 (&o)[D / 16],
+                                             f16x8 (&p)[2]) {
+    float top = x[0][0];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __builtin_fmaxf(top, x[t][e]);
+    top *= factor;
+    if (__any(top > m + kSlack)) {
+        top = __builtin_fmaxf(top, shfl_xor_f32(top, 16));
+        top = __builtin_fmaxf(top, shfl_xor_f32(top, 32));
+        const float raised = __builtin_fmaxf(m, top);
+        const float f = __builtin_amdgcn_exp2f(m - raised);
+        m = raised;
+        l *= f;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) o[dt] *= f;
+    }
+    const float shift = kBias - m;
+    float part[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][e], factor, shift));
+        part[t] = (w[0] + w[1]) + (w[2] + w[3]);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const f32x2 pair = {w[e], w[e + 1]};
+            const f16x2 h = __builtin_convertvector(pair, f16x2);
+            p[t >> 1][4 * (t & 1) + e] = h.x;
+            p[t >> 1][4 * (t & 1) + e + 1] = h.y;
+        }
+    }
+    l += (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// V blocks whose scale is NaN: rows whose weight for one of their tokens is not zero get
+// NaN in the block's 16 elements, others nothing (the staged scales are cleaned after).
+template <int D, int NT>
+__device__ __forceinline__ void nan_blocks(const uint8_t* scales, int g, const f16x8 (&p)[NT][2],
+                                           f32x4 (&o)[NT][D / 16]) {
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) {
+        const f16x8* sc = reinterpret_cast<const f16x8*>(scales + dt * 128 + g * 32);
+        f16x8 hit[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const f16x8 v = sc[u];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) hit[u][j] = v[j] != v[j] ? (f16)1.0f : (f16)0.0f;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4 z = {0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(hit[u], p[n][u], z, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!(z[e] == 0.0f)) o[n][dt][e] = __builtin_nanf("");
+        }
+    }
+}
+
+// ---------------------------------------------------------------- results
+// Natural logarithm of the sum of exponentials of a row with maximum m (base 2) and biased sum.
+__device__ __forceinline__ float row_lse(float m, float sum) {
+    return sum == 0.0f ? -__builtin_inff() : ((m - kBias) + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+}
+
+// Four elements d0 .. d0 + 3 of row r of a unit: the finished output where the row has one
+// split, else the split's part.  d0 == 0 also stores the row's sums.
+template <int D>
+__device__ __forceinline__ void store_rows(const AttnArgs& a, const Seq& seq, int64_t unit, int kvh, int split, int used,
+                                           int tile_rows, int64_t r_in_seq, int d0, const f32x4& v, float m, float sum,
+                                           float vg) {
+    if (used == 1) {
+        const int qi = (int)(r_in_seq / a.group), head = kvh * a.group + (int)(r_in_seq - (int64_t)qi * a.group);
+        const float inv = sum == 0.0f ? 0.0f : vg / sum;
+        uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D + d0;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+        if (a.lse && d0 == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(m, sum);
+        return;
+    }
+    const int64_t at = (unit * a.splits + split) * tile_rows + r_in_seq % tile_rows;
+    *reinterpret_cast<f32x4*>(a.part_o + at * D + d0) = v;
+    if (d0 == 0) a.part_ml[at] = make_float2(m, sum);
+}
+
+}  // namespace
+
+}  // namespace mxq

@@ -77,7 +77,14 @@ struct AttnArgs {
     int32_t window, sinks;
     float scale_log2;                 // softmax_scale * log2(e)
     KvCache c;
+    // the plan: a unit is (sequence, row tile, cached head) with tile_rows query rows, its
+    // visible 64-token tiles in at most `splits` chunks of `chunk` (the last takes the rest)
+    int32_t tile_rows, row_tiles;
+    int32_t splits, chunk;
+    float* part_o;                    // workspace: [unit][split][tile_rows][head_dim]
+    float2* part_ml;                  // workspace: [unit][split][tile_rows] (maximum, sum)
 };
-hipError_t launch_attention_nvfp4(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_join(const AttnArgs& a, hipStream_t stream);
 
 }  // namespace mxq

@@ -69,6 +69,55 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
     return MXQ_OK;
 }
 
+// How the attention call splits its work.  A unit is (sequence, row tile, cached head).
+//   rows form    up to 32 query rows per cached head, 16 or 32 a unit: a decoding step or
+//                a draft reads the cache once.
+// The cache axis of a unit is cut into chunks of 64-token tiles so that the launch has
+// about kTargetGroups work-groups (three fit a CU, and ragged lengths want some to spare),
+// but no chunk is shorter than one tile per wave.
+constexpr int64_t kTargetGroups = 256 * 6;
+constexpr int64_t kMaxSplits = 256;
+struct AttnPlan {
+    int32_t tile_rows, row_tiles, splits, chunk;
+    int64_t units;
+    size_t ml_offset, bytes;          // workspace: parts, then maxima and sums
+};
+
+bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, int64_t total_q, int64_t max_q,
+                    int64_t max_len, int64_t window, int64_t sinks, AttnPlan* p) {
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (d != 64 && d != 128) || batch < 1 || batch > 65535 ||
+        total_q < 1 || max_q < 1 || max_len < 0 || window < 0 || sinks < 0 || !product_below(total_q, q_heads, 1ll << 31))
+        return false;
+    if (max_q > total_q) max_q = total_q;
+    const int64_t group = q_heads / kv_heads, rows = max_q * group;
+    p->tile_rows = rows <= 16 ? 16 : 32;
+    p->row_tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
+    p->units = batch * p->row_tiles * kv_heads;
+    int64_t tiles = (max_len + 63) / 64;
+    if (window > 0) {
+        const int64_t near = (window + p->tile_rows / group + 62) / 64 + 1, far = (sinks + 63) / 64;
+        tiles = tiles < near + far ? tiles : near + far;
+    }
+    if (tiles < 1) tiles = 1;
+    int64_t chunk = product_below(tiles, p->units, 1ll << 62) ? (tiles * p->units + kTargetGroups - 1) / kTargetGroups : tiles;
+    chunk = (chunk + 3) / 4 * 4;
+    int64_t splits = (tiles + chunk - 1) / chunk;
+    if (splits > kMaxSplits) {
+        chunk = (tiles + kMaxSplits - 1) / kMaxSplits;
+        chunk = (chunk + 3) / 4 * 4;
+        splits = (tiles + chunk - 1) / chunk;
+    }
+    p->splits = (int32_t)splits;
+    p->chunk = (int32_t)chunk;
+    p->ml_offset = p->bytes = 0;
+    if (splits > 1) {
+        const int64_t rows_all = p->units * splits * p->tile_rows;
+        p->ml_offset = (size_t)(rows_all * d * 4);
+        p->bytes = (size_t)((rows_all * (d * 4 + 8) + 255) / 256 * 256);
+    }
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -146,9 +195,9 @@ mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_head
 size_t mxq_attention_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,
                                           int64_t total_q, int64_t max_q_len, int64_t max_seq_len,
                                           int32_t window, int32_t sinks) {
-    (void)q_heads, (void)kv_heads, (void)head_dim, (void)batch, (void)total_q, (void)max_q_len, (void)max_seq_len;
-    (void)window, (void)sinks;
-    return 0;
+    AttnPlan p;
+    if (!plan_attention(q_heads, kv_heads, head_dim, batch, total_q, max_q_len, max_seq_len, window, sinks, &p)) return 0;
+    return p.bytes;
 }
 
 mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q,
@@ -178,11 +227,13 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
     if (!extent_ok(total_q, ld_q, width) || !extent_ok(total_q, ld_out, width) ||
         !extent_ok(batch, ld_table, table_pages) || table_pages > kMaxRows)
         return MXQ_ERR_UNSUPPORTED;
-    const size_t need = mxq_attention_nvfp4_workspace_size(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len,
-                                                           max_seq_len, window, sinks);
-    if (need > 0) {
+    AttnPlan p;
+    if (!plan_attention(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len, max_seq_len, window, sinks, &p) ||
+        !product_below(p.units * p.splits, 256, kMaxGridThreads) || !product_below(p.units, 64ll * p.tile_rows, kMaxGridThreads))
+        return MXQ_ERR_UNSUPPORTED;
+    if (p.bytes > 0) {
         if (!workspace) return MXQ_ERR_INVALID_ARGUMENT;
-        if (workspace_bytes < need) return MXQ_ERR_WORKSPACE_TOO_SMALL;
+        if (workspace_bytes < p.bytes) return MXQ_ERR_WORKSPACE_TOO_SMALL;
         if (!aligned(workspace, 256)) return MXQ_ERR_MISALIGNED;
     }
     mxq::AttnArgs a{};
@@ -205,7 +256,18 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
     a.sinks = sinks;
     a.scale_log2 = softmax_scale * 1.44269504088896341f;
     a.c = c;
-    return mxq::launch_attention_nvfp4(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
+    if (c.num_pages == 0) a.table_pages = 0;                 // no page can be read: no tokens
+    a.tile_rows = p.tile_rows;
+    a.row_tiles = p.row_tiles;
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    a.part_o = p.bytes ? reinterpret_cast<float*>(ws) : nullptr;
+    a.part_ml = p.bytes ? reinterpret_cast<float2*>(ws + p.ml_offset) : nullptr;
+    hipStream_t const hs = static_cast<hipStream_t>(stream);
+    if (mxq::launch_attention_rows(a, hs) != hipSuccess) return MXQ_ERR_HIP;
+    if (p.splits > 1 && mxq::launch_attention_join(a, hs) != hipSuccess) return MXQ_ERR_HIP;
+    return MXQ_OK;
 }
 
 }  // extern "C"

@@ -93,12 +93,12 @@ def decode_rows(codes, scales):
 # ------------------------------------------------------------------ attention
 def attention_reference(q, kc, ks, vc, vs, kg, vg, table, lens, starts, scale, window=0, sinks=0):
     """64-bit attention.  q [total][heads][d] float32; cache arrays [pages][kv][page][..]
-    (host uint8); returns out, lse, and for the tolerance the weighted mean of |v| and the
-    largest sum |q k| of each row.  Rows of no sequence come back NaN."""
+    (host uint8); returns out, lse and how far each may be off (attention_bounds).  Rows of
+    no sequence come back NaN."""
     total, hq, d = q.shape
     pages, hk, page = kc.shape[:3]
     out = np.full((total, hq, d), np.nan)
-    mean_v = np.zeros((total, hq, d))
+    mean_v, sum_v = np.zeros((total, hq, d)), np.zeros((total, hq, d))
     lse = np.full((total, hq), np.nan)
     big = np.zeros((total, hq))
     for b, n in enumerate(lens):
@@ -128,21 +128,25 @@ def attention_reference(q, kc, ks, vc, vs, kg, vg, table, lens, starts, scale, w
                     p = np.exp(x - m)
                     out[lo + i, j] = p @ v[idx] / p.sum()
                     mean_v[lo + i, j] = p @ np.abs(v[idx]) / p.sum()
+                    sum_v[lo + i, j] = np.abs(v[idx]).sum(0)
                     lse[lo + i, j] = m + np.log(p.sum())
                     big[lo + i, j] = (np.abs(k[idx]) @ np.abs(qq[i])).max() * scale
-    return out, lse, mean_v, big
+    return (out, lse, *attention_bounds(out, lse, mean_v, sum_v, big, d))
 
 
-def attention_bounds(out, lse, mean_v, big, d):
+def attention_bounds(out, lse, mean_v, sum_v, big, d):
     """How far FP32 arithmetic with BF16 output may be off.  A score: its d products are
     exact and summed in FP32 (d roundings of at most 2^-24 of sum |q k|), then scaled, shifted
     and exponentiated (4 more roundings relative to a shifted score of at most twice the
     largest, and 2^-22 for the exponential): delta.  Weights are held in 11 significant bits
-    (2^-11 each, half a step 2^-12, one part 2^-30 below the normal range) and their
-    sum in FP32; numerator and denominator both carry delta.  The output is rounded to BF16
-    (2^-8 of it, or half the smallest subnormal)."""
+    (half a step 2^-12; 2^-11 counted) and their sum in FP32; numerator and denominator both
+    carry delta.  Below FP16's normal range a weight is off by at most half its smallest
+    subnormal, 2^-25, where the row's largest weight is at least 2^9 and so is the sum: 2^-34
+    of sum |v| over the tokens seen.  All that is e; the output is then rounded to BF16: 2^-8
+    of at most |out| + e (or half the smallest subnormal)."""
     delta = (d + 8) * 2.0 ** -24 * big[..., None] + 2.0 ** -22
-    o = 2.0 ** -8 * np.abs(out) + mean_v * (2 * delta + 2.0 ** -11) * 1.05 + 2.0 ** -60
+    e = mean_v * (2 * delta + 2.0 ** -11) * 1.05 + 2.0 ** -34 * sum_v
+    o = 2.0 ** -8 * (np.abs(out) + e) + e + 2.0 ** -60
     l = delta[..., 0] + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0.0))
     return o, l
 
