@@ -33,62 +33,81 @@ namespace mxq {
 namespace {
 
 // ---------------------------------------------------------------- a step's loads
-template <int D>
-struct StepRegs {
-    uint32_t k[4][D / 32];            // codes of this lane's K rows (score tile t): D / 4 elements each
-    uint32_t ks[4];                   // their scales (D / 64 bytes)
-    uint4 v[D / 32];                  // V codes on their way to LDS
-    uint32_t vs[D / 64];              // V scales of this lane's token
-    bool ok;                          // the page of this lane's 16 tokens may be read
-};
-
 struct Lane {
     int lane, g, q, low;              // g = lane / 16, q = (lane / 4) % 4, low = lane % 4
 };
 
+// The page of the 16 tokens 16 q .. of a tile that this lane loads, raw from the table
+// (0 past the sequence: nothing of such tokens is used).
+__device__ __forceinline__ int32_t page_entry(const AttnArgs& a, const int32_t* table, int len, int tile, const Lane& L) {
+    const int tg = tile * 64 + 16 * L.q;
+    return tg < len ? table[tg >> a.c.page_shift] : 0;
+}
+
+// Where those tokens' codes and scales lie (page 0 for a page that may not be read).
+struct Place {
+    int64_t codes, scales;
+    bool ok;
+};
+__device__ __forceinline__ Place place(const AttnArgs& a, int32_t entry, int tile, int kvh, const Lane& L) {
+    Place p;
+    p.ok = (uint32_t)entry < (uint32_t)a.c.num_pages;
+    const int64_t page = p.ok ? entry : 0;
+    const int64_t row = (tile * 64 + 16 * L.q) & ((1 << a.c.page_shift) - 1);
+    p.codes = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok;
+    p.scales = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok;
+    return p;
+}
+
+// (Named members: an array indexed in the long score loop would end up in scratch.)
 template <int D>
-__device__ __forceinline__ void load_step(const AttnArgs& a, const int32_t* table, int len, int tile, int kvh,
-                                          const Lane& L, StepRegs<D>& s) {
-    const int tg = tile * 64 + 16 * L.q;                    // the lane's 16 tokens
-    int64_t page = 0;
-    s.ok = true;
-    if (tg < len) {
-        const int32_t p = table[tg >> a.c.page_shift];
-        s.ok = (uint32_t)p < (uint32_t)a.c.num_pages;
-        page = s.ok ? p : 0;
-    }
-    const int64_t row = tg & ((1 << a.c.page_shift) - 1);
-    const int64_t oc = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok;
-    const int64_t os = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok;
-    const uint8_t* kc = a.c.kc + oc + L.low * a.c.cs_tok + L.g * (D / 8);
-    const uint8_t* ks = a.c.ks + os + L.low * a.c.ss_tok + L.g * (D / 64);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(kc + 4 * t * a.c.cs_tok);
-            s.k[t][0] = w.x, s.k[t][1] = w.y, s.k[t][2] = w.z, s.k[t][3] = w.w;
-            s.ks[t] = *reinterpret_cast<const uint16_t*>(ks + 4 * t * a.c.ss_tok);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(kc + 4 * t * a.c.cs_tok);
-            s.k[t][0] = w.x, s.k[t][1] = w.y;
-            s.ks[t] = ks[4 * t * a.c.ss_tok];
-        }
-    }
-    const uint8_t* vc = a.c.vc + oc;
+struct KRegs {
+    KWords<D> w0, w1, w2, w3;         // codes of this lane's K rows (score tile t): D / 4 elements each
+    uint32_t s0, s1, s2, s3;          // their scales (D / 64 bytes)
+};
+template <int D>
+__device__ __forceinline__ uint32_t k_scales(const uint8_t* p) {
+    if constexpr (D == 128) return *reinterpret_cast<const uint16_t*>(p);
+    return *p;
+}
+template <int D>
+__device__ __forceinline__ void load_k(const AttnArgs& a, const Place& p, const Lane& L, KRegs<D>& r) {
+    const uint8_t* kc = a.c.kc + p.codes + L.low * a.c.cs_tok + L.g * (D / 8);
+    const uint8_t* ks = a.c.ks + p.scales + L.low * a.c.ss_tok + L.g * (D / 64);
+    r.w0 = *reinterpret_cast<const KWords<D>*>(kc);
+    r.w1 = *reinterpret_cast<const KWords<D>*>(kc + 4 * a.c.cs_tok);
+    r.w2 = *reinterpret_cast<const KWords<D>*>(kc + 8 * a.c.cs_tok);
+    r.w3 = *reinterpret_cast<const KWords<D>*>(kc + 12 * a.c.cs_tok);
+    r.s0 = k_scales<D>(ks);
+    r.s1 = k_scales<D>(ks + 4 * a.c.ss_tok);
+    r.s2 = k_scales<D>(ks + 8 * a.c.ss_tok);
+    r.s3 = k_scales<D>(ks + 12 * a.c.ss_tok);
+}
+
+template <int D>
+struct VRegs {
+    u32x4v w[D / 32];                 // codes on their way to LDS
+    uint32_t s[D / 64];               // scales of this lane's token
+    bool ok;
+};
+template <int D>
+__device__ __forceinline__ void load_v(const AttnArgs& a, const Place& p, const Lane& L, VRegs<D>& r) {
+    const uint8_t* vc = a.c.vc + p.codes;
     const int sw = L.low ^ L.g;                             // 16-byte chunk order of the staging
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
         const int tok = D == 128 ? 4 * j + L.g : 8 * j + 2 * L.g + (sw >> 1);
         const int chunk = D == 128 ? sw : sw & 1;
-        s.v[j] = *reinterpret_cast<const uint4*>(vc + tok * a.c.cs_tok + 16 * chunk);
+        r.w[j] = *reinterpret_cast<const u32x4v*>(vc + tok * a.c.cs_tok + 16 * chunk);
     }
-    const uint8_t* vs = a.c.vs + os + (4 * L.g + L.low) * a.c.ss_tok;
+    const uint8_t* vs = a.c.vs + p.scales + (4 * L.g + L.low) * a.c.ss_tok;
     if constexpr (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(vs);
-        s.vs[0] = w.x, s.vs[1] = w.y;
+        const u32x2v w = *reinterpret_cast<const u32x2v*>(vs);
+        r.s[0] = w.x, r.s[1] = w.y;
     } else {
-        s.vs[0] = *reinterpret_cast<const uint32_t*>(vs);
+        r.s[0] = *reinterpret_cast<const uint32_t*>(vs);
     }
+    r.ok = p.ok;
 }
 
 // ---------------------------------------------------------------- LDS of one wave
@@ -108,7 +127,7 @@ __device__ __forceinline__ int v_addr(int G, int k, int dt) {
     return (k >> 3) * kVJ + 256 * g + 64 * G + 16 * ((2 * (k & 1) + (dt >> 1)) ^ g) + 8 * (dt & 1);
 }
 
-// FP16 scales of this lane's token into LDS; sane: a NaN scale is written as zero.
+// FP16 scales of this lane's token into LDS (zero for a token that is not valid).
 template <int D>
 __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[D / 64], bool valid, const Lane& L) {
     f16* const p = reinterpret_cast<f16*>(lds + WaveLds<D>::kScales) + 16 * L.q + 4 * L.g + L.low;
@@ -120,6 +139,17 @@ __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[
         p[(4 * w + 1) * 64] = valid ? a.y : z;
         p[(4 * w + 2) * 64] = valid ? b.x : z;
         p[(4 * w + 3) * 64] = valid ? b.y : z;
+    }
+}
+
+// This lane's staged scales with NaN ones replaced by zero.
+template <int D>
+__device__ __forceinline__ void clean_scales(uint8_t* lds, const Lane& L) {
+    f16* const p = reinterpret_cast<f16*>(lds + WaveLds<D>::kScales) + 16 * L.q + 4 * L.g + L.low;
+#pragma unroll
+    for (int b = 0; b < D / 16; ++b) {
+        const f16 v = p[b * 64];
+        p[b * 64] = v != v ? (f16)0.0f : v;
     }
 }
 
@@ -191,42 +221,57 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const A
     uint8_t* const mine = lds + wave * kWave;
     const int32_t* const table = a.table + (int64_t)b * a.ld_table;
 
-    StepRegs<D> s;
+    // Loads run ahead of the step that uses them: the page table entry by two steps, V by
+    // one (its registers are free once it is in LDS), K by one (after its use).
+    KRegs<D> k;
+    VRegs<D> v;
     int i = first + wave;
-    if (i < last) load_step<D>(a, table, seq.len, span.tile(i), kvh, L, s);
+    int32_t entry = 0;
+    if (i < last) {
+        const Place at = place(a, page_entry(a, table, seq.len, span.tile(i), L), span.tile(i), kvh, L);
+        load_v<D>(a, at, L, v);
+        load_k<D>(a, at, L, k);
+        if (i + 4 < last) entry = page_entry(a, table, seq.len, span.tile(i + 4), L);
+    }
     while (i < last) {
         const int tile = span.tile(i), t0 = tile * 64;
         // V and its scales to LDS; tokens past the sequence or of unreadable pages get
         // zero scales, so whatever lies there stays out
-        const bool v_valid = s.ok && t0 + 16 * L.q + 4 * L.g + L.low < seq.len;
-        const uint64_t bad = __ballot(!s.ok);
+        const bool v_valid = v.ok && t0 + 16 * L.q + 4 * L.g + L.low < seq.len;
+        const uint64_t bad = __ballot(!v.ok);
         bool nan_here = false;
 #pragma unroll
-        for (int w = 0; w < D / 64; ++w) nan_here |= has_nan_scale(s.vs[w]);
+        for (int w = 0; w < D / 64; ++w) nan_here |= has_nan_scale(v.s[w]);
         const bool nan_v = __any(nan_here && v_valid);
-        uint32_t vs_keep[D / 64];
 #pragma unroll
-        for (int w = 0; w < D / 64; ++w) vs_keep[w] = s.vs[w];
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) *reinterpret_cast<uint4*>(mine + j * kVJ + L.lane * 16) = s.v[j];
-        stage_scales<D>(mine, s.vs, v_valid, L);
+        for (int j = 0; j < D / 32; ++j) *reinterpret_cast<u32x4v*>(mine + j * kVJ + L.lane * 16) = v.w[j];
+        stage_scales<D>(mine, v.s, v_valid, L);
+        const int next = i + 4;
+        Place at;
+        if (next < last) {
+            at = place(a, entry, span.tile(next), kvh, L);
+            load_v<D>(a, at, L, v);
+            if (next + 4 < last) entry = page_entry(a, table, seq.len, span.tile(next + 4), L);
+        }
 
         // scores of 64 tokens: tile t row 4 g' + i' is token 16 g' + 4 t + i'
         f32x4 x[NT][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            f16x8 k[D / 32];
-            dequant_row<D>(s.k[t], s.ks[t], k);
+        const auto score = [&](int t, KWords<D> w, uint32_t scales) {
+            f16x8 kk[D / 32];
+            dequant_row<D>(w, scales, kk);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 x[n][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c)
-                    x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[c], q[n][c], x[n][t], 0, 0, 0);
+                    x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk[c], q[n][c], x[n][t], 0, 0, 0);
             }
-        }
-        const int next = i + 4;
-        if (next < last) load_step<D>(a, table, seq.len, span.tile(next), kvh, L, s);
+        };
+        score(0, k.w0, k.s0);
+        score(1, k.w1, k.s1);
+        score(2, k.w2, k.s2);
+        score(3, k.w3, k.s3);
+        if (next < last) load_k<D>(a, at, L, k);
 
         f16x8 p[NT][2];
 #pragma unroll
@@ -249,10 +294,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const A
 
         if (nan_v) {
             nan_blocks<D, NT>(mine + WaveLds<D>::kScales, L.g, p, o);
-            uint32_t clean[D / 64];
-#pragma unroll
-            for (int w = 0; w < D / 64; ++w) clean[w] = drop_nan_scales(vs_keep[w]);
-            stage_scales<D>(mine, clean, v_valid, L);
+            clean_scales<D>(mine, L);
         }
         // O^T += V^T P^T
 #pragma unroll
@@ -262,10 +304,10 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const A
             const f16x8* sc = reinterpret_cast<const f16x8*>(mine + WaveLds<D>::kScales + dt * 128 + L.g * 32);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const f16x8 v = e2m1_8(u ? c.y : c.x) * sc[u];
+                const f16x8 vv = e2m1_8(u ? c.y : c.x) * sc[u];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[n][u], o[n][dt], 0, 0, 0);
+                    o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[n][u], o[n][dt], 0, 0, 0);
             }
         }
         i = next;
@@ -305,46 +347,69 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const A
     }
 }
 
-// Joins the splits of every query row: a wave per row.
+// Joins the splits of every query row: a work-group per row.  Its lanes first turn the
+// splits' maxima and sums into weights (LDS), then each wave adds every fourth split, all
+// of a lane's loads independent of one another.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_join(const AttnArgs a) {
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = (int)threadIdx.x & 63;
-    const int tile_rows = a.tile_rows;
-    const int64_t unit = item / tile_rows;
-    const int r = (int)(item - unit * tile_rows);
+    __shared__ float weight[kMaxSplits];
+    __shared__ float wave_sum[4], wave_top[4];
+    __shared__ float part[4][D];
+    const int64_t unit = blockIdx.x / (unsigned)a.tile_rows;
+    const int r = (int)(blockIdx.x % (unsigned)a.tile_rows);
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int kvh = (int)(unit % a.c.kv_heads);
     const int64_t bt = unit / a.c.kv_heads;
     const int b = (int)(bt / a.row_tiles), rt = (int)(bt - (int64_t)b * a.row_tiles);
-    if (b >= a.batch) return;
     const Seq seq = sequence(a, b);
     const int64_t rows = min((int64_t)seq.nq, (int64_t)a.max_q_len) * a.group;
-    const int64_t r0 = (int64_t)rt * tile_rows;
+    const int64_t r0 = (int64_t)rt * a.tile_rows;
     if (r0 + r >= rows) return;
-    const int64_t r1 = min(r0 + tile_rows, rows) - 1;
+    const int64_t r1 = min(r0 + a.tile_rows, rows) - 1;
     const Span span = tile_span(a, seq, (int)(r0 / a.group), (int)(r1 / a.group));
     const int used = splits_used(a, span.n);
     if (used <= 1) return;                                   // written by the first kernel
-    const float2* ml = a.part_ml + (unit * a.splits) * tile_rows + r;
-    const float* po = a.part_o + ((unit * a.splits) * tile_rows + r) * D + lane * (D / 64);
-    float top = kFloor;
-    for (int s = 0; s < used; ++s) top = __builtin_fmaxf(top, ml[(int64_t)s * tile_rows].x);
-    float sum = 0.0f, v[D / 64] = {};
-    for (int s = 0; s < used; ++s) {
-        const float2 e = ml[(int64_t)s * tile_rows];
-        const float f = __builtin_amdgcn_exp2f(e.x - top);
-        sum += e.y * f;
+    const int64_t at = unit * a.splits * a.tile_rows + r;
+    const int mine = (int)threadIdx.x;
+    const float2 ml = mine < used ? a.part_ml[at + (int64_t)mine * a.tile_rows] : make_float2(kFloor, 0.0f);
+    float top = ml.x;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) v[j] += po[(int64_t)s * tile_rows * D + j] * f;
+    for (int o = 1; o < 64; o <<= 1) top = __builtin_fmaxf(top, shfl_xor_f32(top, o));
+    if (lane == 0) wave_top[wave] = top;
+    __syncthreads();
+    top = __builtin_fmaxf(__builtin_fmaxf(wave_top[0], wave_top[1]), __builtin_fmaxf(wave_top[2], wave_top[3]));
+    const float f = __builtin_amdgcn_exp2f(ml.x - top);
+    weight[mine] = f;
+    float sum = ml.y * f;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += shfl_xor_f32(sum, o);
+    if (lane == 0) wave_sum[wave] = sum;
+    __syncthreads();
+    sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+    const float* po = a.part_o + at * D + lane * (D / 64);
+    float v[D / 64] = {};
+#pragma unroll 8
+    for (int s = wave; s < used; s += 4) {
+        const float w = weight[s];
+        const float* src = po + (int64_t)s * a.tile_rows * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) v[j] += src[j] * w;
     }
-    const float vg = a.c.vg[kvh], inv = sum == 0.0f ? 0.0f : vg / sum;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) part[wave][lane * (D / 64) + j] = v[j];
+    __syncthreads();
+    if ((int)threadIdx.x >= D / 2) return;
     const int qi = (int)((r0 + r) / a.group), head = kvh * a.group + (int)((r0 + r) - (int64_t)qi * a.group);
-    uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D + lane * (D / 64);
-    if constexpr (D == 128)
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v[0] * inv, v[1] * inv);
-    else
-        *dst = (uint16_t)(pack_bf16(v[0] * inv, 0.0f) & 0xFFFFu);
-    if (a.lse && lane == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(top, sum);
+    const float inv = sum == 0.0f ? 0.0f : a.c.vg[kvh] / sum;
+    float x[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int d = 2 * (int)threadIdx.x + j;
+        x[j] = ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) * inv;
+    }
+    uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D;
+    reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = pack_bf16(x[0], x[1]);
+    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(top, sum);
 }
 
 hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
@@ -365,7 +430,7 @@ hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
 
 hipError_t launch_attention_join(const AttnArgs& a, hipStream_t stream) {
     const int64_t items = (int64_t)a.batch * a.row_tiles * a.c.kv_heads * a.tile_rows;
-    const dim3 grid((unsigned)((items + 3) / 4));
+    const dim3 grid((unsigned)items);
     if (a.c.head_dim == 128)
         hipLaunchKernelGGL(k_attention_join<128>, grid, dim3(256), 0, stream, a);
     else

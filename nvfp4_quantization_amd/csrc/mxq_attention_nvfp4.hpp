@@ -76,7 +76,9 @@ __device__ __forceinline__ f16x2 e4m3_pair(uint32_t w, bool high) {
 }
 // D / 4 elements of a K row (D / 32 dwords) with their D / 64 block scales.
 template <int D>
-__device__ __forceinline__ void dequant_row(const uint32_t (&w)[D / 32], uint32_t scales, f16x8 (&k)[D / 32]) {
+using KWords = uint32_t __attribute__((ext_vector_type(D / 32)));
+template <int D>
+__device__ __forceinline__ void dequant_row(KWords<D> w, uint32_t scales, f16x8 (&k)[D / 32]) {
     const f16x2 s = e4m3_pair(scales, false);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
@@ -106,10 +108,6 @@ __device__ __forceinline__ f16x8 q_operand(const uint4& w, float up) {
 // A byte of w is an E4M3 NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool has_nan_scale(uint32_t w) {
     return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-}
-__device__ __forceinline__ uint32_t drop_nan_scales(uint32_t w) {
-    const uint32_t hit = ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
-    return w & ~hit;
 }
 
 // ---------------------------------------------------------------- softmax

@@ -59,6 +59,7 @@ struct RopeAppendArgs {
 hipError_t launch_rope_append_nvfp4(const RopeAppendArgs& a, bool interleaved, hipStream_t stream);
 
 // ---------------------------------------------------------------- attention
+constexpr int kMaxSplits = 256;       // chunks of one unit's cache axis (a join work-group's threads)
 struct AttnArgs {
     const uint16_t* q;
     uint16_t* out;

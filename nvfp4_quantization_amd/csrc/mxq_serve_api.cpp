@@ -76,7 +76,6 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
 // about kTargetGroups work-groups (three fit a CU, and ragged lengths want some to spare),
 // but no chunk is shorter than one tile per wave.
 constexpr int64_t kTargetGroups = 256 * 6;
-constexpr int64_t kMaxSplits = 256;
 struct AttnPlan {
     int32_t tile_rows, row_tiles, splits, chunk;
     int64_t units;
@@ -102,8 +101,8 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
     int64_t chunk = product_below(tiles, p->units, 1ll << 62) ? (tiles * p->units + kTargetGroups - 1) / kTargetGroups : tiles;
     chunk = (chunk + 3) / 4 * 4;
     int64_t splits = (tiles + chunk - 1) / chunk;
-    if (splits > kMaxSplits) {
-        chunk = (tiles + kMaxSplits - 1) / kMaxSplits;
+    if (splits > mxq::kMaxSplits) {
+        chunk = (tiles + mxq::kMaxSplits - 1) / mxq::kMaxSplits;
         chunk = (chunk + 3) / 4 * 4;
         splits = (tiles + chunk - 1) / chunk;
     }
@@ -229,7 +228,7 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
         return MXQ_ERR_UNSUPPORTED;
     AttnPlan p;
     if (!plan_attention(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len, max_seq_len, window, sinks, &p) ||
-        !product_below(p.units * p.splits, 256, kMaxGridThreads) || !product_below(p.units, 64ll * p.tile_rows, kMaxGridThreads))
+        !product_below(p.units * p.splits, 256, kMaxGridThreads) || !product_below(p.units, 256ll * p.tile_rows, kMaxGridThreads))
         return MXQ_ERR_UNSUPPORTED;
     if (p.bytes > 0) {
         if (!workspace) return MXQ_ERR_INVALID_ARGUMENT;
