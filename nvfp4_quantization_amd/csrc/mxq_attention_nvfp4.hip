@@ -193,11 +193,11 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const A
         const int qi = live ? (r0 + r) / a.group : 0, head = kvh * a.group + (live ? r0 + r - qi * a.group : 0);
         pos[n] = live ? max(seq.len - seq.nq + qi, -1) : -1;
         const uint16_t* src = a.q + (int64_t)(seq.start + qi) * a.ld_q + (int64_t)head * D + L.g * (D / 4);
-        uint4 w[D / 32];
+        u32x4v w[D / 32];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            w[i] = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+            w[i] = live ? reinterpret_cast<const u32x4v*>(src)[i] : u32x4v{0, 0, 0, 0};
             top = absmax_pk(absmax_pk(absmax_pk(absmax_pk(top, w[i].x), w[i].y), w[i].z), w[i].w);
         }
         top = fold_pk(top);
@@ -293,7 +293,18 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const A
         }
 
         if (nan_v) {
-            nan_blocks<D, NT>(mine + WaveLds<D>::kScales, L.g, p, o);
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+                const f16x8* sc = reinterpret_cast<const f16x8*>(mine + WaveLds<D>::kScales + dt * 128 + L.g * 32);
+                f16x8 hit[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const f16x8 s = sc[u];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) hit[u][j] = s[j] != s[j] ? (f16)1.0f : (f16)0.0f;
+                }
+                spread_nan<NT, D / 16>(hit, dt, p, o);
+            }
             clean_scales<D>(mine, L);
         }
         // O^T += V^T P^T

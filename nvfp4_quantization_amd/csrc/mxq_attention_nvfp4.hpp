@@ -94,7 +94,7 @@ __device__ __forceinline__ float q_power(uint32_t top, float& inverse) {
     inverse = __builtin_bit_cast(float, (uint32_t)(e - 14 + 127) << 23);
     return __builtin_bit_cast(float, (uint32_t)(14 - e + 127) << 23);
 }
-__device__ __forceinline__ f16x8 q_operand(const uint4& w, float up) {
+__device__ __forceinline__ f16x8 q_operand(const u32x4v& w, float up) {
     const uint32_t p[4] = {w.x, w.y, w.z, w.w};
     f16x8 r;
 #pragma unroll
@@ -154,29 +154,18 @@ __device__ __forceinline__ void softmax_step(f32x4 (&x)[4], float factor, float&
 }
 
 // V blocks whose scale is NaN: rows whose weight for one of their tokens is not zero get
-// NaN in the block's 16 elements, others nothing (the staged scales are cleaned after).
-template <int D, int NT>
-__device__ __forceinline__ void nan_blocks(const uint8_t* scales, int g, const f16x8 (&p)[NT][2],
-                                           f32x4 (&o)[NT][D / 16]) {
+// NaN in the block's 16 elements, others nothing.  hit: 1 where a token's block of element
+// tile dt is NaN (its staged scale is zero), in the tokens' operand order.
+template <int NT, int DT>
+__device__ __forceinline__ void spread_nan(const f16x8 (&hit)[2], int dt, const f16x8 (&p)[NT][2], f32x4 (&o)[NT][DT]) {
 #pragma unroll
-    for (int dt = 0; dt < D / 16; ++dt) {
-        const f16x8* sc = reinterpret_cast<const f16x8*>(scales + dt * 128 + g * 32);
-        f16x8 hit[2];
+    for (int n = 0; n < NT; ++n) {
+        f32x4 z = {0, 0, 0, 0};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const f16x8 v = sc[u];
+        for (int u = 0; u < 2; ++u) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(hit[u], p[n][u], z, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) hit[u][j] = v[j] != v[j] ? (f16)1.0f : (f16)0.0f;
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            f32x4 z = {0, 0, 0, 0};
-#pragma unroll
-            for (int u = 0; u < 2; ++u) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(hit[u], p[n][u], z, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!(z[e] == 0.0f)) o[n][dt][e] = __builtin_nanf("");
-        }
+        for (int e = 0; e < 4; ++e)
+            if (!(z[e] == 0.0f)) o[n][dt][e] = __builtin_nanf("");
     }
 }
 

@@ -86,6 +86,7 @@ struct AttnArgs {
     float2* part_ml;                  // workspace: [unit][split][tile_rows] (maximum, sum)
 };
 hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_prompt(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_join(const AttnArgs& a, hipStream_t stream);
 
 }  // namespace mxq

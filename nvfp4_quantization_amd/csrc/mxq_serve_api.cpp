@@ -72,10 +72,12 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
 // How the attention call splits its work.  A unit is (sequence, row tile, cached head).
 //   rows form    up to 32 query rows per cached head, 16 or 32 a unit: a decoding step or
 //                a draft reads the cache once.
+//   prompt form  more rows, 128 a unit, whose waves share the dequantized tiles.
 // The cache axis of a unit is cut into chunks of 64-token tiles so that the launch has
-// about kTargetGroups work-groups (three fit a CU, and ragged lengths want some to spare),
-// but no chunk is shorter than one tile per wave.
-constexpr int64_t kTargetGroups = 256 * 6;
+// about kRowsGroups or kPromptGroups work-groups (three or two fit a CU, and ragged lengths
+// want some to spare), but no chunk is shorter than one tile per wave.
+constexpr int64_t kRowsGroups = 256 * 6;
+constexpr int64_t kPromptGroups = 256 * 2;
 struct AttnPlan {
     int32_t tile_rows, row_tiles, splits, chunk;
     int64_t units;
@@ -89,7 +91,7 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
         return false;
     if (max_q > total_q) max_q = total_q;
     const int64_t group = q_heads / kv_heads, rows = max_q * group;
-    p->tile_rows = rows <= 16 ? 16 : 32;
+    p->tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
     p->row_tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
     p->units = batch * p->row_tiles * kv_heads;
     int64_t tiles = (max_len + 63) / 64;
@@ -98,7 +100,8 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
         tiles = tiles < near + far ? tiles : near + far;
     }
     if (tiles < 1) tiles = 1;
-    int64_t chunk = product_below(tiles, p->units, 1ll << 62) ? (tiles * p->units + kTargetGroups - 1) / kTargetGroups : tiles;
+    const int64_t groups = p->tile_rows == 128 ? kPromptGroups : kRowsGroups;
+    int64_t chunk = product_below(tiles, p->units, 1ll << 62) ? (tiles * p->units + groups - 1) / groups : tiles;
     chunk = (chunk + 3) / 4 * 4;
     int64_t splits = (tiles + chunk - 1) / chunk;
     if (splits > mxq::kMaxSplits) {
@@ -264,7 +267,8 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
     a.part_o = p.bytes ? reinterpret_cast<float*>(ws) : nullptr;
     a.part_ml = p.bytes ? reinterpret_cast<float2*>(ws + p.ml_offset) : nullptr;
     hipStream_t const hs = static_cast<hipStream_t>(stream);
-    if (mxq::launch_attention_rows(a, hs) != hipSuccess) return MXQ_ERR_HIP;
+    if ((p.tile_rows == 128 ? mxq::launch_attention_prompt(a, hs) : mxq::launch_attention_rows(a, hs)) != hipSuccess)
+        return MXQ_ERR_HIP;
     if (p.splits > 1 && mxq::launch_attention_join(a, hs) != hipSuccess) return MXQ_ERR_HIP;
     return MXQ_OK;
 }
