@@ -8,8 +8,10 @@
 // A thread turns 32 codes (head_dim 128) of K and of V of one token into FP16 per tile; two
 // tiles of LDS let that overlap the products of the tile before, one barrier a tile.
 //  * K's rows are read as operands with 16-byte loads, V's with ds_read_b64_tr_b16 (four
-//    tokens of one element a lane).  Both images are row-major, K's rows 16 bytes and V's 32
-//    bytes apart in the banks, so the eight rows (four rows' 32 bytes) of a read meet in none.
+//    tokens of one element a lane).  Both images are row-major: K's rows lie 16 bytes apart
+//    in the 64 banks, so 16 rows' chunks of a read meet in none; V's chunks are permuted
+//    by row, so that neither four rows' 64 bytes (a read) nor four rows' four quarters (a
+//    write) do.
 //  * What must not reach a row: codes past the sequence's end get a zero scale (V) or are
 //    masked (K); an unreadable page's K scales are NaN, so that only rows that see it are.
 //    A NaN V scale is staged as zero and noted; rows that see its token put NaN into that
@@ -34,11 +36,13 @@ constexpr int kRowTile = 128;         // query rows of a work-group
 
 __device__ __forceinline__ f32x16 zero16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
 
-// Row pitches of the LDS images of K and V, bytes.
+// Row pitch of K's LDS image, bytes, and the byte of 16-byte chunk c of row t of V's.
 template <int D>
 constexpr int kPitchK = 2 * D + 16;
 template <int D>
-constexpr int kPitchV = 2 * D + 32;
+__device__ __forceinline__ int v_byte(int t, int c) {
+    return t * (2 * D) + 16 * (c ^ 5 * (D == 128 ? t & 3 : (t >> 1) & 1));
+}
 
 template <int D>
 struct TileRegs {
@@ -67,7 +71,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, int32_t entry, int 
 template <int D>
 struct TileLds {
     alignas(16) uint8_t k[64 * kPitchK<D>];
-    alignas(16) uint8_t v[64 * kPitchV<D>];
+    alignas(16) uint8_t v[64 * 2 * D];
     alignas(16) uint8_t nan[64 * 4];                   // per token and quarter: its V blocks with a NaN scale
     alignas(16) int any_nan[4];                        // per storing wave: one of them is not zero
 };
@@ -87,7 +91,7 @@ __device__ __forceinline__ void store_tile(TileLds<D>& lds, const TileRegs<D>& r
     dequant_row<D>(r.v, vs & ~(hit * 0xFFu), x);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
-        *reinterpret_cast<f16x8*>(lds.v + t * kPitchV<D> + part * (D / 2) + 16 * c) = x[c];
+        *reinterpret_cast<f16x8*>(lds.v + v_byte<D>(t, part * (D / 32) + c)) = x[c];
     lds.nan[t * 4 + part] = (uint8_t)((hit | hit >> 7) & 3u);
     const int any = __any(hit != 0);
     if ((t & 15) == 0 && part == 0) lds.any_nan[t >> 4] = any;
@@ -169,7 +173,10 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
         }
     }
     const int k_lane = col * kPitchK<D> + 16 * h;
-    const int v_lane = (4 * h + ((lane & 15) >> 2)) * kPitchV<D> + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+    int v_lane[D / 32];                                // (rows 8 apart keep the chunk order)
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+        v_lane[dt] = v_byte<D>(4 * h + ((lane & 15) >> 2), 4 * dt + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) + 8 * (lane & 1);
 
     // One tile: its products from `now`, the next tile into `then`.
     const auto step = [&](int i, TileLds<D>& now, TileLds<D>& then) {
@@ -259,7 +266,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
-                    now.v + v_lane + (16 * f + 8 * e) * kPitchV<D> + 64 * dt));
+                    now.v + v_lane[dt] + (16 * f + 8 * e) * (2 * D)));
             return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
         };
         f16x8 v[2][D / 32], p[2];
