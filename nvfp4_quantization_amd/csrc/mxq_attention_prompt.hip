@@ -17,11 +17,11 @@
 //    A NaN V scale is staged as zero and noted; rows that see its token put NaN into that
 //    block at the end.
 //
-// Instructions are placed so that the matrix unit runs beside the rest: the next tile's
-// dequantization between the products with K, the weights between those with V, operands
-// read from LDS some products ahead.  The tile loop is unrolled over the two LDS images, as
-// separate arrays: with one array and a dynamic buffer index the compiler orders every read
-// after the other image's writes.
+// Instructions are placed so that the matrix unit runs beside the rest: the weights of a tile
+// between the next tile's products with K, dequantization between the products with V,
+// operands read from LDS some products ahead.  The tile loop is unrolled over the two LDS
+// images, as separate arrays: with one array and a dynamic buffer index the compiler orders
+// every read after the other image's writes.
 #include "mxq_attention_nvfp4.hpp"
 
 namespace mxq {
@@ -31,6 +31,7 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRowTile = 128;         // query rows of a work-group
 
@@ -44,64 +45,105 @@ __device__ __forceinline__ int v_byte(int t, int c) {
     return t * (2 * D) + 16 * (c ^ 5 * (D == 128 ? t & 3 : (t >> 1) & 1));
 }
 
+// A thread's share of one tile's K or V: D / 4 codes of one token and their scales.
 template <int D>
-struct TileRegs {
-    KWords<D> k, v;                   // D / 4 codes of this thread's token
-    uint32_t ks, vs;                  // their scales (D / 64 bytes)
+struct Part {
+    KWords<D> w;
+    uint32_t s;                       // D / 64 bytes
     bool ok;                          // the token's page may be read
 };
-
+// Where it lies.
+struct Spot {
+    int64_t codes, scales;
+    bool ok;
+};
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, int32_t entry, int t, int kvh, int part, TileRegs<D>& r) {
+__device__ __forceinline__ Spot spot(const AttnArgs& a, int32_t entry, int t, int kvh, int part) {
+    Spot r;
     r.ok = (uint32_t)entry < (uint32_t)a.c.num_pages;
     const int64_t page = r.ok ? entry : 0, row = t & ((1 << a.c.page_shift) - 1);
-    const int64_t oc = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok + part * (D / 8);
-    const int64_t os = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok + part * (D / 64);
-    r.k = *reinterpret_cast<const KWords<D>*>(a.c.kc + oc);
-    r.v = *reinterpret_cast<const KWords<D>*>(a.c.vc + oc);
-    if constexpr (D == 128) {
-        r.ks = *reinterpret_cast<const uint16_t*>(a.c.ks + os);
-        r.vs = *reinterpret_cast<const uint16_t*>(a.c.vs + os);
-    } else {
-        r.ks = a.c.ks[os];
-        r.vs = a.c.vs[os];
-    }
+    r.codes = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok + part * (D / 8);
+    r.scales = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok + part * (D / 64);
+    return r;
+}
+template <int D>
+__device__ __forceinline__ void load_part(const uint8_t* codes, const uint8_t* scales, const Spot& at, Part<D>& r) {
+    r.w = *reinterpret_cast<const KWords<D>*>(codes + at.codes);
+    if constexpr (D == 128)
+        r.s = *reinterpret_cast<const uint16_t*>(scales + at.scales);
+    else
+        r.s = scales[at.scales];
+    r.ok = at.ok;
 }
 
 template <int D>
-struct TileLds {
-    alignas(16) uint8_t k[64 * kPitchK<D>];
-    alignas(16) uint8_t v[64 * 2 * D];
+struct KImage {
+    alignas(16) uint8_t b[64 * kPitchK<D>];
+};
+template <int D>
+struct VImage {
+    alignas(16) uint8_t b[64 * 2 * D];
     alignas(16) uint8_t nan[64 * 4];                   // per token and quarter: its V blocks with a NaN scale
     alignas(16) int any_nan[4];                        // per storing wave: one of them is not zero
 };
 
-// The thread's share of a tile into LDS.
+// The scales a part is dequantized with, as FP16: K's are NaN where the page may not be
+// read; V's are zero there, past the sequence and where they are NaN, and the latter are
+// noted (a byte per thread, a word per wave).
 template <int D>
-__device__ __forceinline__ void store_tile(TileLds<D>& lds, const TileRegs<D>& r, int t, bool valid, int part) {
-    const uint32_t nan = D == 128 ? 0x7F7Fu : 0x7Fu;
-    f16x8 x[D / 32];
-    dequant_row<D>(r.k, r.ok ? r.ks : nan, x);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-        *reinterpret_cast<f16x8*>(lds.k + t * kPitchK<D> + part * (D / 2) + 16 * c) = x[c];
-    const uint32_t vs = valid && r.ok ? r.vs : 0u;
-    // a NaN scale byte keeps its seven bits only in `hit` (bit 0: its low block, bit 8: its high one)
-    const uint32_t hit = (((vs & 0x7F7Fu) + 0x0101u) & 0x8080u) >> 7;
-    dequant_row<D>(r.v, vs & ~(hit * 0xFFu), x);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-        *reinterpret_cast<f16x8*>(lds.v + v_byte<D>(t, part * (D / 32) + c)) = x[c];
+__device__ __forceinline__ f16x2 k_factors(const Part<D>& r) {
+    return e4m3_pair(r.ok ? r.s : (D == 128 ? 0x7F7Fu : 0x7Fu), false);
+}
+template <int D>
+__device__ __forceinline__ f16x2 v_factors(const Part<D>& r, bool valid, VImage<D>& lds, int t, int part) {
+    const uint32_t s = valid && r.ok ? r.s : 0u;
+    const uint32_t hit = (((s & 0x7F7Fu) + 0x0101u) & 0x8080u) >> 7;     // bit 0: the low block, bit 8: the high one
     lds.nan[t * 4 + part] = (uint8_t)((hit | hit >> 7) & 3u);
     const int any = __any(hit != 0);
     if ((t & 15) == 0 && part == 0) lds.any_nan[t >> 4] = any;
+    return e4m3_pair(s & ~(hit * 0xFFu), false);
+}
+// Four elements: the low or high half of code dword c of a part.
+template <int D>
+__device__ __forceinline__ f16x4 dequant_half(const KWords<D>& w, f16x2 factors, int c, int half) {
+    const f16 f = (D == 128 && c >= 2) ? factors.y : factors.x;
+    const f16x2 a = __builtin_bit_cast(f16x2, half ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[c], 1.0f, 2)
+                                                   : __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[c], 1.0f, 0));
+    const f16x2 b = __builtin_bit_cast(f16x2, half ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[c], 1.0f, 3)
+                                                   : __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[c], 1.0f, 1));
+    return f16x4{a.x, a.y, b.x, b.y} * f16x4{f, f, f, f};
+}
+template <int D>
+__device__ __forceinline__ void store_chunk_k(KImage<D>& lds, int t, int part, int c, const f16x8& x) {
+    *reinterpret_cast<f16x8*>(lds.b + t * kPitchK<D> + part * (D / 2) + 16 * c) = x;
+}
+template <int D>
+__device__ __forceinline__ void store_chunk_v(VImage<D>& lds, int t, int part, int c, const f16x8& x) {
+    *reinterpret_cast<f16x8*>(lds.b + v_byte<D>(t, part * (D / 32) + c)) = x;
+}
+template <int D>
+__device__ __forceinline__ void store_k(KImage<D>& lds, const Part<D>& r, int t, int part) {
+    const f16x2 f = k_factors<D>(r);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+        store_chunk_k<D>(lds, t, part, c,
+                         __builtin_shufflevector(dequant_half<D>(r.w, f, c, 0), dequant_half<D>(r.w, f, c, 1), 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int D>
+__device__ __forceinline__ void store_v(VImage<D>& lds, const Part<D>& r, int t, bool valid, int part) {
+    const f16x2 f = v_factors<D>(r, valid, lds, t, part);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+        store_chunk_v<D>(lds, t, part, c,
+                         __builtin_shufflevector(dequant_half<D>(r.w, f, c, 0), dequant_half<D>(r.w, f, c, 1), 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 }  // namespace
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
-    __shared__ TileLds<D> image0, image1;
+    __shared__ KImage<D> k0, k1;
+    __shared__ VImage<D> v0, v1;
 
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 31, h = lane >> 5;
@@ -152,58 +194,70 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 
     const int32_t* const table = a.table + (int64_t)b * a.ld_table;
     const int my_tok = tid >> 2, part = tid & 3;
-    const auto entry_of = [&](int i) {
-        const int t = span.tile(i) * 64 + my_tok;
-        return t < seq.len ? table[t >> a.c.page_shift] : 0;
-    };
+    // this thread's token of tile i (the last tile past the end) and its page
+    const auto token = [&](int i) { return span.tile(min(i, last - 1)) * 64 + my_tok; };
+    const auto entry_of = [&](int i) { return table[min(token(i), seq.len - 1) >> a.c.page_shift]; };
     // the positions of this wave's rows, for its masks
     const int w_lo = max(seq.len - seq.nq + (int)((r0 + wave * 32) / a.group), -1);
     const int w_hi = max(seq.len - seq.nq + (int)((r0 + min(wave * 32 + 31, rows - 1)) / a.group), -1);
 
-    TileRegs<D> regs;
-    int32_t entry = 0;
+    constexpr int kProducts = D / 8, kAhead = 4;       // with K, and with V, per tile
     uint32_t nan_blocks = 0;                           // V blocks that this lane's tokens make NaN
-    if (first < last) {
-        load_tile<D>(a, entry_of(first), span.tile(first) * 64 + my_tok, kvh, part, regs);
-        if (first + 1 < last) entry = entry_of(first + 1);
-        store_tile<D>(image0, regs, my_tok, span.tile(first) * 64 + my_tok < seq.len, part);
-        if (first + 1 < last) {
-            load_tile<D>(a, entry, span.tile(first + 1) * 64 + my_tok, kvh, part, regs);
-            if (first + 2 < last) entry = entry_of(first + 2);
-        }
-    }
     const int k_lane = col * kPitchK<D> + 16 * h;
     int v_lane[D / 32];                                // (rows 8 apart keep the chunk order)
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
         v_lane[dt] = v_byte<D>(4 * h + ((lane & 15) >> 2), 4 * dt + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) + 8 * (lane & 1);
 
-    // One tile: its products from `now`, the next tile into `then`.
-    const auto step = [&](int i, TileLds<D>& now, TileLds<D>& then) {
-        __syncthreads();                               // this tile is whole; the other image is free
+    // Scores of a tile: token 32 T + 8 (e / 4) + 4 h + e % 4 in x[T][e].  Product n adds the
+    // 16 elements n / 2 to half T = n % 2.
+    f32x16 x[2];
+    const auto k_operand = [&](const KImage<D>& k, int n) {
+        return *reinterpret_cast<const f16x8*>(k.b + k_lane + 32 * (n & 1) * kPitchK<D> + 32 * (n >> 1));
+    };
+    const auto v_operand = [&](const VImage<D>& v, int n) {            // 16 tokens n / (D / 32), elements 32 (n % (D / 32)) ..
+        const int f = n / (D / 32), dt = n % (D / 32);
+        s16x4 r[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            r[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
+                v.b + v_lane[dt] + (16 * f + 8 * e) * (2 * D)));
+        return __builtin_bit_cast(f16x8, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+
+    // Tile i's weights and products with V share a stretch of code with the scores of
+    // tile i + 1 and the dequantization of K of tile i + 2 and V of tile i + 1, so that the
+    // matrix unit always has work beside the vector unit's.  Past the last tile the last one
+    // is staged and scored again, unused.
+    Part<D> kr, vr;
+    Spot at;                                           // of the last loaded K
+    int32_t entry = 0;
+    if (first < last) {
+        at = spot<D>(a, entry_of(first), token(first), kvh, part);
+        load_part<D>(a.c.kc, a.c.ks, at, kr);
+        load_part<D>(a.c.vc, a.c.vs, at, vr);
+        const int32_t e1 = entry_of(first + 1), e2 = entry_of(first + 2);
+        entry = entry_of(first + 3);
+        store_k<D>(k0, kr, my_tok, part);
+        store_v<D>(v0, vr, my_tok, token(first) < seq.len, part);
+        at = spot<D>(a, e1, token(first + 1), kvh, part);
+        load_part<D>(a.c.kc, a.c.ks, at, kr);
+        load_part<D>(a.c.vc, a.c.vs, at, vr);
+        store_k<D>(k1, kr, my_tok, part);
+        at = spot<D>(a, e2, token(first + 2), kvh, part);
+        load_part<D>(a.c.kc, a.c.ks, at, kr);
+        __syncthreads();
+        x[0] = x[1] = zero16();
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n)
+            x[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_operand(k0, n), q[n >> 1], x[n & 1], 0, 0, 0);
+    }
+
+    // kn, vn: images of K of tile i + 1 and V of tile i; kf, vf: free ones
+    const auto step = [&](int i, const KImage<D>& kn, KImage<D>& kf, const VImage<D>& vn, VImage<D>& vf) {
+        __syncthreads();
         const int t0 = span.tile(i) * 64;
-        const u32x4v noted = *reinterpret_cast<const u32x4v*>(now.any_nan);
-
-        // Scores: token 32 T + 8 (e / 4) + 4 h + e % 4 in x[T][e].  The next tile's
-        // dequantization (the last one's again at the end: that image is not read) runs
-        // between the products.
-        f32x16 x[2];
-#pragma unroll
-        for (int T = 0; T < 2; ++T) {
-            x[T] = zero16();
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                const f16x8 k = *reinterpret_cast<const f16x8*>(now.k + k_lane + 32 * T * kPitchK<D> + 32 * c);
-                x[T] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c], x[T], 0, 0, 0);
-            }
-        }
-        const int next = min(i + 1, last - 1);
-        store_tile<D>(then, regs, my_tok, span.tile(next) * 64 + my_tok < seq.len, part);
-        if (i + 2 < last) {
-            load_tile<D>(a, entry, span.tile(i + 2) * 64 + my_tok, kvh, part, regs);
-            if (i + 3 < last) entry = entry_of(i + 3);
-        }
-
+        const u32x4v noted = *reinterpret_cast<const u32x4v*>(vn.any_nan);
         // masks only where an edge crosses the tile for this wave's rows
         if (t0 + 63 > w_lo || (a.window && t0 <= (int64_t)w_hi - a.window)) {
 #pragma unroll
@@ -220,7 +274,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             for (int e = 0; e < 32; ++e) {
                 const int tok = t0 + 8 * (e >> 2) + 4 * h + (e & 3);
                 const bool see = tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(now.nan + 4 * (tok - t0));
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(vn.nan + 4 * (tok - t0));
                 const uint32_t blocks = D == 128 ? (w & 3u) | (w >> 6 & 0xCu) | (w >> 12 & 0x30u) | (w >> 18 & 0xC0u)
                                                  : (w & 1u) | (w >> 7 & 2u) | (w >> 14 & 4u) | (w >> 21 & 8u);
                 nan_blocks |= see ? blocks : 0u;
@@ -242,58 +296,70 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             for (int dt = 0; dt < D / 32; ++dt) o[dt] *= f;
         }
 
-        // Weights of 16 tokens at a time and their products with V: the weights and V
-        // operands of the next 16 are formed between the products.
+        // Products with K of tile i + 1, a share of tile i's weights after each; then those
+        // with V of tile i, a share of the dequantization after each.  Operands are read kAhead
+        // products before their use.  The order is fixed by hand: left alone, the compiler
+        // forms all weights first and reads each operand right before its product.
         const float shift = kBias - m;
-        const auto weights = [&](int f) {
-            float w[8];
-            f16x8 p;
+        f32x16 y[2] = {zero16(), zero16()};
+        f16x8 p[4], ahead[kAhead];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[f >> 1][8 * (f & 1) + e], factor, shift));
-            l += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        for (int n = 0; n < kAhead; ++n) ahead[n] = k_operand(kn, n);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const f32x2 pair = {w[e], w[e + 1]};
-                const f16x2 r = __builtin_convertvector(pair, f16x2);
-                p[e] = r.x;
-                p[e + 1] = r.y;
+        for (int n = 0; n < kProducts; ++n) {
+            y[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[n % kAhead], q[n >> 1], y[n & 1], 0, 0, 0);
+            ahead[n % kAhead] = n + kAhead < kProducts ? k_operand(kn, n + kAhead) : v_operand(vn, n + kAhead - kProducts);
+            constexpr int kShare = 32 / kProducts;
+#pragma unroll
+            for (int e = n * kShare; e < (n + 1) * kShare; e += 2) {
+                const f32x2 w = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 4][e & 15], factor, shift)),
+                                 __builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 4][(e & 15) + 1], factor, shift))};
+                l += w.x + w.y;
+                const f16x2 r = __builtin_convertvector(w, f16x2);
+                p[e >> 3][e & 7] = r.x;
+                p[e >> 3][(e & 7) + 1] = r.y;
             }
-            return p;
-        };
-        const auto v_operand = [&](int f, int dt) {
-            s16x4 v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
-                    now.v + v_lane[dt] + (16 * f + 8 * e) * (2 * D)));
-            return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        };
-        f16x8 v[2][D / 32], p[2];
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) v[0][dt] = v_operand(0, dt);
-        p[0] = weights(0);
-        __builtin_amdgcn_sched_group_barrier(0x100, D / 16, 0);            // reads
-        __builtin_amdgcn_sched_group_barrier(0x002, 48, 0);                // vector instructions
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            if (f < 3) {
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) v[(f + 1) & 1][dt] = v_operand(f + 1, dt);
-                p[(f + 1) & 1] = weights(f + 1);
-                __builtin_amdgcn_sched_group_barrier(0x100, D / 16, 0);
-            }
-#pragma unroll
-            for (int dt = 0; dt < D / 32; ++dt) {
-                o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[f & 1][dt], p[f & 1], o[dt], 0, 0, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);         // a product
-                if (f < 3) __builtin_amdgcn_sched_group_barrier(0x002, 40 / (D / 32), 0);
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        f16x4 low = {};
+        f16x2 fk, fv;
+        Spot at_v;
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+            o[n % (D / 32)] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[n % kAhead], p[n / (D / 32)], o[n % (D / 32)], 0, 0, 0);
+            if (n + kAhead < kProducts) ahead[n % kAhead] = v_operand(vn, n + kAhead);
+            const int c = (n >> 1) % (D / 32);
+            const bool is_v = n >= kProducts / 2;
+            if (n == 0) fk = k_factors<D>(kr);
+            if (n == kProducts / 2) fv = v_factors<D>(vr, token(i + 1) < seq.len, vf, my_tok, part);
+            const f16x4 half = is_v ? dequant_half<D>(vr.w, fv, c, n & 1) : dequant_half<D>(kr.w, fk, c, n & 1);
+            if (n & 1) {
+                const f16x8 whole = __builtin_shufflevector(low, half, 0, 1, 2, 3, 4, 5, 6, 7);
+                if (is_v)
+                    store_chunk_v<D>(vf, my_tok, part, c, whole);
+                else
+                    store_chunk_k<D>(kf, my_tok, part, c, whole);
+            } else {
+                low = half;
+            }
+            // the registers of K are free after half of the products, V's after all; the loads
+            // are used three quarters of a tile later
+            if (n == kProducts / 2 - 1) {
+                at_v = at;
+                at = spot<D>(a, entry, token(i + 3), kvh, part);
+                load_part<D>(a.c.kc, a.c.ks, at, kr);                                        // K of tile i + 3
+                entry = entry_of(i + 4);
+            }
+            if (n == kProducts - 1) load_part<D>(a.c.vc, a.c.vs, at_v, vr);                  // V of tile i + 2
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        x[0] = y[0];
+        x[1] = y[1];
     };
     for (int i = first; i < last; i += 2) {
-        step(i, image0, image1);
-        if (i + 1 < last) step(i + 1, image1, image0);
+        step(i, k1, k0, v0, v1);
+        if (i + 1 < last) step(i + 1, k0, k1, v1, v0);
     }
 
     l += shfl_xor_f32(l, 32);
