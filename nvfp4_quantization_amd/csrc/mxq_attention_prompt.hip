@@ -52,27 +52,28 @@ struct Part {
     uint32_t s;                       // D / 64 bytes
     bool ok;                          // the token's page may be read
 };
-// Where it lies.
+// Where the 16 tokens of a wave lie (they share a page: everything here is uniform).
 struct Spot {
     int64_t codes, scales;
     bool ok;
 };
-template <int D>
-__device__ __forceinline__ Spot spot(const AttnArgs& a, int32_t entry, int t, int kvh, int part) {
+__device__ __forceinline__ Spot spot(const AttnArgs& a, int32_t entry, int t, int kvh) {
     Spot r;
     r.ok = (uint32_t)entry < (uint32_t)a.c.num_pages;
     const int64_t page = r.ok ? entry : 0, row = t & ((1 << a.c.page_shift) - 1);
-    r.codes = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok + part * (D / 8);
-    r.scales = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok + part * (D / 64);
+    r.codes = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok;
+    r.scales = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok;
     return r;
 }
+// code_at, scale_at: this lane's bytes inside the 16 rows.
 template <int D>
-__device__ __forceinline__ void load_part(const uint8_t* codes, const uint8_t* scales, const Spot& at, Part<D>& r) {
-    r.w = *reinterpret_cast<const KWords<D>*>(codes + at.codes);
+__device__ __forceinline__ void load_part(const uint8_t* codes, const uint8_t* scales, const Spot& at, uint32_t code_at,
+                                          uint32_t scale_at, Part<D>& r) {
+    r.w = *reinterpret_cast<const KWords<D>*>(codes + at.codes + code_at);
     if constexpr (D == 128)
-        r.s = *reinterpret_cast<const uint16_t*>(scales + at.scales);
+        r.s = *reinterpret_cast<const uint16_t*>(scales + at.scales + scale_at);
     else
-        r.s = scales[at.scales];
+        r.s = (scales + at.scales)[scale_at];
     r.ok = at.ok;
 }
 
@@ -100,7 +101,7 @@ __device__ __forceinline__ f16x2 v_factors(const Part<D>& r, bool valid, VImage<
     const uint32_t hit = (((s & 0x7F7Fu) + 0x0101u) & 0x8080u) >> 7;     // bit 0: the low block, bit 8: the high one
     lds.nan[t * 4 + part] = (uint8_t)((hit | hit >> 7) & 3u);
     const int any = __any(hit != 0);
-    if ((t & 15) == 0 && part == 0) lds.any_nan[t >> 4] = any;
+    lds.any_nan[t >> 4] = any;                                           // (the whole wave writes one word)
     return e4m3_pair(s & ~(hit * 0xFFu), false);
 }
 // Four elements: the low or high half of code dword c of a part.
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     __shared__ KImage<D> k0, k1;
     __shared__ VImage<D> v0, v1;
 
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
     // work-groups of one (sequence, cached head) run together; later rows (more tiles) first
     const int split = (int)(blockIdx.x % (unsigned)a.splits);
@@ -194,9 +195,15 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 
     const int32_t* const table = a.table + (int64_t)b * a.ld_table;
     const int my_tok = tid >> 2, part = tid & 3;
-    // this thread's token of tile i (the last tile past the end) and its page
-    const auto token = [&](int i) { return span.tile(min(i, last - 1)) * 64 + my_tok; };
+    const uint32_t code_at = (uint32_t)((my_tok & 15) * a.c.cs_tok + part * (D / 8));
+    const uint32_t scale_at = (uint32_t)((my_tok & 15) * a.c.ss_tok + part * (D / 64));
+    // the first token of tile i (the last tile past the end) that this wave stages, and its
+    // page's table entry; both uniform over the wave
+    const int wave16 = wave * 16;
+    const auto token = [&](int i) { return span.tile(min(i, last - 1)) * 64 + wave16; };
     const auto entry_of = [&](int i) { return table[min(token(i), seq.len - 1) >> a.c.page_shift]; };
+    const auto spot_of = [&](int32_t entry, int i) { return spot(a, __builtin_amdgcn_readfirstlane(entry), token(i), kvh); };
+    const auto valid = [&](int i) { return token(i) + (my_tok & 15) < seq.len; };
     // the positions of this wave's rows, for its masks
     const int w_lo = max(seq.len - seq.nq + (int)((r0 + wave * 32) / a.group), -1);
     const int w_hi = max(seq.len - seq.nq + (int)((r0 + min(wave * 32 + 31, rows - 1)) / a.group), -1);
@@ -233,19 +240,19 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     Spot at;                                           // of the last loaded K
     int32_t entry = 0;
     if (first < last) {
-        at = spot<D>(a, entry_of(first), token(first), kvh, part);
-        load_part<D>(a.c.kc, a.c.ks, at, kr);
-        load_part<D>(a.c.vc, a.c.vs, at, vr);
+        at = spot_of(entry_of(first), first);
+        load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
+        load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
         const int32_t e1 = entry_of(first + 1), e2 = entry_of(first + 2);
         entry = entry_of(first + 3);
         store_k<D>(k0, kr, my_tok, part);
-        store_v<D>(v0, vr, my_tok, token(first) < seq.len, part);
-        at = spot<D>(a, e1, token(first + 1), kvh, part);
-        load_part<D>(a.c.kc, a.c.ks, at, kr);
-        load_part<D>(a.c.vc, a.c.vs, at, vr);
+        store_v<D>(v0, vr, my_tok, valid(first), part);
+        at = spot_of(e1, first + 1);
+        load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
+        load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
         store_k<D>(k1, kr, my_tok, part);
-        at = spot<D>(a, e2, token(first + 2), kvh, part);
-        load_part<D>(a.c.kc, a.c.ks, at, kr);
+        at = spot_of(e2, first + 2);
+        load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
         __syncthreads();
         x[0] = x[1] = zero16();
 #pragma unroll
@@ -315,7 +322,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             for (int e = n * kShare; e < (n + 1) * kShare; e += 2) {
                 const f32x2 w = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 4][e & 15], factor, shift)),
                                  __builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 4][(e & 15) + 1], factor, shift))};
-                l += w.x + w.y;
+                l += w.x + w.y;                        // before the rounding: lse is an output
                 const f16x2 r = __builtin_convertvector(w, f16x2);
                 p[e >> 3][e & 7] = r.x;
                 p[e >> 3][(e & 7) + 1] = r.y;
@@ -332,7 +339,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             const int c = (n >> 1) % (D / 32);
             const bool is_v = n >= kProducts / 2;
             if (n == 0) fk = k_factors<D>(kr);
-            if (n == kProducts / 2) fv = v_factors<D>(vr, token(i + 1) < seq.len, vf, my_tok, part);
+            if (n == kProducts / 2) fv = v_factors<D>(vr, valid(i + 1), vf, my_tok, part);
             const f16x4 half = is_v ? dequant_half<D>(vr.w, fv, c, n & 1) : dequant_half<D>(kr.w, fk, c, n & 1);
             if (n & 1) {
                 const f16x8 whole = __builtin_shufflevector(low, half, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -347,11 +354,11 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             // are used three quarters of a tile later
             if (n == kProducts / 2 - 1) {
                 at_v = at;
-                at = spot<D>(a, entry, token(i + 3), kvh, part);
-                load_part<D>(a.c.kc, a.c.ks, at, kr);                                        // K of tile i + 3
+                at = spot_of(entry, i + 3);
+                load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);                                      // K of tile i + 3
                 entry = entry_of(i + 4);
             }
-            if (n == kProducts - 1) load_part<D>(a.c.vc, a.c.vs, at_v, vr);                  // V of tile i + 2
+            if (n == kProducts - 1) load_part<D>(a.c.vc, a.c.vs, at_v, code_at, scale_at, vr);               // V of tile i + 2
             __builtin_amdgcn_sched_barrier(0);
         }
         x[0] = y[0];
