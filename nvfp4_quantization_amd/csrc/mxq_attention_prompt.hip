@@ -17,9 +17,9 @@
 //    A NaN V scale is staged as zero and noted; rows that see its token put NaN into that
 //    block at the end.
 //
-// Instructions are placed so that the matrix unit runs beside the rest: the weights of a tile
-// between the next tile's products with K, dequantization between the products with V,
-// operands read from LDS some products ahead.  The tile loop is unrolled over the two LDS
+// Instructions are placed so that the matrix unit runs beside the rest: the next tile's
+// dequantization between the products with K, weights between the products with V, operands
+// read from LDS some products ahead.  The tile loop is unrolled over the two LDS
 // images, as separate arrays: with one array and a dynamic buffer index the compiler orders
 // every read after the other image's writes.
 #include "mxq_attention_nvfp4.hpp"
@@ -32,8 +32,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kRowTile = 128;         // query rows of a work-group
 
 __device__ __forceinline__ f32x16 zero16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
 
@@ -141,8 +139,10 @@ __device__ __forceinline__ void store_v(VImage<D>& lds, const Part<D>& r, int t,
 
 }  // namespace
 
+// A wave holds 32 query rows (lane column = row), a work-group 128.
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
+    constexpr int kWaveRows = 32, kRowTile = 4 * kWaveRows;
     __shared__ KImage<D> k0, k1;
     __shared__ VImage<D> v0, v1;
 
@@ -165,10 +165,10 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 
     // Q as the second operand of S^T = K Q^T: lane (col, h) holds elements 16 c + 8 h .. + 7
     f16x8 q[D / 16];
-    const int my_row = wave * 32 + col;
-    const bool live = my_row < rows;
-    const int qi = live ? (int)((r0 + my_row) / a.group) : 0;
-    const int head = kvh * a.group + (live ? (int)(r0 + my_row - (int64_t)qi * a.group) : 0);
+    const int row = wave * kWaveRows + col;
+    const bool live = row < rows;
+    const int qi = live ? (int)((r0 + row) / a.group) : 0;
+    const int head = kvh * a.group + (live ? (int)(r0 + row - (int64_t)qi * a.group) : 0);
     const int pos = live ? max(seq.len - seq.nq + qi, -1) : -1;
     float factor;
     {
@@ -190,6 +190,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 
     f32x16 o[D / 32];
     float m = kFloor, l = 0.0f;
+    uint32_t nan_blocks = 0;                           // V blocks that this lane's tokens make NaN
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
 
@@ -205,11 +206,10 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     const auto spot_of = [&](int32_t entry, int i) { return spot(a, __builtin_amdgcn_readfirstlane(entry), token(i), kvh); };
     const auto valid = [&](int i) { return token(i) + (my_tok & 15) < seq.len; };
     // the positions of this wave's rows, for its masks
-    const int w_lo = max(seq.len - seq.nq + (int)((r0 + wave * 32) / a.group), -1);
-    const int w_hi = max(seq.len - seq.nq + (int)((r0 + min(wave * 32 + 31, rows - 1)) / a.group), -1);
+    const int w_lo = max(seq.len - seq.nq + (int)((r0 + wave * kWaveRows) / a.group), -1);
+    const int w_hi = max(seq.len - seq.nq + (int)((r0 + min(wave * kWaveRows + kWaveRows - 1, rows - 1)) / a.group), -1);
 
     constexpr int kProducts = D / 8, kAhead = 4;       // with K, and with V, per tile
-    uint32_t nan_blocks = 0;                           // V blocks that this lane's tokens make NaN
     const int k_lane = col * kPitchK<D> + 16 * h;
     int v_lane[D / 32];                                // (rows 8 apart keep the chunk order)
 #pragma unroll
@@ -232,110 +232,39 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
         return __builtin_bit_cast(f16x8, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
 
-    // Tile i's weights and products with V share a stretch of code with the scores of
-    // tile i + 1 and the dequantization of K of tile i + 2 and V of tile i + 1, so that the
-    // matrix unit always has work beside the vector unit's.  Past the last tile the last one
-    // is staged and scored again, unused.
     Part<D> kr, vr;
-    Spot at;                                           // of the last loaded K
     int32_t entry = 0;
     if (first < last) {
-        at = spot_of(entry_of(first), first);
+        Spot at = spot_of(entry_of(first), first);
         load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
         load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
-        const int32_t e1 = entry_of(first + 1), e2 = entry_of(first + 2);
-        entry = entry_of(first + 3);
+        const int32_t e1 = entry_of(first + 1);
+        entry = entry_of(first + 2);
         store_k<D>(k0, kr, my_tok, part);
         store_v<D>(v0, vr, my_tok, valid(first), part);
         at = spot_of(e1, first + 1);
         load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
         load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
-        store_k<D>(k1, kr, my_tok, part);
-        at = spot_of(e2, first + 2);
-        load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
-        __syncthreads();
-        x[0] = x[1] = zero16();
-#pragma unroll
-        for (int n = 0; n < kProducts; ++n)
-            x[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_operand(k0, n), q[n >> 1], x[n & 1], 0, 0, 0);
     }
 
-    // kn, vn: images of K of tile i + 1 and V of tile i; kf, vf: free ones
+    // One tile: kn, vn its images; kf, vf the next one's (the last tile's again at the end).
+    // The order of the products and what stands between them is fixed by hand: left alone,
+    // the compiler forms all weights first and reads each operand right before its product.
     const auto step = [&](int i, const KImage<D>& kn, KImage<D>& kf, const VImage<D>& vn, VImage<D>& vf) {
-        __syncthreads();
+        __syncthreads();                               // kn and vn are whole; kf and vf are free
         const int t0 = span.tile(i) * 64;
         const u32x4v noted = *reinterpret_cast<const u32x4v*>(vn.any_nan);
-        // masks only where an edge crosses the tile for this wave's rows
-        if (t0 + 63 > w_lo || (a.window && t0 <= (int64_t)w_hi - a.window)) {
-#pragma unroll
-            for (int T = 0; T < 2; ++T)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int tok = t0 + 32 * T + 8 * (e >> 2) + 4 * h + (e & 3);
-                    const bool see = tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
-                    x[T][e] = see ? x[T][e] : -__builtin_inff();
-                }
-        }
-        if (noted.x | noted.y | noted.z | noted.w) {   // (rare) note the NaN V blocks this lane sees
-#pragma unroll 1
-            for (int e = 0; e < 32; ++e) {
-                const int tok = t0 + 8 * (e >> 2) + 4 * h + (e & 3);
-                const bool see = tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(vn.nan + 4 * (tok - t0));
-                const uint32_t blocks = D == 128 ? (w & 3u) | (w >> 6 & 0xCu) | (w >> 12 & 0x30u) | (w >> 18 & 0xC0u)
-                                                 : (w & 1u) | (w >> 7 & 2u) | (w >> 14 & 4u) | (w >> 21 & 8u);
-                nan_blocks |= see ? blocks : 0u;
-            }
-        }
-        float top = x[0][0];
-#pragma unroll
-        for (int T = 0; T < 2; ++T)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, x[T][e]);
-        top *= factor;
-        if (__any(top > m + kSlack)) {
-            top = __builtin_fmaxf(top, shfl_xor_f32(top, 32));
-            const float raised = __builtin_fmaxf(m, top);
-            const float f = __builtin_amdgcn_exp2f(m - raised);
-            m = raised;
-            l *= f;
-#pragma unroll
-            for (int dt = 0; dt < D / 32; ++dt) o[dt] *= f;
-        }
-
-        // Products with K of tile i + 1, a share of tile i's weights after each; then those
-        // with V of tile i, a share of the dequantization after each.  Operands are read kAhead
-        // products before their use.  The order is fixed by hand: left alone, the compiler
-        // forms all weights first and reads each operand right before its product.
-        const float shift = kBias - m;
-        f32x16 y[2] = {zero16(), zero16()};
-        f16x8 p[4], ahead[kAhead];
+        f16x8 ahead[kAhead];
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) ahead[n] = k_operand(kn, n);
+        f16x4 low = {};
+        f16x2 fk, fv;
+        x[0] = x[1] = zero16();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < kProducts; ++n) {
-            y[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[n % kAhead], q[n >> 1], y[n & 1], 0, 0, 0);
+            x[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[n % kAhead], q[n >> 1], x[n & 1], 0, 0, 0);
             ahead[n % kAhead] = n + kAhead < kProducts ? k_operand(kn, n + kAhead) : v_operand(vn, n + kAhead - kProducts);
-            constexpr int kShare = 32 / kProducts;
-#pragma unroll
-            for (int e = n * kShare; e < (n + 1) * kShare; e += 2) {
-                const f32x2 w = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 4][e & 15], factor, shift)),
-                                 __builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 4][(e & 15) + 1], factor, shift))};
-                l += w.x + w.y;                        // before the rounding: lse is an output
-                const f16x2 r = __builtin_convertvector(w, f16x2);
-                p[e >> 3][e & 7] = r.x;
-                p[e >> 3][(e & 7) + 1] = r.y;
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        f16x4 low = {};
-        f16x2 fk, fv;
-        Spot at_v;
-#pragma unroll
-        for (int n = 0; n < kProducts; ++n) {
-            o[n % (D / 32)] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[n % kAhead], p[n / (D / 32)], o[n % (D / 32)], 0, 0, 0);
-            if (n + kAhead < kProducts) ahead[n % kAhead] = v_operand(vn, n + kAhead);
             const int c = (n >> 1) % (D / 32);
             const bool is_v = n >= kProducts / 2;
             if (n == 0) fk = k_factors<D>(kr);
@@ -350,23 +279,79 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             } else {
                 low = half;
             }
-            // the registers of K are free after half of the products, V's after all; the loads
-            // are used three quarters of a tile later
-            if (n == kProducts / 2 - 1) {
-                at_v = at;
-                at = spot_of(entry, i + 3);
-                load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);                                      // K of tile i + 3
-                entry = entry_of(i + 4);
-            }
-            if (n == kProducts - 1) load_part<D>(a.c.vc, a.c.vs, at_v, code_at, scale_at, vr);               // V of tile i + 2
             __builtin_amdgcn_sched_barrier(0);
         }
-        x[0] = y[0];
-        x[1] = y[1];
+        {
+            const Spot at = spot_of(entry, i + 2);
+            load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
+            load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
+            entry = entry_of(i + 3);
+        }
+        // masks only where an edge crosses the tile for this wave's rows
+        if (t0 + 63 > w_lo || (a.window && t0 <= (int64_t)w_hi - a.window)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int tok = t0 + 8 * (e >> 2) + 4 * h + (e & 3);
+                const bool see = tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
+                x[e >> 4][e & 15] = see ? x[e >> 4][e & 15] : -__builtin_inff();
+            }
+        }
+        if (noted.x | noted.y | noted.z | noted.w) {   // (rare) note the NaN V blocks this lane sees
+#pragma unroll 1
+            for (int e = 0; e < 32; ++e) {
+                const int tok = t0 + 8 * (e >> 2) + 4 * h + (e & 3);
+                const bool see = tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(vn.nan + 4 * (tok - t0));
+                const uint32_t blocks = D == 128 ? (w & 3u) | (w >> 6 & 0xCu) | (w >> 12 & 0x30u) | (w >> 18 & 0xC0u)
+                                                 : (w & 1u) | (w >> 7 & 2u) | (w >> 14 & 4u) | (w >> 21 & 8u);
+                nan_blocks |= see ? blocks : 0u;
+            }
+        }
+        float top = x[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e) top = __builtin_fmaxf(top, x[e >> 4][e & 15]);
+        top *= factor;
+        if (__any(top > m + kSlack)) {
+            top = __builtin_fmaxf(top, shfl_xor_f32(top, 32));
+            const float raised = __builtin_fmaxf(m, top);
+            const float f = __builtin_amdgcn_exp2f(m - raised);
+            m = raised;
+            l *= f;
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt) o[dt] *= f;
+        }
+
+        // Weights of 16 tokens at a time; their products with V between the weights of the
+        // next 16.
+        const float shift = kBias - m;
+        f16x8 p[2];
+        const auto weights = [&](int f, int e) {                           // two of them
+            const int k = 8 * f + e;
+            const f32x2 w = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[k >> 4][k & 15], factor, shift)),
+                             __builtin_amdgcn_exp2f(__builtin_fmaf(x[k >> 4][(k & 15) + 1], factor, shift))};
+            l += w.x + w.y;                            // before the rounding: lse is an output
+            const f16x2 b = __builtin_convertvector(w, f16x2);
+            p[f & 1][e] = b.x;
+            p[f & 1][e + 1] = b.y;
+        };
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) weights(0, e);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+            const int f = n / (D / 32), dt = n % (D / 32);
+            o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[n % kAhead], p[f & 1], o[dt], 0, 0, 0);
+            if (n + kAhead < kProducts) ahead[n % kAhead] = v_operand(vn, n + kAhead);
+            if (f < 3) {
+#pragma unroll
+                for (int e = 0; e < 8 / (D / 32); e += 2) weights(f + 1, dt * (8 / (D / 32)) + e);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     for (int i = first; i < last; i += 2) {
-        step(i, k1, k0, v0, v1);
-        if (i + 1 < last) step(i + 1, k0, k1, v1, v0);
+        step(i, k0, k1, v0, v1);
+        if (i + 1 < last) step(i + 1, k1, k0, v1, v0);
     }
 
     l += shfl_xor_f32(l, 32);
@@ -384,7 +369,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int e = 0; e < 16; e += 4)
-            store_rows<D>(a, seq, unit, kvh, split, used, kRowTile, r0 + my_row, 32 * dt + 2 * e + 4 * h,
+            store_rows<D>(a, seq, unit, kvh, split, used, kRowTile, r0 + row, 32 * dt + 2 * e + 4 * h,
                           f32x4{o[dt][e], o[dt][e + 1], o[dt][e + 2], o[dt][e + 3]}, m, l, vg);
 }
 
