@@ -16,359 +16,576 @@
 //    FP16 (nearest-even) for the product with V, their FP32 values are summed.  With
 //    kBias = 9 a weight keeps all 11 bits down to 2^-23 of the row's largest and adds in
 //    down to 2^-33 of it.
-//  * S^T leaves the matrix unit with a query row per lane column and four tokens per lane
-//    register group, which is P^T's operand layout for the second product when score
-//    tile t row 4g + i is token 16 g + 4 t + i: K's rows are loaded in that order, and
-//    the weights never leave their registers.
+//  * S^T leaves the matrix unit with a query row per lane column and, in lane group g of 16,
+//    tokens 16 t + 4 g + e (score tile t, register e): P^T's operand layout for the second
+//    product when its k index 8 g + j of half u stands for token 16 (2 u + j / 4) + 4 g +
+//    j % 4.  The weights never leave their registers.
 //  * V is staged per wave in LDS as it lies in the cache (two codes a byte, a token per
 //    row) and read back transposed (ds_read_b64_tr_b4): a lane gets the 16 tokens of one
 //    output element.  Its scales are staged as FP16, a token pair per dword.
 //
-// A work-group of four waves takes one chunk of one (sequence, cached head, rows of
-// queries) and interleaves its 64-token tiles over the waves; the waves join through LDS.
+// Work split: with many units (sequence, cached head), a work-group each.  Otherwise the
+// 64-token tiles of all units lie on one line, and every work-group takes an equal stretch
+// of it, however ragged the lengths are: a unit inside one stretch is finished there, one
+// cut by a stretch's end leaves partial outputs (maximum, sum, unnormalized FP32 rows) in
+// the workspace for the join.  A work-group's four waves take every fourth tile of a unit
+// and join through LDS.
 #include "mxq_attention_nvfp4.hpp"
 
 namespace mxq {
 
 namespace {
 
-// ---------------------------------------------------------------- a step's loads
 struct Lane {
-    int lane, g, q, low;              // g = lane / 16, q = (lane / 4) % 4, low = lane % 4
+    int lane, g, col;                 // g = lane / 16, col = lane % 16
 };
 
-// The page of the 16 tokens 16 q .. of a tile that this lane loads, raw from the table
-// (0 past the sequence: nothing of such tokens is used).
-__device__ __forceinline__ int32_t page_entry(const AttnArgs& a, const int32_t* table, int len, int tile, const Lane& L) {
-    const int tg = tile * 64 + 16 * L.q;
-    return tg < len ? table[tg >> a.c.page_shift] : 0;
+// ---------------------------------------------------------------- a tile's loads
+// The table entries of a tile's four groups of 16 tokens, group lane % 4 in each lane
+// (past the sequence the last token's page: nothing of such tokens is used).
+__device__ __forceinline__ int32_t page_entries(const AttnArgs& a, const int32_t* table, int len, int tile, const Lane& L) {
+    return table[min(tile * 64 + 16 * (L.lane & 3), len - 1) >> a.c.page_shift];
 }
 
-// Where those tokens' codes and scales lie (page 0 for a page that may not be read).
+// Where the four groups lie (uniform; page 0 for a page that may not be read).
 struct Place {
-    int64_t codes, scales;
-    bool ok;
+    int64_t codes[4], scales[4];
+    uint32_t bad;                     // bit t: group t's page may not be read
 };
-__device__ __forceinline__ Place place(const AttnArgs& a, int32_t entry, int tile, int kvh, const Lane& L) {
+__device__ __forceinline__ Place place(const AttnArgs& a, int32_t entries, int tile) {
     Place p;
-    p.ok = (uint32_t)entry < (uint32_t)a.c.num_pages;
-    const int64_t page = p.ok ? entry : 0;
-    const int64_t row = (tile * 64 + 16 * L.q) & ((1 << a.c.page_shift) - 1);
-    p.codes = page * a.c.cs_page + kvh * a.c.cs_head + row * a.c.cs_tok;
-    p.scales = page * a.c.ss_page + kvh * a.c.ss_head + row * a.c.ss_tok;
+    p.bad = 0;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int32_t e = __builtin_amdgcn_readlane(entries, t);
+        const bool ok = (uint32_t)e < (uint32_t)a.c.num_pages;
+        p.bad |= ok ? 0u : 1u << t;
+        const int64_t page = ok ? e : 0;
+        const int64_t row = (tile * 64 + 16 * t) & ((1 << a.c.page_shift) - 1);
+        p.codes[t] = page * a.c.cs_page + row * a.c.cs_tok;
+        p.scales[t] = page * a.c.ss_page + row * a.c.ss_tok;
+    }
     return p;
 }
 
-// (Named members: an array indexed in the long score loop would end up in scratch.)
+// The cached head's arrays.
+struct Base {
+    const uint8_t *kc, *ks, *vc, *vs;
+};
+
+// This lane's bytes inside a group's 16 rows.
+struct Offsets {
+    uint32_t k, ks, v, vs;
+};
+
+// K: codes D / 4 g .. of token 16 t + col, and their scales.  (Named members: an array
+// indexed in the score loop would end up in scratch.)
 template <int D>
 struct KRegs {
-    KWords<D> w0, w1, w2, w3;         // codes of this lane's K rows (score tile t): D / 4 elements each
-    uint32_t s0, s1, s2, s3;          // their scales (D / 64 bytes)
+    KWords<D> w0, w1, w2, w3;
+    uint32_t s0, s1, s2, s3;
 };
 template <int D>
-__device__ __forceinline__ uint32_t k_scales(const uint8_t* p) {
-    if constexpr (D == 128) return *reinterpret_cast<const uint16_t*>(p);
-    return *p;
+__device__ __forceinline__ uint32_t k_scales(const uint8_t* p, uint32_t off) {
+    if constexpr (D == 128) return *reinterpret_cast<const uint16_t*>(p + off);
+    return p[off];
 }
 template <int D>
-__device__ __forceinline__ void load_k(const AttnArgs& a, const Place& p, const Lane& L, KRegs<D>& r) {
-    const uint8_t* kc = a.c.kc + p.codes + L.low * a.c.cs_tok + L.g * (D / 8);
-    const uint8_t* ks = a.c.ks + p.scales + L.low * a.c.ss_tok + L.g * (D / 64);
-    r.w0 = *reinterpret_cast<const KWords<D>*>(kc);
-    r.w1 = *reinterpret_cast<const KWords<D>*>(kc + 4 * a.c.cs_tok);
-    r.w2 = *reinterpret_cast<const KWords<D>*>(kc + 8 * a.c.cs_tok);
-    r.w3 = *reinterpret_cast<const KWords<D>*>(kc + 12 * a.c.cs_tok);
-    r.s0 = k_scales<D>(ks);
-    r.s1 = k_scales<D>(ks + 4 * a.c.ss_tok);
-    r.s2 = k_scales<D>(ks + 8 * a.c.ss_tok);
-    r.s3 = k_scales<D>(ks + 12 * a.c.ss_tok);
+__device__ __forceinline__ void load_k(const Base& a, const Place& p, const Offsets& o, KRegs<D>& r) {
+    r.w0 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[0] + o.k);
+    r.w1 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[1] + o.k);
+    r.w2 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[2] + o.k);
+    r.w3 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[3] + o.k);
+    // a page that may not be read: NaN scales, so that rows that see its tokens are NaN
+    constexpr uint32_t kNan = D == 128 ? 0x7F7Fu : 0x7Fu;
+    r.s0 = p.bad & 1 ? kNan : k_scales<D>(a.ks + p.scales[0], o.ks);
+    r.s1 = p.bad & 2 ? kNan : k_scales<D>(a.ks + p.scales[1], o.ks);
+    r.s2 = p.bad & 4 ? kNan : k_scales<D>(a.ks + p.scales[2], o.ks);
+    r.s3 = p.bad & 8 ? kNan : k_scales<D>(a.ks + p.scales[3], o.ks);
 }
 
+// V: 16 codes-bytes of a token (D = 128: token 16 j + lane / 4 in load j; D = 64: token
+// 32 j + lane / 2) and the scales of token `lane`.
 template <int D>
 struct VRegs {
-    u32x4v w[D / 32];                 // codes on their way to LDS
-    uint32_t s[D / 64];               // scales of this lane's token
-    bool ok;
+    u32x4v w[D / 32];
+    uint32_t s[D / 64];
+    bool ok;                          // the token's page may be read
 };
 template <int D>
-__device__ __forceinline__ void load_v(const AttnArgs& a, const Place& p, const Lane& L, VRegs<D>& r) {
-    const uint8_t* vc = a.c.vc + p.codes;
-    const int sw = L.low ^ L.g;                             // 16-byte chunk order of the staging
+__device__ __forceinline__ void load_v(const Base& a, const Place& p, const Offsets& o, const Lane& L, VRegs<D>& r) {
+    if constexpr (D == 128) {
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-        const int tok = D == 128 ? 4 * j + L.g : 8 * j + 2 * L.g + (sw >> 1);
-        const int chunk = D == 128 ? sw : sw & 1;
-        r.w[j] = *reinterpret_cast<const u32x4v*>(vc + tok * a.c.cs_tok + 16 * chunk);
+        for (int j = 0; j < 4; ++j) r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + p.codes[j] + o.v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + (L.lane < 32 ? p.codes[2 * j] : p.codes[2 * j + 1]) + o.v);
     }
-    const uint8_t* vs = a.c.vs + p.scales + (4 * L.g + L.low) * a.c.ss_tok;
+    const int64_t lo = L.g & 1 ? p.scales[1] : p.scales[0], hi = L.g & 1 ? p.scales[3] : p.scales[2];
+    const uint8_t* vs = a.vs + (L.g & 2 ? hi : lo) + o.vs;
     if constexpr (D == 128) {
         const u32x2v w = *reinterpret_cast<const u32x2v*>(vs);
         r.s[0] = w.x, r.s[1] = w.y;
     } else {
         r.s[0] = *reinterpret_cast<const uint32_t*>(vs);
     }
-    r.ok = p.ok;
+    r.ok = !((p.bad >> L.g) & 1);
 }
 
 // ---------------------------------------------------------------- LDS of one wave
-// V codes: load j's 64 x 16 bytes at j * kVJ (64 bytes of padding keep the 16 tokens that
-// a transposing read touches in different banks); V scales as FP16 [D/16][64 tokens].
-constexpr int kVJ = 1024 + 64;
+// V codes: load j's 64 x 16 bytes at j * kVJ (16 bytes of padding keep the tokens that a
+// transposing read touches in different banks); V scales as FP16 [D/16][64 tokens], lane
+// group g's 16 tokens together; a byte per token for NaN V blocks.
+constexpr int kVJ = 1024 + 16;
 template <int D>
 struct WaveLds {
     static constexpr int kScales = (D / 32) * kVJ;
-    static constexpr int kBytes = kScales + (D / 16) * 128;
+    static constexpr int kNan = kScales + (D / 16) * 128;
+    static constexpr int kBytes = kNan + 64;
 };
-// The byte of V's LDS image where token k of lane group G starts its element tile dt.
+// The byte of V's LDS image where element tile dt of lane group g's token k starts.
 template <int D>
-__device__ __forceinline__ int v_addr(int G, int k, int dt) {
-    if constexpr (D == 128) return (k >> 2) * kVJ + 256 * (k & 3) + 64 * G + 16 * ((dt >> 1) ^ (k & 3)) + 8 * (dt & 1);
-    const int g = (k >> 1) & 3;
-    return (k >> 3) * kVJ + 256 * g + 64 * G + 16 * ((2 * (k & 1) + (dt >> 1)) ^ g) + 8 * (dt & 1);
+__device__ __forceinline__ int v_addr(int g, int k, int dt) {
+    const int token = 16 * (k >> 2) + 4 * g + (k & 3);
+    if constexpr (D == 128) return (token >> 4) * kVJ + (token & 15) * 64 + 8 * dt;
+    return (token >> 5) * kVJ + (token & 31) * 32 + 8 * dt;
 }
 
 // FP16 scales of this lane's token into LDS (zero for a token that is not valid).
 template <int D>
 __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[D / 64], bool valid, const Lane& L) {
-    f16* const p = reinterpret_cast<f16*>(lds + WaveLds<D>::kScales) + 16 * L.q + 4 * L.g + L.low;
+    f16* const p = reinterpret_cast<f16*>(lds + WaveLds<D>::kScales) + 16 * ((L.lane >> 2) & 3) + 4 * L.g + (L.lane & 3);
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
-        const f16x2 a = e4m3_pair(vs[w], false), b = e4m3_pair(vs[w], true);
-        const f16 z = (f16)0.0f;
-        p[(4 * w + 0) * 64] = valid ? a.x : z;
-        p[(4 * w + 1) * 64] = valid ? a.y : z;
-        p[(4 * w + 2) * 64] = valid ? b.x : z;
-        p[(4 * w + 3) * 64] = valid ? b.y : z;
+        const uint32_t s = valid ? vs[w] : 0u;
+        const f16x2 a = e4m3_pair(s, false), b = e4m3_pair(s, true);
+        p[(4 * w + 0) * 64] = a.x;
+        p[(4 * w + 1) * 64] = a.y;
+        p[(4 * w + 2) * 64] = b.x;
+        p[(4 * w + 3) * 64] = b.y;
     }
 }
 
-// This lane's staged scales with NaN ones replaced by zero.
-template <int D>
-__device__ __forceinline__ void clean_scales(uint8_t* lds, const Lane& L) {
-    f16* const p = reinterpret_cast<f16*>(lds + WaveLds<D>::kScales) + 16 * L.q + 4 * L.g + L.low;
-#pragma unroll
-    for (int b = 0; b < D / 16; ++b) {
-        const f16 v = p[b * 64];
-        p[b * 64] = v != v ? (f16)0.0f : v;
-    }
+// ---------------------------------------------------------------- the line of tiles
+constexpr int kLineSeqs = 1024;       // sequences of a call whose units share the line
+// Tiles of a unit of a sequence (one at least where there are queries, which then get their
+// zeros).
+__device__ __forceinline__ int unit_tiles(const AttnArgs& a, const Seq& s) {
+    const int nq = min(s.nq, a.max_q_len);
+    return nq > 0 ? max(tile_span(a, s, 0, nq - 1).n, 1) : 0;
+}
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);       // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);       // lane 15 of the row before, rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);       // lane 31, rows 2 and 3
+    return v;
 }
 
 }  // namespace
 
 template <int D, int NT>
-__global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void k_attention_rows(const AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
     constexpr int kWave = WaveLds<D>::kBytes;
     constexpr int kJoin = (D / 16) * 64 * 16;               // a wave's outputs of one column tile
     constexpr int kLds = 4 * kWave > 4 * kJoin ? 4 * kWave : 4 * kJoin;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     __shared__ float2 join[4][NT * 16];
+    // of the sequences on the line: length, first query row, queries, tiles of a unit
+    __shared__ int4 seqs[kLineSeqs];
+    __shared__ uint32_t wave_tiles[4], wave_most[4];
+    __shared__ int found;
+    __shared__ int64_t found_before;
 
-    const int wave = (int)threadIdx.x >> 6;
+    const int tid = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Lane L;
-    L.lane = (int)threadIdx.x & 63;
-    L.g = L.lane >> 4, L.q = (L.lane >> 2) & 3, L.low = L.lane & 3;
-    const int col = L.lane & 15;
+    L.lane = tid & 63;
+    L.g = L.lane >> 4, L.col = L.lane & 15;
 
-    const int split = (int)(blockIdx.x % (unsigned)a.splits);
-    const int unit = (int)(blockIdx.x / (unsigned)a.splits);
-    const int kvh = unit % a.c.kv_heads, bt = unit / a.c.kv_heads;
-    const int b = bt / a.row_tiles, r0 = (bt - b * a.row_tiles) * (NT * 16);
-    const Seq seq = sequence(a, b);
-    const int rows = min(min(seq.nq, a.max_q_len) * a.group - r0, NT * 16);      // of this unit
-    if (rows <= 0) return;
-    const Span span = tile_span(a, seq, r0 / a.group, (r0 + rows - 1) / a.group);
-    const int used = splits_used(a, span.n);
-    if (split >= used) return;
-    const int first = split * a.chunk, last = split == used - 1 ? span.n : first + a.chunk;
-
-    // Q as the second operand of S^T = K Q^T: lane (col, g) holds elements D/4 g .. of row
-    // col, scaled to FP16 by the row's power of two
-    f16x8 q[NT][D / 32];
-    float factor[NT];
-    int pos[NT];
+    // ---- this work-group's stretch of the line [at, end), and the sequence it starts in
+    int64_t at = 0, end, share = 0, before = 0;             // before: line tiles of the sequences before b
+    int b;
+    if (!a.desc) {                                          // a unit of its own
+        b = (int)(blockIdx.x / (unsigned)a.c.kv_heads);
+        const Seq s = sequence(a, b);
+        const int n = unit_tiles(a, s);
+        if (n == 0) return;
+        seqs[0] = make_int4(s.len, s.start, s.nq, n);       // (every thread the same)
+        at = (int64_t)(blockIdx.x - (unsigned)b * (unsigned)a.c.kv_heads) * n;
+        end = at + n;
+    } else {
+        // four consecutive sequences a thread
+        uint32_t n[4], sum = 0, most = 0;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int r = n * 16 + col;
-        const bool live = r < rows;
-        const int qi = live ? (r0 + r) / a.group : 0, head = kvh * a.group + (live ? r0 + r - qi * a.group : 0);
-        pos[n] = live ? max(seq.len - seq.nq + qi, -1) : -1;
-        const uint16_t* src = a.q + (int64_t)(seq.start + qi) * a.ld_q + (int64_t)head * D + L.g * (D / 4);
-        u32x4v w[D / 32];
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            w[i] = live ? reinterpret_cast<const u32x4v*>(src)[i] : u32x4v{0, 0, 0, 0};
-            top = absmax_pk(absmax_pk(absmax_pk(absmax_pk(top, w[i].x), w[i].y), w[i].z), w[i].w);
-        }
-        top = fold_pk(top);
-        top = max(top, shfl_xor_u32(top, 16));
-        top = max(top, shfl_xor_u32(top, 32));
-        const float up = q_power(top, factor[n]);
-        factor[n] *= a.scale_log2 * a.c.kg[kvh];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) q[n][i] = q_operand(w[i], up);
-    }
-
-    f32x4 o[NT][D / 16];
-    float m[NT], l[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n] = kFloor;
-        l[n] = 0.0f;
-#pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) o[n][dt] = f32x4{0, 0, 0, 0};
-    }
-    uint8_t* const mine = lds + wave * kWave;
-    const int32_t* const table = a.table + (int64_t)b * a.ld_table;
-
-    // Loads run ahead of the step that uses them: the page table entry by two steps, V by
-    // one (its registers are free once it is in LDS), K by one (after its use).
-    KRegs<D> k;
-    VRegs<D> v;
-    int i = first + wave;
-    int32_t entry = 0;
-    if (i < last) {
-        const Place at = place(a, page_entry(a, table, seq.len, span.tile(i), L), span.tile(i), kvh, L);
-        load_v<D>(a, at, L, v);
-        load_k<D>(a, at, L, k);
-        if (i + 4 < last) entry = page_entry(a, table, seq.len, span.tile(i + 4), L);
-    }
-    while (i < last) {
-        const int tile = span.tile(i), t0 = tile * 64;
-        // V and its scales to LDS; tokens past the sequence or of unreadable pages get
-        // zero scales, so whatever lies there stays out
-        const bool v_valid = v.ok && t0 + 16 * L.q + 4 * L.g + L.low < seq.len;
-        const uint64_t bad = __ballot(!v.ok);
-        bool nan_here = false;
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) nan_here |= has_nan_scale(v.s[w]);
-        const bool nan_v = __any(nan_here && v_valid);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) *reinterpret_cast<u32x4v*>(mine + j * kVJ + L.lane * 16) = v.w[j];
-        stage_scales<D>(mine, v.s, v_valid, L);
-        const int next = i + 4;
-        Place at;
-        if (next < last) {
-            at = place(a, entry, span.tile(next), kvh, L);
-            load_v<D>(a, at, L, v);
-            if (next + 4 < last) entry = page_entry(a, table, seq.len, span.tile(next + 4), L);
-        }
-
-        // scores of 64 tokens: tile t row 4 g' + i' is token 16 g' + 4 t + i'
-        f32x4 x[NT][4];
-        const auto score = [&](int t, KWords<D> w, uint32_t scales) {
-            f16x8 kk[D / 32];
-            dequant_row<D>(w, scales, kk);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                x[n][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-                    x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk[c], q[n][c], x[n][t], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+            n[j] = 0;
+            if (4 * tid + j < a.batch) {
+                const Seq s = sequence(a, 4 * tid + j);
+                n[j] = (uint32_t)unit_tiles(a, s);
+                seqs[4 * tid + j] = make_int4(s.len, s.start, s.nq, (int)n[j]);
             }
-        };
-        score(0, k.w0, k.s0);
-        score(1, k.w1, k.s1);
-        score(2, k.w2, k.s2);
-        score(3, k.w3, k.s3);
-        if (next < last) load_k<D>(a, at, L, k);
+            sum += n[j];
+            most = max(most, n[j]);
+        }
+        const uint32_t upto = wave_scan(sum);
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) most = max(most, shfl_xor_u32(most, o));
+        if (L.lane == 63) wave_tiles[wave] = upto, wave_most[wave] = most;
+        __syncthreads();
+        int64_t mine = 0, line = 0;                         // tiles before this thread's sequences; all
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) mine += wave_tiles[w];
+            line += wave_tiles[w];
+            most = max(most, wave_most[w]);
+        }
+        line *= a.c.kv_heads;
+        // equal stretches; of whole rounds of four waves, unless all units are shorter
+        share = (line + gridDim.x - 1) / gridDim.x;
+        share = share > 4 ? (share + 3) / 4 * 4 : max(share, (int64_t)min(most, 4u));
+        at = (int64_t)blockIdx.x * share;
+        end = min(at + share, line);
+        if (at >= end) return;
+        mine = (mine + (upto - sum)) * a.c.kv_heads;
+        if (at >= mine && at < mine + (int64_t)sum * a.c.kv_heads) {
+            int j = 0;
+            while (at >= mine + (int64_t)n[j] * a.c.kv_heads) mine += (int64_t)n[j++] * a.c.kv_heads;
+            found = 4 * tid + j;
+            found_before = mine;
+        }
+        __syncthreads();
+        b = __builtin_amdgcn_readfirstlane(found);
+        before = found_before;
+    }
 
-        f16x8 p[NT][2];
+    Offsets off;
+    off.k = (uint32_t)(L.col * a.c.cs_tok + L.g * (D / 8));
+    off.ks = (uint32_t)(L.col * a.c.ss_tok + L.g * (D / 64));
+    off.v = D == 128 ? (uint32_t)((L.lane >> 2) * a.c.cs_tok + 16 * (L.lane & 3))
+                     : (uint32_t)(((L.lane >> 1) & 15) * a.c.cs_tok + 16 * (L.lane & 1));
+    off.vs = (uint32_t)(L.col * a.c.ss_tok);
+    uint8_t* const mine = lds + wave * kWave;
+
+    // ---- segment by segment: the part of one unit inside the stretch
+    while (at < end) {
+        const int4 info = seqs[a.desc ? b : 0];
+        const int n_unit = info.w;
+        if (n_unit == 0) {                                  // (a sequence without queries)
+            ++b;
+            continue;
+        }
+        const int kvh = __builtin_amdgcn_readfirstlane((int)((at - before) / n_unit));
+        const int first = __builtin_amdgcn_readfirstlane((int)((at - before) - (int64_t)kvh * n_unit));
+        const int last = __builtin_amdgcn_readfirstlane((int)min((int64_t)n_unit, first + (end - at)));
+        Seq seq;
+        seq.len = __builtin_amdgcn_readfirstlane(info.x);
+        seq.start = __builtin_amdgcn_readfirstlane(info.y);
+        seq.nq = __builtin_amdgcn_readfirstlane(info.z);
+        const int rows = min(seq.nq, a.max_q_len) * a.group;
+        const Span span = tile_span(a, seq, 0, (rows - 1) / a.group);
+        const int stop = min(last, span.n);                 // (no tile where no query sees a token)
+        const Base head{a.c.kc + kvh * a.c.cs_head, a.c.ks + kvh * a.c.ss_head, a.c.vc + kvh * a.c.cs_head,
+                        a.c.vs + kvh * a.c.ss_head};
+
+        // Loads run ahead of the tile that uses them: the page table entries by two tiles, V
+        // by one (its registers are free once it is in LDS), K by one (after its use).
+        const int32_t* const table = a.table + (int64_t)b * a.ld_table;
+        KRegs<D> k;
+        VRegs<D> v;
+        int i = first + wave;
+        int32_t entries = 0, entries0 = 0;
+        if (i < stop) {
+            entries0 = page_entries(a, table, seq.len, span.tile(i), L);
+            entries = page_entries(a, table, seq.len, span.tile(min(i + 4, stop - 1)), L);
+        }
+        const float kg = a.c.kg[kvh], vg = a.c.vg[kvh];
+
+        if (i < stop) {
+            const Place where = place(a, entries0, span.tile(i));
+            load_v<D>(head, where, off, L, v);
+            load_k<D>(head, where, off, k);
+        }
+
+        // Q as the second operand of S^T = K Q^T: lane (col, g) holds elements D/4 g .. of
+        // row col, scaled to FP16 by the row's power of two
+        f16x8 q[NT][D / 32];
+        float factor[NT];
+        int pos[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            // masks only where an edge crosses the tile (uniform over the wave)
-            const bool edge = t0 + 63 > span.p_lo || (a.window && t0 <= (int64_t)span.p_hi - a.window) || bad != 0;
-            if (edge) {
+            const int r = n * 16 + L.col;
+            const bool live = r < rows;
+            const int qi = live ? r / a.group : 0, h = kvh * a.group + (live ? r - qi * a.group : 0);
+            pos[n] = live ? max(seq.len - seq.nq + qi, -1) : -1;
+            const uint16_t* src = a.q + (int64_t)(seq.start + qi) * a.ld_q + (int64_t)h * D + L.g * (D / 4);
+            u32x4v w[D / 32];
+            uint32_t top = 0;
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int tok = t0 + 16 * L.g + 4 * t + e;
-                        const bool see = tok <= pos[n] && (!a.window || tok > pos[n] - a.window || tok < a.sinks);
-                        if ((bad >> (4 * L.g)) & 1) x[n][t][e] = __builtin_nanf("");
-                        x[n][t][e] = see ? x[n][t][e] : -__builtin_inff();
-                    }
+            for (int i = 0; i < D / 32; ++i) {
+                w[i] = live ? reinterpret_cast<const u32x4v*>(src)[i] : u32x4v{0, 0, 0, 0};
+                top = absmax_pk(absmax_pk(absmax_pk(absmax_pk(top, w[i].x), w[i].y), w[i].z), w[i].w);
             }
-            softmax_step<D>(x[n], factor[n], m[n], l[n], o[n], p[n]);
+            top = fold_pk(top);
+            top = max(top, shfl_xor_u32(top, 16));
+            top = max(top, shfl_xor_u32(top, 32));
+            const float up = q_power(top, factor[n]);
+            factor[n] *= a.scale_log2 * kg;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) q[n][i] = q_operand(w[i], up);
         }
 
-        if (nan_v) {
+        f32x4 o[NT][D / 16];
+        float m[NT], l[NT];
+        uint32_t nan_blocks[NT];                            // V blocks that this lane's tokens make NaN
 #pragma unroll
-            for (int dt = 0; dt < D / 16; ++dt) {
-                const f16x8* sc = reinterpret_cast<const f16x8*>(mine + WaveLds<D>::kScales + dt * 128 + L.g * 32);
-                f16x8 hit[2];
+        for (int n = 0; n < NT; ++n) {
+            m[n] = kFloor;
+            l[n] = 0.0f;
+            nan_blocks[n] = 0;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const f16x8 s = sc[u];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) hit[u][j] = s[j] != s[j] ? (f16)1.0f : (f16)0.0f;
-                }
-                spread_nan<NT, D / 16>(hit, dt, p, o);
-            }
-            clean_scales<D>(mine, L);
+            for (int dt = 0; dt < D / 16; ++dt) o[n][dt] = f32x4{0, 0, 0, 0};
         }
-        // O^T += V^T P^T
+
+        while (i < stop) {
+            const int t0 = span.tile(i) * 64;
+            // V and its scales to LDS; tokens past the sequence or of unreadable pages get
+            // zero scales, so whatever lies there stays out
+            const bool valid = v.ok && t0 + L.lane < seq.len;
+            bool nan_here = false;
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) {
-            const i32x2 c = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                (__attribute__((address_space(3))) i32x2*)(mine + v_addr<D>(L.g, col, dt)));
-            const f16x8* sc = reinterpret_cast<const f16x8*>(mine + WaveLds<D>::kScales + dt * 128 + L.g * 32);
+            for (int w = 0; w < D / 64; ++w) nan_here |= has_nan_scale(v.s[w]);
+            if (__any(nan_here && valid)) {                 // (rare) note NaN V blocks, stage them as zero
+                uint32_t blocks = 0;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const f16x8 vv = e2m1_8(u ? c.y : c.x) * sc[u];
+                for (int w = 0; w < D / 64; ++w) {
+                    const uint32_t hit = (((v.s[w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+                    v.s[w] &= ~(hit * 0xFFu);
+                    blocks |= ((hit | hit >> 7 | hit >> 14 | hit >> 21) & 0xFu) << (4 * w);
+                }
+                mine[WaveLds<D>::kNan + L.lane] = (uint8_t)(valid ? blocks : 0u);
+                for (int j = 0; j < 16; ++j) {
+                    const int tok = 16 * (j >> 2) + 4 * L.g + (j & 3);
+                    const uint32_t x = mine[WaveLds<D>::kNan + tok];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) nan_blocks[n] |= sees(a, pos[n], t0 + tok) ? x : 0u;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) *reinterpret_cast<u32x4v*>(mine + j * kVJ + L.lane * 16) = v.w[j];
+            stage_scales<D>(mine, v.s, valid, L);
+            const int next = i + 4;
+            Place where;
+            if (next < stop) {
+                where = place(a, entries, span.tile(next));
+                load_v<D>(head, where, off, L, v);
+                entries = page_entries(a, table, seq.len, span.tile(min(next + 4, stop - 1)), L);
+            }
+
+            // scores of 64 tokens
+            f32x4 x[NT][4];
+            const auto score = [&](int t, KWords<D> w, uint32_t scales) {
+                f16x8 kk[D / 32];
+                dequant_row<D>(w, scales, kk);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    x[n][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c)
+                        x[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk[c], q[n][c], x[n][t], 0, 0, 0);
+                }
+            };
+            score(0, k.w0, k.s0);
+            score(1, k.w1, k.s1);
+            score(2, k.w2, k.s2);
+            score(3, k.w3, k.s3);
+            if (next < stop) load_k<D>(head, where, off, k);
+
+            // masks only where an edge crosses the tile (uniform)
+            if (t0 + 63 > span.p_lo || (a.window && t0 <= (int64_t)span.p_hi - a.window)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[n][u], o[n][dt], 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[n][t][e] = sees(a, pos[n], t0 + 16 * t + 4 * L.g + e) ? x[n][t][e] : -__builtin_inff();
+            }
+            f16x8 p[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) softmax_step<D>(x[n], factor[n], m[n], l[n], o[n], p[n]);
+
+            // O^T += V^T P^T
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+                const i32x2 c = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                    (__attribute__((address_space(3))) i32x2*)(mine + v_addr<D>(L.g, L.col, dt)));
+                const f16x8* sc = reinterpret_cast<const f16x8*>(mine + WaveLds<D>::kScales + dt * 128 + L.g * 32);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const f16x8 vv = e2m1_8(u ? c.y : c.x) * sc[u];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[n][u], o[n][dt], 0, 0, 0);
+                }
+            }
+            i = next;
+        }
+
+        // ---- join the four waves
+        __syncthreads();                                    // the staging areas are free
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            l[n] += shfl_xor_f32(l[n], 16);
+            l[n] += shfl_xor_f32(l[n], 32);
+            nan_blocks[n] |= shfl_xor_u32(nan_blocks[n], 16);
+            nan_blocks[n] |= shfl_xor_u32(nan_blocks[n], 32);
+            if (__any(nan_blocks[n] != 0)) {
+#pragma unroll
+                for (int dt = 0; dt < D / 16; ++dt)
+                    if ((nan_blocks[n] >> dt) & 1) o[n][dt] = f32x4{0, 0, 0, 0} + __builtin_nanf("");
+            }
+            if (L.g == 0) join[wave][n * 16 + L.col] = make_float2(m[n], l[n]);
+        }
+        const bool whole = first == 0 && last == n_unit;
+        // a cut unit's part: slot 1 of the work-group where it begins, slot 0 of those it goes on in
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
+        if (first == 0 && tid == 0 && a.desc) {
+            const int64_t rest = before + (int64_t)(kvh + 1) * n_unit - end;                 // tiles past this stretch
+            a.desc[(int64_t)b * a.c.kv_heads + kvh] =
+                make_int2((int)blockIdx.x, whole ? 0 : (int)((rest + share - 1) / share) + 1);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4* const all = reinterpret_cast<f32x4*>(lds);
+            if (n) __syncthreads();
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) all[(wave * (D / 16) + dt) * 64 + L.lane] = o[n][dt];
+            __syncthreads();
+            float top = kFloor, total = 0.0f, f[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, join[w][n * 16 + L.col].x);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                f[w] = __builtin_amdgcn_exp2f(join[w][n * 16 + L.col].x - top);
+                total += join[w][n * 16 + L.col].y * f[w];
+            }
+            const int r = n * 16 + L.col;
+            const bool live = r < rows;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const int dt = wave * (D / 64) + j;
+                f32x4 y = all[dt * 64 + L.lane] * f[0];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) y += all[(w * (D / 16) + dt) * 64 + L.lane] * f[w];
+                const int d0 = 16 * dt + 4 * L.g;
+                if (!live) continue;
+                if (whole)
+                    store_finished<D>(a, seq, kvh, r, d0, y, top, total, vg);
+                else
+                    store_part<D>(a, slot * (NT * 16) + r, d0, y, top, total);
             }
         }
-        i = next;
-    }
-
-    // join the four waves
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        l[n] += shfl_xor_f32(l[n], 16);
-        l[n] += shfl_xor_f32(l[n], 32);
-        if (L.g == 0) join[wave][n * 16 + col] = make_float2(m[n], l[n]);
-    }
-    const float vg = a.c.vg[kvh];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        __syncthreads();
-        float top = kFloor, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, join[w][n * 16 + col].x);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += join[w][n * 16 + col].y * __builtin_amdgcn_exp2f(join[w][n * 16 + col].x - top);
-        const float f = __builtin_amdgcn_exp2f(m[n] - top);
-        f32x4* const all = reinterpret_cast<f32x4*>(lds);
-#pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) all[(wave * (D / 16) + dt) * 64 + L.lane] = o[n][dt] * f;
-        __syncthreads();
-        const int r = n * 16 + col;
-        const bool live = r < rows;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            const int dt = wave * (D / 64) + j;
-            f32x4 v = all[dt * 64 + L.lane];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) v += all[(w * (D / 16) + dt) * 64 + L.lane];
-            if (live) store_rows<D>(a, seq, unit, kvh, split, used, NT * 16, r0 + r, 16 * dt + 4 * L.g, v, top, sum, vg);
+        __syncthreads();                                    // before the next segment's staging
+        at += last - first;
+        if (last == n_unit && kvh == a.c.kv_heads - 1) {
+            before += (int64_t)n_unit * a.c.kv_heads;
+            ++b;
         }
     }
 }
 
-// Joins the splits of every query row: a work-group per row.  Its lanes first turn the
-// splits' maxima and sums into weights (LDS), then each wave adds every fourth split, all
-// of a lane's loads independent of one another.
-template <int D>
-__global__ __launch_bounds__(256) void k_attention_join(const AttnArgs a) {
-    __shared__ float weight[kMaxSplits];
+// Joins a query row's parts: W waves per row (a work-group has four).  Lanes first turn the
+// parts' maxima and sums into weights (LDS), then each wave adds every W-th part, all of a
+// lane's loads independent of one another.  parts: at most kMaxParts; part 0 at `first`, the
+// others `step` apart from `rest` on (rows).  Every thread of the work-group calls it; a row
+// with no parts to join does nothing.
+template <int D, int W>
+__device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int kvh, int64_t r, int parts, int64_t first,
+                                         int64_t rest, int64_t step) {
+    constexpr int kRows = 4 / W;                             // rows of a work-group
+    __shared__ float weight[kRows][kMaxParts];
     __shared__ float wave_sum[4], wave_top[4];
     __shared__ float part[4][D];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int mine = tid / (64 * W), t = tid % (64 * W), w0 = wave % W;
+    const auto row_of = [&](int s) { return s == 0 ? first : rest + (s - 1) * step; };
+    float2 ml[kMaxParts / (64 * W)];
+    float top = kFloor;
+#pragma unroll
+    for (int j = 0; j < kMaxParts / (64 * W); ++j) {
+        const int s = t + 64 * W * j;
+        ml[j] = s < parts ? a.part_ml[row_of(s)] : make_float2(kFloor, 0.0f);
+        top = __builtin_fmaxf(top, ml[j].x);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = __builtin_fmaxf(top, shfl_xor_f32(top, o));
+    if (W > 1) {
+        if (lane == 0) wave_top[wave] = top;
+        __syncthreads();
+        top = __builtin_fmaxf(__builtin_fmaxf(wave_top[0], wave_top[1]), __builtin_fmaxf(wave_top[2], wave_top[3]));
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMaxParts / (64 * W); ++j) {
+        const float f = __builtin_amdgcn_exp2f(ml[j].x - top);
+        weight[mine][t + 64 * W * j] = f;
+        sum += ml[j].y * f;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += shfl_xor_f32(sum, o);
+    if (W > 1) {
+        if (lane == 0) wave_sum[wave] = sum;
+        __syncthreads();
+        sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+    }
+    float v[D / 64] = {};
+#pragma unroll 8
+    for (int s = w0; s < parts; s += W) {
+        const float w = weight[mine][s];
+        const float* src = a.part_o + row_of(s) * D + lane * (D / 64);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) v[j] += src[j] * w;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) part[wave][lane * (D / 64) + j] = v[j];
+    if (W > 1) __syncthreads();
+    if (t >= D / 4 || parts == 0) return;
+    f32x4 y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int d = 4 * t + j;
+        y[j] = W > 1 ? (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]) : part[wave][d];
+    }
+    store_finished<D>(a, seq, kvh, r, 4 * t, y, top, sum, a.c.vg[kvh]);
+}
+
+// The units that the line's stretches cut (desc: where the unit begins, and its parts).
+// W = 4: a work-group per row; W = 1: a wave.
+template <int D, int W>
+__global__ __launch_bounds__(256) void k_attention_join_units(const AttnArgs a) {
+    const int64_t item = (int64_t)blockIdx.x * (4 / W) + (threadIdx.x >> 6) / W;
+    const int64_t unit = item / a.tile_rows;                 // (tile_rows is a multiple of 4)
+    const int r = (int)(item - unit * a.tile_rows);
+    const int2 d = a.desc[unit];
+    if (d.y == 0 && W > 1) return;                           // finished by its work-group
+    const int b = (int)(unit / a.c.kv_heads), kvh = (int)(unit - (int64_t)b * a.c.kv_heads);
+    const Seq seq = sequence(a, b);
+    const int rows = min(seq.nq, a.max_q_len) * a.group;
+    const int64_t at = 2 * (int64_t)d.x;
+    const int parts = r < rows ? d.y : 0;
+    if (parts == 0) return;
+    join_row<D, W>(a, seq, kvh, r, parts, (at + 1) * a.tile_rows + r, (at + 2) * a.tile_rows + r, 2 * (int64_t)a.tile_rows);
+}
+
+// The units that the form for many rows split.
+template <int D>
+__global__ __launch_bounds__(256) void k_attention_join_splits(const AttnArgs a) {
     const int64_t unit = blockIdx.x / (unsigned)a.tile_rows;
     const int r = (int)(blockIdx.x % (unsigned)a.tile_rows);
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int kvh = (int)(unit % a.c.kv_heads);
     const int64_t bt = unit / a.c.kv_heads;
     const int b = (int)(bt / a.row_tiles), rt = (int)(bt - (int64_t)b * a.row_tiles);
@@ -377,54 +594,14 @@ __global__ __launch_bounds__(256) void k_attention_join(const AttnArgs a) {
     const int64_t r0 = (int64_t)rt * a.tile_rows;
     if (r0 + r >= rows) return;
     const int64_t r1 = min(r0 + a.tile_rows, rows) - 1;
-    const Span span = tile_span(a, seq, (int)(r0 / a.group), (int)(r1 / a.group));
-    const int used = splits_used(a, span.n);
+    const int used = splits_used(a, tile_span(a, seq, (int)(r0 / a.group), (int)(r1 / a.group)).n);
     if (used <= 1) return;                                   // written by the first kernel
     const int64_t at = unit * a.splits * a.tile_rows + r;
-    const int mine = (int)threadIdx.x;
-    const float2 ml = mine < used ? a.part_ml[at + (int64_t)mine * a.tile_rows] : make_float2(kFloor, 0.0f);
-    float top = ml.x;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) top = __builtin_fmaxf(top, shfl_xor_f32(top, o));
-    if (lane == 0) wave_top[wave] = top;
-    __syncthreads();
-    top = __builtin_fmaxf(__builtin_fmaxf(wave_top[0], wave_top[1]), __builtin_fmaxf(wave_top[2], wave_top[3]));
-    const float f = __builtin_amdgcn_exp2f(ml.x - top);
-    weight[mine] = f;
-    float sum = ml.y * f;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) sum += shfl_xor_f32(sum, o);
-    if (lane == 0) wave_sum[wave] = sum;
-    __syncthreads();
-    sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
-    const float* po = a.part_o + at * D + lane * (D / 64);
-    float v[D / 64] = {};
-#pragma unroll 8
-    for (int s = wave; s < used; s += 4) {
-        const float w = weight[s];
-        const float* src = po + (int64_t)s * a.tile_rows * D;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) v[j] += src[j] * w;
-    }
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) part[wave][lane * (D / 64) + j] = v[j];
-    __syncthreads();
-    if ((int)threadIdx.x >= D / 2) return;
-    const int qi = (int)((r0 + r) / a.group), head = kvh * a.group + (int)((r0 + r) - (int64_t)qi * a.group);
-    const float inv = sum == 0.0f ? 0.0f : a.c.vg[kvh] / sum;
-    float x[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int d = 2 * (int)threadIdx.x + j;
-        x[j] = ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) * inv;
-    }
-    uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D;
-    reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = pack_bf16(x[0], x[1]);
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(top, sum);
+    join_row<D, 4>(a, seq, kvh, r0 + r, used, at, at + a.tile_rows, a.tile_rows);
 }
 
 hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.batch * a.row_tiles * a.c.kv_heads * a.splits));
+    const dim3 grid((unsigned)a.splits);
     if (a.c.head_dim == 128) {
         if (a.tile_rows == 16)
             hipLaunchKernelGGL((k_attention_rows<128, 1>), grid, dim3(256), 0, stream, a);
@@ -439,13 +616,23 @@ hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_attention_join(const AttnArgs& a, hipStream_t stream) {
-    const int64_t items = (int64_t)a.batch * a.row_tiles * a.c.kv_heads * a.tile_rows;
-    const dim3 grid((unsigned)items);
-    if (a.c.head_dim == 128)
-        hipLaunchKernelGGL(k_attention_join<128>, grid, dim3(256), 0, stream, a);
+// The work-groups that may cut a unit number gridDim / units on average: with few, a wave
+// adds a row's parts alone (a fourth of the work-groups).
+template <int D>
+static void launch_join(const AttnArgs& a, hipStream_t stream) {
+    const int64_t units = (int64_t)a.batch * a.row_tiles * a.c.kv_heads, rows = units * a.tile_rows;
+    if (!a.desc)
+        hipLaunchKernelGGL(k_attention_join_splits<D>, dim3((unsigned)rows), dim3(256), 0, stream, a);
+    else if (units < a.splits / 4)
+        hipLaunchKernelGGL((k_attention_join_units<D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL(k_attention_join<64>, grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_join_units<D, 1>), dim3((unsigned)(rows / 4)), dim3(256), 0, stream, a);
+}
+hipError_t launch_attention_join(const AttnArgs& a, hipStream_t stream) {
+    if (a.c.head_dim == 128)
+        launch_join<128>(a, stream);
+    else
+        launch_join<64>(a, stream);
     return hipGetLastError();
 }
 

@@ -60,6 +60,11 @@ __device__ __forceinline__ int splits_used(const AttnArgs& a, int tiles) {
     return max(min((tiles + a.chunk - 1) / a.chunk, a.splits), 1);
 }
 
+// The query at position p sees token t (p < t: never; window and sinks are >= 0).
+__device__ __forceinline__ bool sees(const AttnArgs& a, int p, int t) {
+    return t <= p && (!a.window || t > p - a.window || t < a.sinks);
+}
+
 // ---------------------------------------------------------------- FP16 operands
 // 8 E2M1 codes of a dword.
 __device__ __forceinline__ f16x8 e2m1_8(uint32_t w) {
@@ -153,45 +158,27 @@ __device__ __forceinline__ void softmax_step(f32x4 (&x)[4], float factor, float&
     l += (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// V blocks whose scale is NaN: rows whose weight for one of their tokens is not zero get
-// NaN in the block's 16 elements, others nothing.  hit: 1 where a token's block of element
-// tile dt is NaN (its staged scale is zero), in the tokens' operand order.
-template <int NT, int DT>
-__device__ __forceinline__ void spread_nan(const f16x8 (&hit)[2], int dt, const f16x8 (&p)[NT][2], f32x4 (&o)[NT][DT]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        f32x4 z = {0, 0, 0, 0};
-#pragma unroll
-        for (int u = 0; u < 2; ++u) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(hit[u], p[n][u], z, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (!(z[e] == 0.0f)) o[n][dt][e] = __builtin_nanf("");
-    }
-}
-
 // ---------------------------------------------------------------- results
 // Natural logarithm of the sum of exponentials of a row with maximum m (base 2) and biased sum.
 __device__ __forceinline__ float row_lse(float m, float sum) {
     return sum == 0.0f ? -__builtin_inff() : ((m - kBias) + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
-// Four elements d0 .. d0 + 3 of row r of a unit: the finished output where the row has one
-// split, else the split's part.  d0 == 0 also stores the row's sums.
+// Four elements d0 .. d0 + 3 of row r of a sequence's rows of one cached head, finished (o:
+// unnormalized) ...
 template <int D>
-__device__ __forceinline__ void store_rows(const AttnArgs& a, const Seq& seq, int64_t unit, int kvh, int split, int used,
-                                           int tile_rows, int64_t r_in_seq, int d0, const f32x4& v, float m, float sum,
-                                           float vg) {
-    if (used == 1) {
-        const int qi = (int)(r_in_seq / a.group), head = kvh * a.group + (int)(r_in_seq - (int64_t)qi * a.group);
-        const float inv = sum == 0.0f ? 0.0f : vg / sum;
-        uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D + d0;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
-        if (a.lse && d0 == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(m, sum);
-        return;
-    }
-    const int64_t at = (unit * a.splits + split) * tile_rows + r_in_seq % tile_rows;
-    *reinterpret_cast<f32x4*>(a.part_o + at * D + d0) = v;
+__device__ __forceinline__ void store_finished(const AttnArgs& a, const Seq& seq, int kvh, int64_t r, int d0, const f32x4& o,
+                                               float m, float sum, float vg) {
+    const int qi = (int)(r / a.group), head = kvh * a.group + (int)(r - (int64_t)qi * a.group);
+    const float inv = sum == 0.0f ? 0.0f : vg / sum;
+    uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D + d0;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    if (a.lse && d0 == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(m, sum);
+}
+// ... or as one part of it, in row `at` of the workspace.
+template <int D>
+__device__ __forceinline__ void store_part(const AttnArgs& a, int64_t at, int d0, const f32x4& o, float m, float sum) {
+    *reinterpret_cast<f32x4*>(a.part_o + at * D + d0) = o;
     if (d0 == 0) a.part_ml[at] = make_float2(m, sum);
 }
 

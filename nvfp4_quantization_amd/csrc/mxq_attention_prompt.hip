@@ -292,19 +292,17 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 const int tok = t0 + 8 * (e >> 2) + 4 * h + (e & 3);
-                const bool see = tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
-                x[e >> 4][e & 15] = see ? x[e >> 4][e & 15] : -__builtin_inff();
+                x[e >> 4][e & 15] = sees(a, pos, tok) ? x[e >> 4][e & 15] : -__builtin_inff();
             }
         }
         if (noted.x | noted.y | noted.z | noted.w) {   // (rare) note the NaN V blocks this lane sees
 #pragma unroll 1
             for (int e = 0; e < 32; ++e) {
                 const int tok = t0 + 8 * (e >> 2) + 4 * h + (e & 3);
-                const bool see = tok <= pos && (!a.window || tok > pos - a.window || tok < a.sinks);
                 const uint32_t w = *reinterpret_cast<const uint32_t*>(vn.nan + 4 * (tok - t0));
                 const uint32_t blocks = D == 128 ? (w & 3u) | (w >> 6 & 0xCu) | (w >> 12 & 0x30u) | (w >> 18 & 0xC0u)
                                                  : (w & 1u) | (w >> 7 & 2u) | (w >> 14 & 4u) | (w >> 21 & 8u);
-                nan_blocks |= see ? blocks : 0u;
+                nan_blocks |= sees(a, pos, tok) ? blocks : 0u;
             }
         }
         float top = x[0][0];
@@ -368,9 +366,13 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-            store_rows<D>(a, seq, unit, kvh, split, used, kRowTile, r0 + row, 32 * dt + 2 * e + 4 * h,
-                          f32x4{o[dt][e], o[dt][e + 1], o[dt][e + 2], o[dt][e + 3]}, m, l, vg);
+        for (int e = 0; e < 16; e += 4) {
+            const f32x4 y = {o[dt][e], o[dt][e + 1], o[dt][e + 2], o[dt][e + 3]};
+            if (used == 1)
+                store_finished<D>(a, seq, kvh, r0 + row, 32 * dt + 2 * e + 4 * h, y, m, l, vg);
+            else
+                store_part<D>(a, (unit * a.splits + split) * kRowTile + row, 32 * dt + 2 * e + 4 * h, y, m, l);
+        }
 }
 
 hipError_t launch_attention_prompt(const AttnArgs& a, hipStream_t stream) {

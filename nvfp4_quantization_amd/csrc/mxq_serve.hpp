@@ -59,7 +59,7 @@ struct RopeAppendArgs {
 hipError_t launch_rope_append_nvfp4(const RopeAppendArgs& a, bool interleaved, hipStream_t stream);
 
 // ---------------------------------------------------------------- attention
-constexpr int kMaxSplits = 256;       // chunks of one unit's cache axis (a join work-group's threads)
+constexpr int kMaxParts = 512;        // parts of one unit that the join adds (and work-groups of the rows form)
 struct AttnArgs {
     const uint16_t* q;
     uint16_t* out;
@@ -78,12 +78,15 @@ struct AttnArgs {
     int32_t window, sinks;
     float scale_log2;                 // softmax_scale * log2(e)
     KvCache c;
-    // the plan: a unit is (sequence, row tile, cached head) with tile_rows query rows, its
-    // visible 64-token tiles in at most `splits` chunks of `chunk` (the last takes the rest)
+    // the plan: a unit is (sequence, row tile, cached head) with tile_rows query rows.
+    // Rows form: `splits` work-groups share the line of all units' tiles (one row tile);
+    // form for many rows: each unit's visible tiles in at most `splits` chunks of `chunk`
+    // (the last takes the rest).
     int32_t tile_rows, row_tiles;
     int32_t splits, chunk;
-    float* part_o;                    // workspace: [unit][split][tile_rows][head_dim]
-    float2* part_ml;                  // workspace: [unit][split][tile_rows] (maximum, sum)
+    float* part_o;                    // workspace: parts, [part][tile_rows][head_dim]
+    float2* part_ml;                  // workspace: [part][tile_rows] (maximum, sum)
+    int2* desc;                       // workspace, rows form: [unit] (first work-group, parts or 0)
 };
 hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_prompt(const AttnArgs& a, hipStream_t stream);

@@ -39,6 +39,8 @@ bool index3_ok(int64_t a, int64_t sa, int64_t b, int64_t sb, int64_t c, int64_t 
     return (a - 1) * sa + (b - 1) * sb < kMaxElems - (c - 1) * sc;
 }
 
+int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+
 mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
     if (!c || c->num_pages < 0 || c->kv_heads < 1 || c->page_size < 1 || c->head_dim < 1)
         return MXQ_ERR_INVALID_ARGUMENT;
@@ -70,18 +72,23 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
 }
 
 // How the attention call splits its work.  A unit is (sequence, row tile, cached head).
-//   rows form    up to 32 query rows per cached head, 16 or 32 a unit: a decoding step or
-//                a draft reads the cache once.
-//   prompt form  more rows, 128 a unit, whose waves share the dequantized tiles.
-// The cache axis of a unit is cut into chunks of 64-token tiles so that the launch has
-// about kRowsGroups or kPromptGroups work-groups (three or two fit a CU, and ragged lengths
-// want some to spare), but no chunk is shorter than one tile per wave.
-constexpr int64_t kRowsGroups = 256 * 6;
+//   rows form    up to 32 query rows per cached head: a decoding step or a draft.  One row
+//                tile of 16 or 32.  With kManyUnits units or more, or where no unit has
+//                more than four tiles (one per wave), a work-group takes a unit; else at
+//                most kRowsGroups work-groups (what the chip holds at once) share the line
+//                of all units' 64-token tiles evenly, four each at least.
+//   prompt form  more rows, 128 a unit, whose waves share the dequantized tiles.  A unit's
+//                tiles are cut into chunks only where there are fewer units than
+//                kPromptGroups work-groups (two fit a CU).
+constexpr int64_t kRowsGroups = 256 * 2;
+constexpr int64_t kManyUnits = 8 * kRowsGroups;
+constexpr int64_t kLineSeqs = 1024;            // sequences that one work-group lays out
 constexpr int64_t kPromptGroups = 256 * 2;
+static_assert(kRowsGroups <= mxq::kMaxParts, "a unit may be cut by every work-group");
 struct AttnPlan {
     int32_t tile_rows, row_tiles, splits, chunk;
     int64_t units;
-    size_t ml_offset, bytes;          // workspace: parts, then maxima and sums
+    size_t ml_offset, desc_offset, bytes;      // workspace: parts, maxima and sums, unit descriptors
 };
 
 bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, int64_t total_q, int64_t max_q,
@@ -90,6 +97,7 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
         total_q < 1 || max_q < 1 || max_len < 0 || window < 0 || sinks < 0 || !product_below(total_q, q_heads, 1ll << 31))
         return false;
     if (max_q > total_q) max_q = total_q;
+    if (max_len > (1ll << 31)) max_len = 1ll << 31;
     const int64_t group = q_heads / kv_heads, rows = max_q * group;
     p->tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
     p->row_tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
@@ -100,22 +108,27 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
         tiles = tiles < near + far ? tiles : near + far;
     }
     if (tiles < 1) tiles = 1;
-    const int64_t groups = p->tile_rows == 128 ? kPromptGroups : kRowsGroups;
-    int64_t chunk = product_below(tiles, p->units, 1ll << 62) ? (tiles * p->units + groups - 1) / groups : tiles;
-    chunk = (chunk + 3) / 4 * 4;
-    int64_t splits = (tiles + chunk - 1) / chunk;
-    if (splits > mxq::kMaxSplits) {
-        chunk = (tiles + mxq::kMaxSplits - 1) / mxq::kMaxSplits;
-        chunk = (chunk + 3) / 4 * 4;
-        splits = (tiles + chunk - 1) / chunk;
+    int64_t parts = 0;
+    p->ml_offset = p->desc_offset = p->bytes = 0;
+    if (p->tile_rows < 128) {
+        const bool line = tiles > 4 && p->units < kManyUnits && batch <= kLineSeqs;
+        const int64_t most = product_below(p->units, tiles, 4 * kRowsGroups) ? (p->units * tiles + 3) / 4 : kRowsGroups;
+        p->splits = (int32_t)(!line ? p->units : most < kRowsGroups ? most : kRowsGroups);
+        p->chunk = 0;
+        parts = line ? 2 * (int64_t)p->splits : 0;
+    } else {
+        int64_t chunk = product_below(p->units, tiles, 1ll << 62) ? (p->units * tiles + kPromptGroups - 1) / kPromptGroups : tiles;
+        if (p->units * 2 > kPromptGroups || chunk > tiles) chunk = tiles;
+        if (chunk < 4) chunk = 4;
+        p->chunk = (int32_t)chunk;
+        p->splits = (int32_t)((tiles + chunk - 1) / chunk);
+        if (p->splits > mxq::kMaxParts) return false;        // (units >= 1 and kPromptGroups chunks: never)
+        parts = p->splits > 1 ? p->units * p->splits : 0;
     }
-    p->splits = (int32_t)splits;
-    p->chunk = (int32_t)chunk;
-    p->ml_offset = p->bytes = 0;
-    if (splits > 1) {
-        const int64_t rows_all = p->units * splits * p->tile_rows;
-        p->ml_offset = (size_t)(rows_all * d * 4);
-        p->bytes = (size_t)((rows_all * (d * 4 + 8) + 255) / 256 * 256);
+    if (parts > 0) {
+        p->ml_offset = (size_t)(parts * p->tile_rows * d * 4);
+        p->desc_offset = p->ml_offset + (size_t)(parts * p->tile_rows * 8);
+        p->bytes = (size_t)round256((int64_t)p->desc_offset + (p->tile_rows < 128 ? p->units * 8 : 0));
     }
     return true;
 }
@@ -231,7 +244,8 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
         return MXQ_ERR_UNSUPPORTED;
     AttnPlan p;
     if (!plan_attention(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len, max_seq_len, window, sinks, &p) ||
-        !product_below(p.units * p.splits, 256, kMaxGridThreads) || !product_below(p.units, 256ll * p.tile_rows, kMaxGridThreads))
+        !product_below(p.units, 256ll * p.tile_rows, kMaxGridThreads) ||
+        !product_below(p.tile_rows == 128 ? p.units * p.splits : p.splits, 256, kMaxGridThreads))
         return MXQ_ERR_UNSUPPORTED;
     if (p.bytes > 0) {
         if (!workspace) return MXQ_ERR_INVALID_ARGUMENT;
@@ -266,10 +280,11 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     a.part_o = p.bytes ? reinterpret_cast<float*>(ws) : nullptr;
     a.part_ml = p.bytes ? reinterpret_cast<float2*>(ws + p.ml_offset) : nullptr;
+    a.desc = p.bytes && p.tile_rows < 128 ? reinterpret_cast<int2*>(ws + p.desc_offset) : nullptr;
     hipStream_t const hs = static_cast<hipStream_t>(stream);
     if ((p.tile_rows == 128 ? mxq::launch_attention_prompt(a, hs) : mxq::launch_attention_rows(a, hs)) != hipSuccess)
         return MXQ_ERR_HIP;
-    if (p.splits > 1 && mxq::launch_attention_join(a, hs) != hipSuccess) return MXQ_ERR_HIP;
+    if (p.bytes > 0 && mxq::launch_attention_join(a, hs) != hipSuccess) return MXQ_ERR_HIP;
     return MXQ_OK;
 }
 
