@@ -501,8 +501,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
 // Joins a query row's parts: W waves per row (a work-group has four).  Lanes first turn the
 // parts' maxima and sums into weights (LDS), then each wave adds every W-th part, all of a
 // lane's loads independent of one another.  parts: at most kMaxParts; part 0 at `first`, the
-// others `step` apart from `rest` on (rows).  Every thread of the work-group calls it; a row
-// with no parts to join does nothing.
+// others `step` apart from `rest` on (rows).
 template <int D, int W>
 __device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int kvh, int64_t r, int parts, int64_t first,
                                          int64_t rest, int64_t step) {
@@ -553,7 +552,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int 
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) part[wave][lane * (D / 64) + j] = v[j];
     if (W > 1) __syncthreads();
-    if (t >= D / 4 || parts == 0) return;
+    if (t >= D / 4) return;
     f32x4 y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -570,14 +569,15 @@ __global__ __launch_bounds__(256) void k_attention_join_units(const AttnArgs a) 
     const int64_t item = (int64_t)blockIdx.x * (4 / W) + (threadIdx.x >> 6) / W;
     const int64_t unit = item / a.tile_rows;                 // (tile_rows is a multiple of 4)
     const int r = (int)(item - unit * a.tile_rows);
-    const int2 d = a.desc[unit];
-    if (d.y == 0 && W > 1) return;                           // finished by its work-group
+    int2 d = a.desc[unit];
+    d.x = min(max(d.x, 0), a.splits - 1);                    // (in bounds whatever the workspace holds)
+    d.y = min(max(d.y, 0), a.splits - d.x);
+    if (d.y == 0) return;                                    // finished by its work-group
     const int b = (int)(unit / a.c.kv_heads), kvh = (int)(unit - (int64_t)b * a.c.kv_heads);
     const Seq seq = sequence(a, b);
-    const int rows = min(seq.nq, a.max_q_len) * a.group;
+    if (r >= min(seq.nq, a.max_q_len) * a.group) return;
     const int64_t at = 2 * (int64_t)d.x;
-    const int parts = r < rows ? d.y : 0;
-    if (parts == 0) return;
+    const int parts = d.y;
     join_row<D, W>(a, seq, kvh, r, parts, (at + 1) * a.tile_rows + r, (at + 2) * a.tile_rows + r, 2 * (int64_t)a.tile_rows);
 }
 
