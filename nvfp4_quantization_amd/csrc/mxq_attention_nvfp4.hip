@@ -169,11 +169,13 @@ __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[
 
 // ---------------------------------------------------------------- the line of tiles
 constexpr int kLineSeqs = 1024;       // sequences of a call whose units share the line
-// Tiles of a unit of a sequence (one at least where there are queries, which then get their
-// zeros).
-__device__ __forceinline__ int unit_tiles(const AttnArgs& a, const Seq& s) {
+// A unit's length on the line: its tiles and kUnitCost more for what a unit costs beside them
+// (queries, the first loads' latency, the join of the waves: about one round of four
+// tiles), so that stretches of many short units are not longer in time.  0 without queries.
+constexpr int kUnitCost = 4;
+__device__ __forceinline__ int unit_length(const AttnArgs& a, const Seq& s) {
     const int nq = min(s.nq, a.max_q_len);
-    return nq > 0 ? max(tile_span(a, s, 0, nq - 1).n, 1) : 0;
+    return nq > 0 ? tile_span(a, s, 0, nq - 1).n + kUnitCost : 0;
 }
 // Inclusive sum over the lanes of a wave.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
@@ -195,9 +197,9 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
     constexpr int kLds = 4 * kWave > 4 * kJoin ? 4 * kWave : 4 * kJoin;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     __shared__ float2 join[4][NT * 16];
-    // of the sequences on the line: length, first query row, queries, tiles of a unit
+    // of the sequences on the line: length, first query row, queries, a unit's length on it
     __shared__ int4 seqs[kLineSeqs];
-    __shared__ uint32_t wave_tiles[4], wave_most[4];
+    __shared__ uint32_t wave_length[4];
     __shared__ int found;
     __shared__ int64_t found_before;
 
@@ -207,46 +209,42 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
     L.g = L.lane >> 4, L.col = L.lane & 15;
 
     // ---- this work-group's stretch of the line [at, end), and the sequence it starts in
-    int64_t at = 0, end, share = 0, before = 0;             // before: line tiles of the sequences before b
+    int64_t at = 0, end, share = 0, before = 0;             // before: the line up to sequence b
     int b;
     if (!a.desc) {                                          // a unit of its own
         b = (int)(blockIdx.x / (unsigned)a.c.kv_heads);
         const Seq s = sequence(a, b);
-        const int n = unit_tiles(a, s);
+        const int n = unit_length(a, s);
         if (n == 0) return;
         seqs[0] = make_int4(s.len, s.start, s.nq, n);       // (every thread the same)
         at = (int64_t)(blockIdx.x - (unsigned)b * (unsigned)a.c.kv_heads) * n;
         end = at + n;
     } else {
         // four consecutive sequences a thread
-        uint32_t n[4], sum = 0, most = 0;
+        uint32_t n[4], sum = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             n[j] = 0;
             if (4 * tid + j < a.batch) {
                 const Seq s = sequence(a, 4 * tid + j);
-                n[j] = (uint32_t)unit_tiles(a, s);
+                n[j] = (uint32_t)unit_length(a, s);
                 seqs[4 * tid + j] = make_int4(s.len, s.start, s.nq, (int)n[j]);
             }
             sum += n[j];
-            most = max(most, n[j]);
         }
         const uint32_t upto = wave_scan(sum);
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) most = max(most, shfl_xor_u32(most, o));
-        if (L.lane == 63) wave_tiles[wave] = upto, wave_most[wave] = most;
+        if (L.lane == 63) wave_length[wave] = upto;
         __syncthreads();
-        int64_t mine = 0, line = 0;                         // tiles before this thread's sequences; all
+        int64_t mine = 0, line = 0;                         // before this thread's sequences; all
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            if (w < wave) mine += wave_tiles[w];
-            line += wave_tiles[w];
-            most = max(most, wave_most[w]);
+            if (w < wave) mine += wave_length[w];
+            line += wave_length[w];
         }
         line *= a.c.kv_heads;
-        // equal stretches; of whole rounds of four waves, unless all units are shorter
-        share = (line + gridDim.x - 1) / gridDim.x;
-        share = share > 4 ? (share + 3) / 4 * 4 : max(share, (int64_t)min(most, 4u));
+        // equal stretches of whole rounds of four waves
+        share = line >> 32 ? (line + gridDim.x - 1) / gridDim.x : (int64_t)(((uint32_t)line + gridDim.x - 1) / gridDim.x);
+        share = max((share + 3) / 4 * 4, (int64_t)8);
         at = (int64_t)blockIdx.x * share;
         end = min(at + share, line);
         if (at >= end) return;
@@ -278,8 +276,9 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             ++b;
             continue;
         }
-        const int kvh = __builtin_amdgcn_readfirstlane((int)((at - before) / n_unit));
-        const int first = __builtin_amdgcn_readfirstlane((int)((at - before) - (int64_t)kvh * n_unit));
+        const int64_t ahead = at - before;
+        const int kvh = __builtin_amdgcn_readfirstlane(ahead >> 32 ? (int)(ahead / n_unit) : (int)((uint32_t)ahead / (uint32_t)n_unit));
+        const int first = __builtin_amdgcn_readfirstlane((int)(ahead - (int64_t)kvh * n_unit));
         const int last = __builtin_amdgcn_readfirstlane((int)min((int64_t)n_unit, first + (end - at)));
         Seq seq;
         seq.len = __builtin_amdgcn_readfirstlane(info.x);
@@ -287,7 +286,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
         seq.nq = __builtin_amdgcn_readfirstlane(info.z);
         const int rows = min(seq.nq, a.max_q_len) * a.group;
         const Span span = tile_span(a, seq, 0, (rows - 1) / a.group);
-        const int stop = min(last, span.n);                 // (no tile where no query sees a token)
+        const int stop = min(last, span.n);
         const Base head{a.c.kc + kvh * a.c.cs_head, a.c.ks + kvh * a.c.ss_head, a.c.vc + kvh * a.c.cs_head,
                         a.c.vs + kvh * a.c.ss_head};
 
@@ -454,7 +453,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
         // a cut unit's part: slot 1 of the work-group where it begins, slot 0 of those it goes on in
         const int64_t slot = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
         if (first == 0 && tid == 0 && a.desc) {
-            const int64_t rest = before + (int64_t)(kvh + 1) * n_unit - end;                 // tiles past this stretch
+            const int64_t rest = before + (int64_t)(kvh + 1) * n_unit - end;                 // past this stretch
             a.desc[(int64_t)b * a.c.kv_heads + kvh] =
                 make_int2((int)blockIdx.x, whole ? 0 : (int)((rest + share - 1) / share) + 1);
         }

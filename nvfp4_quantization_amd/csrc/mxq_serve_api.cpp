@@ -74,15 +74,16 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
 // How the attention call splits its work.  A unit is (sequence, row tile, cached head).
 //   rows form    up to 32 query rows per cached head: a decoding step or a draft.  One row
 //                tile of 16 or 32.  With kManyUnits units or more, or where no unit has
-//                more than four tiles (one per wave), a work-group takes a unit; else at
-//                most kRowsGroups work-groups (what the chip holds at once) share the line
-//                of all units' 64-token tiles evenly, four each at least.
+//                more than kShortTiles tiles, a work-group takes a unit; else at most
+//                kRowsGroups work-groups (what the chip holds at once) share the line of
+//                all units' 64-token tiles evenly.
 //   prompt form  more rows, 128 a unit, whose waves share the dequantized tiles.  A unit's
 //                tiles are cut into chunks only where there are fewer units than
 //                kPromptGroups work-groups (two fit a CU).
 constexpr int64_t kRowsGroups = 256 * 2;
 constexpr int64_t kManyUnits = 8 * kRowsGroups;
 constexpr int64_t kLineSeqs = 1024;            // sequences that one work-group lays out
+constexpr int64_t kShortTiles = 16;
 constexpr int64_t kPromptGroups = 256 * 2;
 static_assert(kRowsGroups <= mxq::kMaxParts, "a unit may be cut by every work-group");
 struct AttnPlan {
@@ -111,7 +112,7 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
     int64_t parts = 0;
     p->ml_offset = p->desc_offset = p->bytes = 0;
     if (p->tile_rows < 128) {
-        const bool line = tiles > 4 && p->units < kManyUnits && batch <= kLineSeqs;
+        const bool line = tiles > kShortTiles && p->units < kManyUnits && batch <= kLineSeqs;
         const int64_t most = product_below(p->units, tiles, 4 * kRowsGroups) ? (p->units * tiles + 3) / 4 : kRowsGroups;
         p->splits = (int32_t)(!line ? p->units : most < kRowsGroups ? most : kRowsGroups);
         p->chunk = 0;
