@@ -152,6 +152,16 @@ __device__ __forceinline__ int v_addr(int g, int k, int dt) {
     return (token >> 5) * kVJ + (token & 31) * 32 + 8 * dt;
 }
 
+// The 16 tokens of element 16 dt + col of lane group g: codes, and the scales of half u.
+template <int D>
+__device__ __forceinline__ i32x2 v_codes(uint8_t* lds, const Lane& L, int dt) {
+    return __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i32x2*)(lds + v_addr<D>(L.g, L.col, dt)));
+}
+template <int D>
+__device__ __forceinline__ f16x8 v_scales(const uint8_t* lds, const Lane& L, int dt, int u) {
+    return *reinterpret_cast<const f16x8*>(lds + WaveLds<D>::kScales + dt * 128 + L.g * 32 + u * 16);
+}
+
 // FP16 scales of this lane's token into LDS (zero for a token that is not valid).
 template <int D>
 __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[D / 64], bool valid, const Lane& L) {
@@ -192,6 +202,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 
 template <int D, int NT>
 __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
+    constexpr int kAhead = 1;
     constexpr int kWave = WaveLds<D>::kBytes;
     constexpr int kJoin = (D / 16) * 64 * 16;               // a wave's outputs of one column tile
     constexpr int kLds = 4 * kWave > 4 * kJoin ? 4 * kWave : 4 * kJoin;
@@ -290,24 +301,29 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
         const Base head{a.c.kc + kvh * a.c.cs_head, a.c.ks + kvh * a.c.ss_head, a.c.vc + kvh * a.c.cs_head,
                         a.c.vs + kvh * a.c.ss_head};
 
-        // Loads run ahead of the tile that uses them: the page table entries by two tiles, V
-        // by one (its registers are free once it is in LDS), K by one (after its use).
+        // Loads run kAhead rounds ahead of the tile that uses them (V's registers are free
+        // once it is in LDS, K's after the scores), page table entries one round further.
         const int32_t* const table = a.table + (int64_t)b * a.ld_table;
-        KRegs<D> k;
-        VRegs<D> v;
+        KRegs<D> k[kAhead];
+        VRegs<D> v[kAhead];
+        int32_t entries[kAhead] = {};
         int i = first + wave;
-        int32_t entries = 0, entries0 = 0;
+        const auto tile_of = [&](int j) { return span.tile(min(j, stop - 1)); };
+        const auto entries_of = [&](int j) { return page_entries(a, table, seq.len, tile_of(j), L); };
         if (i < stop) {
-            entries0 = page_entries(a, table, seq.len, span.tile(i), L);
-            entries = page_entries(a, table, seq.len, span.tile(min(i + 4, stop - 1)), L);
+            int32_t e[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) e[j] = entries_of(i + 4 * j);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) entries[j] = entries_of(i + 4 * (kAhead + j));
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const Place where = place(a, e[j], tile_of(i + 4 * j));
+                load_v<D>(head, where, off, L, v[j]);
+                load_k<D>(head, where, off, k[j]);
+            }
         }
         const float kg = a.c.kg[kvh], vg = a.c.vg[kvh];
-
-        if (i < stop) {
-            const Place where = place(a, entries0, span.tile(i));
-            load_v<D>(head, where, off, L, v);
-            load_k<D>(head, where, off, k);
-        }
 
         // Q as the second operand of S^T = K Q^T: lane (col, g) holds elements D/4 g .. of
         // row col, scaled to FP16 by the row's power of two
@@ -349,7 +365,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             for (int dt = 0; dt < D / 16; ++dt) o[n][dt] = f32x4{0, 0, 0, 0};
         }
 
-        while (i < stop) {
+        const auto step = [&](int i, KRegs<D>& k, VRegs<D>& v, int32_t& entries) {
             const int t0 = span.tile(i) * 64;
             // V and its scales to LDS; tokens past the sequence or of unreadable pages get
             // zero scales, so whatever lies there stays out
@@ -366,6 +382,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
                     blocks |= ((hit | hit >> 7 | hit >> 14 | hit >> 21) & 0xFu) << (4 * w);
                 }
                 mine[WaveLds<D>::kNan + L.lane] = (uint8_t)(valid ? blocks : 0u);
+#pragma unroll 1
                 for (int j = 0; j < 16; ++j) {
                     const int tok = 16 * (j >> 2) + 4 * L.g + (j & 3);
                     const uint32_t x = mine[WaveLds<D>::kNan + tok];
@@ -376,13 +393,11 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) *reinterpret_cast<u32x4v*>(mine + j * kVJ + L.lane * 16) = v.w[j];
             stage_scales<D>(mine, v.s, valid, L);
-            const int next = i + 4;
-            Place where;
-            if (next < stop) {
-                where = place(a, entries, span.tile(next));
-                load_v<D>(head, where, off, L, v);
-                entries = page_entries(a, table, seq.len, span.tile(min(next + 4, stop - 1)), L);
-            }
+            // (past the stretch the last tile again: a branch around a load would make every
+            // later wait for loads a wait for all of them)
+            const Place where = place(a, entries, tile_of(i + 4 * kAhead));
+            load_v<D>(head, where, off, L, v);
+            entries = entries_of(i + 8 * kAhead);
 
             // scores of 64 tokens
             f32x4 x[NT][4];
@@ -398,10 +413,14 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
                 }
             };
             score(0, k.w0, k.s0);
+            __builtin_amdgcn_sched_barrier(0);
             score(1, k.w1, k.s1);
+            __builtin_amdgcn_sched_barrier(0);
             score(2, k.w2, k.s2);
+            __builtin_amdgcn_sched_barrier(0);
             score(3, k.w3, k.s3);
-            if (next < stop) load_k<D>(head, where, off, k);
+            __builtin_amdgcn_sched_barrier(0);
+            load_k<D>(head, where, off, k);
 
             // masks only where an edge crosses the tile (uniform)
             if (t0 + 63 > span.p_lo || (a.window && t0 <= (int64_t)span.p_hi - a.window)) {
@@ -417,21 +436,30 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) softmax_step<D>(x[n], factor[n], m[n], l[n], o[n], p[n]);
 
-            // O^T += V^T P^T
+            // O^T += V^T P^T, the operands of an element tile read while the one before is used
+            // (the order is fixed: the compiler would read all of them first, and spill)
+            i32x2 c = v_codes<D>(mine, L, 0);
+            f16x8 s0 = v_scales<D>(mine, L, 0, 0), s1 = v_scales<D>(mine, L, 0, 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt) {
-                const i32x2 c = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                    (__attribute__((address_space(3))) i32x2*)(mine + v_addr<D>(L.g, L.col, dt)));
-                const f16x8* sc = reinterpret_cast<const f16x8*>(mine + WaveLds<D>::kScales + dt * 128 + L.g * 32);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const f16x8 vv = e2m1_8(u ? c.y : c.x) * sc[u];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[n][u], o[n][dt], 0, 0, 0);
+                const f16x8 v0 = e2m1_8(c.x) * s0, v1 = e2m1_8(c.y) * s1;
+                if (dt + 1 < D / 16) {
+                    c = v_codes<D>(mine, L, dt + 1);
+                    s0 = v_scales<D>(mine, L, dt + 1, 0);
+                    s1 = v_scales<D>(mine, L, dt + 1, 1);
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[n][0], o[n][dt], 0, 0, 0);
+                    o[n][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[n][1], o[n][dt], 0, 0, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            i = next;
+        };
+        for (; i < stop; i += 4 * kAhead) {
+            step(i, k[0], v[0], entries[0]);
+            if (kAhead > 1 && i + 4 < stop) step(i + 4, k[kAhead - 1], v[kAhead - 1], entries[kAhead - 1]);
         }
 
         // ---- join the four waves
