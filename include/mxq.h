@@ -442,8 +442,8 @@ mxq_status mxq_add_rmsnorm_quant_fp8(const uint16_t* x_bf16, int64_t ldx, const 
  * arrays are all expressed by them.
  * Requirements: head_dim 64 or 128; page_size a power of two, 16 .. 2^20 (else
  * MXQ_ERR_UNSUPPORTED); strides >= 0, code strides multiples of 16, scale strides of
- * head_dim/16 (else MXQ_ERR_MISALIGNED); codes 16-byte, scales 8-byte, globals 4-byte
- * aligned; rows of different (page, head, row) do not overlap.
+ * head_dim/16 (else MXQ_ERR_MISALIGNED), token strides at most 2^24 (else
+ * MXQ_ERR_UNSUPPORTED); codes 16-byte, scales 8-byte, globals 4-byte aligned; rows of different (page, head, row) do not overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {
     uint8_t* k_codes;

@@ -41,22 +41,28 @@ struct Lane {
 };
 
 // ---------------------------------------------------------------- a tile's loads
-// The table entries of a tile's four groups of 16 tokens, group lane % 4 in each lane
-// (past the sequence the last token's page: nothing of such tokens is used).
+// A tile's 64 tokens lie in G groups that share a page each: one where pages hold 64 tokens
+// or more, else four of 16 (a page of 32 holds two).  The group addresses are uniform; with
+// one group the scalar unit forms a quarter of them (173 -> 70 scalar instructions a tile).
+//
+// The table entries of a tile's groups, group lane % 4 in each lane (past the sequence the
+// last token's page: nothing of such tokens is used).
 __device__ __forceinline__ int32_t page_entries(const AttnArgs& a, const int32_t* table, int len, int tile, const Lane& L) {
     return table[min(tile * 64 + 16 * (L.lane & 3), len - 1) >> a.c.page_shift];
 }
 
-// Where the four groups lie (uniform; page 0 for a page that may not be read).
+// Where the groups lie (page 0 for a page that may not be read).
+template <int G>
 struct Place {
-    int64_t codes[4], scales[4];
+    int64_t codes[G], scales[G];
     uint32_t bad;                     // bit t: group t's page may not be read
 };
-__device__ __forceinline__ Place place(const AttnArgs& a, int32_t entries, int tile) {
-    Place p;
+template <int G>
+__device__ __forceinline__ Place<G> place(const AttnArgs& a, int32_t entries, int tile) {
+    Place<G> p;
     p.bad = 0;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < G; ++t) {
         const int32_t e = __builtin_amdgcn_readlane(entries, t);
         const bool ok = (uint32_t)e < (uint32_t)a.c.num_pages;
         p.bad |= ok ? 0u : 1u << t;
@@ -73,13 +79,28 @@ struct Base {
     const uint8_t *kc, *ks, *vc, *vs;
 };
 
-// This lane's bytes inside a group's 16 rows.
+// This lane's bytes inside a group: K's codes D / 4 g .. of token col (of the tile's 16 t +
+// col with one group) and their scales; V's 16 codes-bytes of token lane / 4 (D = 64: lane /
+// 2) and load j's; the scales of token `lane`.
+template <int D, int G>
 struct Offsets {
-    uint32_t k, ks, v, vs;
+    uint32_t k[5 - G], ks[5 - G], v[G == 1 ? D / 32 : 1], vs;
+    __device__ __forceinline__ Offsets(const AttnArgs& a, const Lane& L) {
+        const uint32_t cs = (uint32_t)a.c.cs_tok, ss = (uint32_t)a.c.ss_tok;
+#pragma unroll
+        for (int t = 0; t < 5 - G; ++t) {
+            k[t] = (uint32_t)(16 * t + L.col) * cs + L.g * (D / 8);
+            ks[t] = (uint32_t)(16 * t + L.col) * ss + L.g * (D / 64);
+        }
+        const int tok = D == 128 ? L.lane >> 2 : (L.lane >> 1) & (G == 1 ? 31 : 15);
+#pragma unroll
+        for (int j = 0; j < (G == 1 ? D / 32 : 1); ++j)
+            v[j] = (uint32_t)((D == 128 ? 16 : 32) * j + tok) * cs + 16 * (L.lane & (D == 128 ? 3 : 1));
+        vs = (uint32_t)(G == 1 ? L.lane : L.col) * ss;
+    }
 };
 
-// K: codes D / 4 g .. of token 16 t + col, and their scales.  (Named members: an array
-// indexed in the score loop would end up in scratch.)
+// (Named members: an array indexed in the score loop would end up in scratch.)
 template <int D>
 struct KRegs {
     KWords<D> w0, w1, w2, w3;
@@ -90,47 +111,48 @@ __device__ __forceinline__ uint32_t k_scales(const uint8_t* p, uint32_t off) {
     if constexpr (D == 128) return *reinterpret_cast<const uint16_t*>(p + off);
     return p[off];
 }
-template <int D>
-__device__ __forceinline__ void load_k(const Base& a, const Place& p, const Offsets& o, KRegs<D>& r) {
-    r.w0 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[0] + o.k);
-    r.w1 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[1] + o.k);
-    r.w2 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[2] + o.k);
-    r.w3 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[3] + o.k);
-    // a page that may not be read: NaN scales, so that rows that see its tokens are NaN
-    constexpr uint32_t kNan = D == 128 ? 0x7F7Fu : 0x7Fu;
-    r.s0 = p.bad & 1 ? kNan : k_scales<D>(a.ks + p.scales[0], o.ks);
-    r.s1 = p.bad & 2 ? kNan : k_scales<D>(a.ks + p.scales[1], o.ks);
-    r.s2 = p.bad & 4 ? kNan : k_scales<D>(a.ks + p.scales[2], o.ks);
-    r.s3 = p.bad & 8 ? kNan : k_scales<D>(a.ks + p.scales[3], o.ks);
+template <int D, int G>
+__device__ __forceinline__ void load_k(const Base& a, const Place<G>& p, const Offsets<D, G>& o, KRegs<D>& r) {
+    // (which group and which offset: one of the two is always the first)
+    constexpr bool kOne = G == 1;
+    r.w0 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[0] + o.k[0]);
+    r.w1 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[kOne ? 0 : 1] + o.k[kOne ? 1 : 0]);
+    r.w2 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[kOne ? 0 : 2] + o.k[kOne ? 2 : 0]);
+    r.w3 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[kOne ? 0 : 3] + o.k[kOne ? 3 : 0]);
+    r.s0 = k_scales<D>(a.ks + p.scales[0], o.ks[0]);
+    r.s1 = k_scales<D>(a.ks + p.scales[kOne ? 0 : 1], o.ks[kOne ? 1 : 0]);
+    r.s2 = k_scales<D>(a.ks + p.scales[kOne ? 0 : 2], o.ks[kOne ? 2 : 0]);
+    r.s3 = k_scales<D>(a.ks + p.scales[kOne ? 0 : 3], o.ks[kOne ? 3 : 0]);
 }
 
-// V: 16 codes-bytes of a token (D = 128: token 16 j + lane / 4 in load j; D = 64: token
-// 32 j + lane / 2) and the scales of token `lane`.
 template <int D>
 struct VRegs {
     u32x4v w[D / 32];
     uint32_t s[D / 64];
-    bool ok;                          // the token's page may be read
 };
-template <int D>
-__device__ __forceinline__ void load_v(const Base& a, const Place& p, const Offsets& o, const Lane& L, VRegs<D>& r) {
-    if constexpr (D == 128) {
+template <int D, int G>
+__device__ __forceinline__ void load_v(const Base& a, const Place<G>& p, const Offsets<D, G>& o, const Lane& L, VRegs<D>& r) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + p.codes[j] + o.v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + (L.lane < 32 ? p.codes[2 * j] : p.codes[2 * j + 1]) + o.v);
+    for (int j = 0; j < D / 32; ++j) {
+        if constexpr (G == 1)
+            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + p.codes[0] + o.v[j]);
+        else if constexpr (D == 128)
+            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + p.codes[j] + o.v[0]);
+        else
+            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + (L.lane < 32 ? p.codes[2 * j] : p.codes[2 * j + 1]) + o.v[0]);
     }
-    const int64_t lo = L.g & 1 ? p.scales[1] : p.scales[0], hi = L.g & 1 ? p.scales[3] : p.scales[2];
-    const uint8_t* vs = a.vs + (L.g & 2 ? hi : lo) + o.vs;
+    int64_t s = p.scales[0];
+    if constexpr (G == 4) {
+        const int64_t lo = L.g & 1 ? p.scales[1] : p.scales[0], hi = L.g & 1 ? p.scales[3] : p.scales[2];
+        s = L.g & 2 ? hi : lo;
+    }
+    const uint8_t* vs = a.vs + s + o.vs;
     if constexpr (D == 128) {
         const u32x2v w = *reinterpret_cast<const u32x2v*>(vs);
         r.s[0] = w.x, r.s[1] = w.y;
     } else {
         r.s[0] = *reinterpret_cast<const uint32_t*>(vs);
     }
-    r.ok = !((p.bad >> L.g) & 1);
 }
 
 // ---------------------------------------------------------------- LDS of one wave
@@ -200,9 +222,8 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 
 }  // namespace
 
-template <int D, int NT>
+template <int D, int NT, int G>
 __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
-    constexpr int kAhead = 1;
     constexpr int kWave = WaveLds<D>::kBytes;
     constexpr int kJoin = (D / 16) * 64 * 16;               // a wave's outputs of one column tile
     constexpr int kLds = 4 * kWave > 4 * kJoin ? 4 * kWave : 4 * kJoin;
@@ -271,12 +292,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
         before = found_before;
     }
 
-    Offsets off;
-    off.k = (uint32_t)(L.col * a.c.cs_tok + L.g * (D / 8));
-    off.ks = (uint32_t)(L.col * a.c.ss_tok + L.g * (D / 64));
-    off.v = D == 128 ? (uint32_t)((L.lane >> 2) * a.c.cs_tok + 16 * (L.lane & 3))
-                     : (uint32_t)(((L.lane >> 1) & 15) * a.c.cs_tok + 16 * (L.lane & 1));
-    off.vs = (uint32_t)(L.col * a.c.ss_tok);
+    const Offsets<D, G> off(a, L);
     uint8_t* const mine = lds + wave * kWave;
 
     // ---- segment by segment: the part of one unit inside the stretch
@@ -301,27 +317,23 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
         const Base head{a.c.kc + kvh * a.c.cs_head, a.c.ks + kvh * a.c.ss_head, a.c.vc + kvh * a.c.cs_head,
                         a.c.vs + kvh * a.c.ss_head};
 
-        // Loads run kAhead rounds ahead of the tile that uses them (V's registers are free
-        // once it is in LDS, K's after the scores), page table entries one round further.
+        // Loads run one round ahead of the tile that uses them (V's registers are free once
+        // it is in LDS, K's after the scores), page table entries two.
         const int32_t* const table = a.table + (int64_t)b * a.ld_table;
-        KRegs<D> k[kAhead];
-        VRegs<D> v[kAhead];
-        int32_t entries[kAhead] = {};
+        KRegs<D> k;
+        VRegs<D> v;
+        int32_t entries = 0;
+        uint32_t bad = 0;                                   // groups of the loaded tile that may not be read
         int i = first + wave;
         const auto tile_of = [&](int j) { return span.tile(min(j, stop - 1)); };
         const auto entries_of = [&](int j) { return page_entries(a, table, seq.len, tile_of(j), L); };
         if (i < stop) {
-            int32_t e[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) e[j] = entries_of(i + 4 * j);
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) entries[j] = entries_of(i + 4 * (kAhead + j));
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const Place where = place(a, e[j], tile_of(i + 4 * j));
-                load_v<D>(head, where, off, L, v[j]);
-                load_k<D>(head, where, off, k[j]);
-            }
+            const int32_t e = entries_of(i);
+            entries = entries_of(i + 4);
+            const Place<G> where = place<G>(a, e, span.tile(i));
+            load_v<D, G>(head, where, off, L, v);
+            load_k<D, G>(head, where, off, k);
+            bad = where.bad;
         }
         const float kg = a.c.kg[kvh], vg = a.c.vg[kvh];
 
@@ -365,11 +377,12 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             for (int dt = 0; dt < D / 16; ++dt) o[n][dt] = f32x4{0, 0, 0, 0};
         }
 
-        const auto step = [&](int i, KRegs<D>& k, VRegs<D>& v, int32_t& entries) {
+        for (; i < stop; i += 4) {
             const int t0 = span.tile(i) * 64;
             // V and its scales to LDS; tokens past the sequence or of unreadable pages get
             // zero scales, so whatever lies there stays out
-            const bool valid = v.ok && t0 + L.lane < seq.len;
+            const uint32_t unread = bad;
+            const bool valid = !((unread >> (G == 1 ? 0 : L.g)) & 1) && t0 + L.lane < seq.len;
             bool nan_here = false;
 #pragma unroll
             for (int w = 0; w < D / 64; ++w) nan_here |= has_nan_scale(v.s[w]);
@@ -395,15 +408,17 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             stage_scales<D>(mine, v.s, valid, L);
             // (past the stretch the last tile again: a branch around a load would make every
             // later wait for loads a wait for all of them)
-            const Place where = place(a, entries, tile_of(i + 4 * kAhead));
-            load_v<D>(head, where, off, L, v);
-            entries = entries_of(i + 8 * kAhead);
+            const Place<G> where = place<G>(a, entries, tile_of(i + 4));
+            load_v<D, G>(head, where, off, L, v);
+            entries = entries_of(i + 8);
+            bad = where.bad;
 
             // scores of 64 tokens
             f32x4 x[NT][4];
             const auto score = [&](int t, KWords<D> w, uint32_t scales) {
+                // a page that may not be read: NaN scales, so that rows that see its tokens are NaN
                 f16x8 kk[D / 32];
-                dequant_row<D>(w, scales, kk);
+                dequant_row<D>(w, (unread >> (G == 1 ? 0 : t)) & 1 ? (D == 128 ? 0x7F7Fu : 0x7Fu) : scales, kk);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     x[n][t] = f32x4{0, 0, 0, 0};
@@ -420,7 +435,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             __builtin_amdgcn_sched_barrier(0);
             score(3, k.w3, k.s3);
             __builtin_amdgcn_sched_barrier(0);
-            load_k<D>(head, where, off, k);
+            load_k<D, G>(head, where, off, k);
 
             // masks only where an edge crosses the tile (uniform)
             if (t0 + 63 > span.p_lo || (a.window && t0 <= (int64_t)span.p_hi - a.window)) {
@@ -456,10 +471,6 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-        };
-        for (; i < stop; i += 4 * kAhead) {
-            step(i, k[0], v[0], entries[0]);
-            if (kAhead > 1 && i + 4 < stop) step(i + 4, k[kAhead - 1], v[kAhead - 1], entries[kAhead - 1]);
         }
 
         // ---- join the four waves
@@ -627,18 +638,25 @@ __global__ __launch_bounds__(256) void k_attention_join_splits(const AttnArgs a)
     join_row<D, 4>(a, seq, kvh, r0 + r, used, at, at + a.tile_rows, a.tile_rows);
 }
 
-hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
+template <int D, int NT>
+static void launch_rows(const AttnArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)a.splits);
+    if (a.c.page_shift >= 6)
+        hipLaunchKernelGGL((k_attention_rows<D, NT, 1>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_attention_rows<D, NT, 4>), grid, dim3(256), 0, stream, a);
+}
+hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
     if (a.c.head_dim == 128) {
         if (a.tile_rows == 16)
-            hipLaunchKernelGGL((k_attention_rows<128, 1>), grid, dim3(256), 0, stream, a);
+            launch_rows<128, 1>(a, stream);
         else
-            hipLaunchKernelGGL((k_attention_rows<128, 2>), grid, dim3(256), 0, stream, a);
+            launch_rows<128, 2>(a, stream);
     } else {
         if (a.tile_rows == 16)
-            hipLaunchKernelGGL((k_attention_rows<64, 1>), grid, dim3(256), 0, stream, a);
+            launch_rows<64, 1>(a, stream);
         else
-            hipLaunchKernelGGL((k_attention_rows<64, 2>), grid, dim3(256), 0, stream, a);
+            launch_rows<64, 2>(a, stream);
     }
     return hipGetLastError();
 }

@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxGridThreads = 0xFFFFFFFFll;    // 1-D grids only; threads per launch < 2^32
 constexpr int64_t kMaxRows = (1ll << 31) - 128;
 constexpr int64_t kMaxElems = 1ll << 40;
+constexpr int64_t kMaxTokenStride = 1ll << 24;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -57,6 +58,8 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
         if (cs[i] < 0 || ss[i] < 0) return MXQ_ERR_INVALID_ARGUMENT;
         if (cs[i] % 16 != 0 || ss[i] % (c->head_dim / 16) != 0) return MXQ_ERR_MISALIGNED;
     }
+    // (the kernels address the rows of a 64-token tile with 32-bit offsets)
+    if (cs[2] > kMaxTokenStride || ss[2] > kMaxTokenStride) return MXQ_ERR_UNSUPPORTED;
     if (cs[2] < c->head_dim / 2 || ss[2] < c->head_dim / 16) return MXQ_ERR_INVALID_ARGUMENT;
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 8) || !aligned(c->v_scales, 8) ||
         !aligned(c->k_global, 4) || !aligned(c->v_global, 4))

@@ -79,7 +79,7 @@ BAD_CACHES = [
     (dict(page=1 << 21), UNSUPPORTED), (dict(c=(2048, 1024, 72)), MISALIGNED), (dict(s=(256, 128, 12)), MISALIGNED),
     (dict(c=(2048, -1024, 64)), INVALID), (dict(c=(2048, 1024, 32)), INVALID), (dict(s=(256, 128, 0)), INVALID),
     (dict(kc=A + 8), MISALIGNED), (dict(vs=A + 4), MISALIGNED), (dict(vg=A + 2), MISALIGNED),
-    (dict(c=(1 << 39, 1024, 64)), UNSUPPORTED), (dict(s=(1 << 60, 1 << 60, 8)), UNSUPPORTED),
+    (dict(c=(1 << 39, 1024, 64)), UNSUPPORTED), (dict(c=(1 << 29, 1 << 29, (1 << 24) + 16)), UNSUPPORTED), (dict(s=(1 << 60, 1 << 60, 8)), UNSUPPORTED),
 ]
 
 
