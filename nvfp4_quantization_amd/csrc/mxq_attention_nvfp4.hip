@@ -100,6 +100,11 @@ struct Offsets {
     }
 };
 
+// The cache's codes are read once by one work-group: loads that pass them through the L2
+// without keeping them ("non-temporal") take 107 us instead of 119 for 604 MB.
+template <typename T>
+__device__ __forceinline__ T stream(const uint8_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const T*>(p)); }
+
 // (Named members: an array indexed in the score loop would end up in scratch.)
 template <int D>
 struct KRegs {
@@ -115,10 +120,10 @@ template <int D, int G>
 __device__ __forceinline__ void load_k(const Base& a, const Place<G>& p, const Offsets<D, G>& o, KRegs<D>& r) {
     // (which group and which offset: one of the two is always the first)
     constexpr bool kOne = G == 1;
-    r.w0 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[0] + o.k[0]);
-    r.w1 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[kOne ? 0 : 1] + o.k[kOne ? 1 : 0]);
-    r.w2 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[kOne ? 0 : 2] + o.k[kOne ? 2 : 0]);
-    r.w3 = *reinterpret_cast<const KWords<D>*>(a.kc + p.codes[kOne ? 0 : 3] + o.k[kOne ? 3 : 0]);
+    r.w0 = stream<KWords<D>>(a.kc + p.codes[0] + o.k[0]);
+    r.w1 = stream<KWords<D>>(a.kc + p.codes[kOne ? 0 : 1] + o.k[kOne ? 1 : 0]);
+    r.w2 = stream<KWords<D>>(a.kc + p.codes[kOne ? 0 : 2] + o.k[kOne ? 2 : 0]);
+    r.w3 = stream<KWords<D>>(a.kc + p.codes[kOne ? 0 : 3] + o.k[kOne ? 3 : 0]);
     r.s0 = k_scales<D>(a.ks + p.scales[0], o.ks[0]);
     r.s1 = k_scales<D>(a.ks + p.scales[kOne ? 0 : 1], o.ks[kOne ? 1 : 0]);
     r.s2 = k_scales<D>(a.ks + p.scales[kOne ? 0 : 2], o.ks[kOne ? 2 : 0]);
@@ -135,11 +140,11 @@ __device__ __forceinline__ void load_v(const Base& a, const Place<G>& p, const O
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
         if constexpr (G == 1)
-            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + p.codes[0] + o.v[j]);
+            r.w[j] = stream<u32x4v>(a.vc + p.codes[0] + o.v[j]);
         else if constexpr (D == 128)
-            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + p.codes[j] + o.v[0]);
+            r.w[j] = stream<u32x4v>(a.vc + p.codes[j] + o.v[0]);
         else
-            r.w[j] = *reinterpret_cast<const u32x4v*>(a.vc + (L.lane < 32 ? p.codes[2 * j] : p.codes[2 * j + 1]) + o.v[0]);
+            r.w[j] = stream<u32x4v>(a.vc + (L.lane < 32 ? p.codes[2 * j] : p.codes[2 * j + 1]) + o.v[0]);
     }
     int64_t s = p.scales[0];
     if constexpr (G == 4) {
