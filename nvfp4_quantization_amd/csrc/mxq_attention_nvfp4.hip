@@ -462,11 +462,9 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             if (t0 + 63 > span.p_lo || (a.window && t0 <= (int64_t)span.p_hi - a.window)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[n][t][e] = sees(a, pos[n], t0 + 16 * t + 4 * L.g + e) ? x[n][t][e] : -__builtin_inff();
+                    each_seen<16>(a, pos[n], t0 + 4 * L.g, [](int e) { return 16 * (e >> 2) + (e & 3); }, [&](int e, bool seen) {
+                        x[n][e >> 2][e & 3] = seen ? x[n][e >> 2][e & 3] : -__builtin_inff();
+                    });
             }
             f16x8 p[NT][2];
 #pragma unroll

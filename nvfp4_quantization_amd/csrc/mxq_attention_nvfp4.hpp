@@ -65,6 +65,18 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int t) {
     return t <= p && (!a.window || t > p - a.window || t < a.sinks);
 }
 
+// keep(e, seen) for N of a lane's tokens, token t0 + at(e), for the query at position p: sees()
+// in vector instructions (unsigned: tokens ahead of the query wrap to far behind it).
+template <int N, typename At, typename Keep>
+__device__ __forceinline__ void each_seen(const AttnArgs& a, int p, int t0, At&& at, Keep&& keep) {
+    constexpr uint32_t kAll = 0x80000000u;
+    const uint32_t window = a.window ? (uint32_t)a.window : kAll;
+    int ago = p - t0, first = a.sinks - t0;
+    asm("" : "+v"(ago), "+v"(first));                        // (or p - at(e) is held for every e across the tiles)
+#pragma unroll
+    for (int e = 0; e < N; ++e) keep(e, (uint32_t)(ago - at(e)) < (at(e) < first ? kAll : window));
+}
+
 // ---------------------------------------------------------------- FP16 operands
 // 8 E2M1 codes of a dword.
 __device__ __forceinline__ f16x8 e2m1_8(uint32_t w) {

@@ -165,30 +165,15 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     if (split >= used) return;
     const int first = split * a.chunk, last = split == used - 1 ? span.n : first + a.chunk;
 
-    // Q as the second operand of S^T = K Q^T: lane (col, h) holds elements 16 c + 8 h .. + 7
+    // Q as the second operand of S^T = K Q^T: lane (col, h) holds elements 16 c + 8 h .. + 7 of
+    // its row (the first row again past the last)
     f16x8 q[D / 16];
     const int row = wave * kWaveRows + col;
     const bool live = row < rows;
-    const int qi = live ? (int)((r0 + row) / a.group) : 0;
-    const int head = kvh * a.group + (live ? (int)(r0 + row - (int64_t)qi * a.group) : 0);
+    const int qi = (int)((r0 + (live ? row : 0)) / a.group);
+    const int head = kvh * a.group + (int)(r0 + (live ? row : 0) - (int64_t)qi * a.group);
     const int pos = live ? max(seq.len - seq.nq + qi, -1) : -1;
-    float factor;
-    {
-        const uint16_t* src = a.q + (int64_t)(seq.start + qi) * a.ld_q + (int64_t)head * D + h * 8;
-        u32x4v w[D / 16];
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            w[c] = live ? *reinterpret_cast<const u32x4v*>(src + 16 * c) : u32x4v{0, 0, 0, 0};
-            top = absmax_pk(absmax_pk(absmax_pk(absmax_pk(top, w[c].x), w[c].y), w[c].z), w[c].w);
-        }
-        top = fold_pk(top);
-        top = max(top, shfl_xor_u32(top, 32));
-        const float up = q_power(top, factor);
-        factor *= a.scale_log2 * a.c.kg[kvh];
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) q[c] = q_operand(w[c], up);
-    }
+    float factor = 0.0f;
 
     f32x16 o[D / 32];
     float m = kFloor, l = 0.0f;
@@ -234,14 +219,33 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
         return __builtin_bit_cast(f16x8, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
 
+    // The queries are asked for ahead of the first tile, which has to wait for its page table
+    // entry: loads come back in order, and so they are made ready while the tile is on its way.
     Part<D> kr, vr;
     int32_t entry = 0;
     if (first < last) {
-        Spot at = spot_of(entry_of(first), first);
+        const int32_t e0 = entry_of(first), e1 = entry_of(first + 1);
+        entry = entry_of(first + 2);
+        const uint16_t* src = a.q + (int64_t)(seq.start + qi) * a.ld_q + (int64_t)head * D + h * 8;
+        u32x4v w[D / 16];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) w[c] = *reinterpret_cast<const u32x4v*>(src + 16 * c);
+        const float kg = a.c.kg[kvh];
+        __builtin_amdgcn_sched_barrier(0);
+        Spot at = spot_of(e0, first);
         load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
         load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
-        const int32_t e1 = entry_of(first + 1);
-        entry = entry_of(first + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+            top = absmax_pk(absmax_pk(absmax_pk(absmax_pk(top, w[c].x), w[c].y), w[c].z), w[c].w);
+        top = fold_pk(top);
+        top = max(top, shfl_xor_u32(top, 32));
+        const float up = q_power(top, factor);
+        factor *= a.scale_log2 * kg;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) q[c] = q_operand(w[c], up);
         store_k<D>(k0, kr, my_tok, part);
         store_v<D>(v0, vr, my_tok, valid(first), part);
         at = spot_of(e1, first + 1);
@@ -290,13 +294,9 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             entry = entry_of(i + 3);
         }
         // masks only where an edge crosses the tile for this wave's rows
-        if (t0 + 63 > w_lo || (a.window && t0 <= (int64_t)w_hi - a.window)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int tok = t0 + 8 * (e >> 2) + 4 * h + (e & 3);
-                x[e >> 4][e & 15] = sees(a, pos, tok) ? x[e >> 4][e & 15] : -__builtin_inff();
-            }
-        }
+        if (t0 + 63 > w_lo || (a.window && t0 <= (int64_t)w_hi - a.window))
+            each_seen<32>(a, pos, t0 + 4 * h, [](int e) { return 8 * (e >> 2) + (e & 3); },
+                          [&](int e, bool seen) { x[e >> 4][e & 15] = seen ? x[e >> 4][e & 15] : -__builtin_inff(); });
         if (noted.x | noted.y | noted.z | noted.w) {   // (rare) note the NaN V blocks this lane sees
 #pragma unroll 1
             for (int e = 0; e < 32; ++e) {
