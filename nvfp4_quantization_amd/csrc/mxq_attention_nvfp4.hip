@@ -213,7 +213,7 @@ __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[
 }
 
 // ---------------------------------------------------------------- the line of tiles
-constexpr int kLineSeqs = 1024;       // sequences of a call whose units share the line
+constexpr int kLineSeqs = 1024;       // sequences of a call whose units share the line: fewer
 // A unit's length on the line: its tiles and kUnitCost more for what a unit costs beside them
 // (queries, the first loads' latency, the join of the waves: about one round of four
 // tiles), so that stretches of many short units are not longer in time.  0 without queries.

@@ -76,19 +76,34 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
 
 // How the attention call splits its work.  A unit is (sequence, row tile, cached head).
 //   rows form    up to 32 query rows per cached head: a decoding step or a draft.  One row
-//                tile of 16 or 32.  With kManyUnits units or more, or where no unit has
-//                more than kShortTiles tiles, a work-group takes a unit; else at most
-//                kRowsGroups work-groups (what the chip holds at once) share the line of
-//                all units' 64-token tiles evenly.
+//                tile of 16 or 32.  A work-group takes a unit, or, where that leaves too
+//                much of the chip idle too long (pays_line), kRowsGroups work-groups (what
+//                the chip holds at once) share the line of all units' tiles evenly.
 //   prompt form  more rows, 128 a unit, whose waves share the dequantized tiles.  A unit's
 //                tiles are cut into chunks only where there are fewer units than
 //                kPromptGroups work-groups (two fit a CU).
 constexpr int64_t kRowsGroups = 256 * 2;
-constexpr int64_t kManyUnits = 8 * kRowsGroups;
-constexpr int64_t kLineSeqs = 1024;            // sequences that one work-group lays out
-constexpr int64_t kShortTiles = 16;
+constexpr int64_t kLineUnits = 1024;           // the line's units, and so its sequences, are fewer
 constexpr int64_t kPromptGroups = 256 * 2;
 static_assert(kRowsGroups <= mxq::kMaxParts, "a unit may be cut by every work-group");
+
+// Whether the line is worth its join and its cut units, about 33 tiles of a CU's time (11 us).
+// With a work-group a unit the fullest CU has ceil(units / 256) units' tiles, with the line
+// every CU has units / 256; up to 256 units, where all start at once, sequences are taken to
+// fill three quarters of the longest.  Measured, line / unit in us (head_dim 128, batches of
+// equal lengths; of lengths from an eighth to the whole):
+//   units  tiles   equal          ragged            units  tiles   equal          ragged
+//      16     24   15.8 / 13.1    15.7 / 13.6         512     24   36.5 / 24.6    33.9 / 20.2
+//      16     48   16.3 / 20.8    15.9 / 20.8         512     96   88.0 / 76.4    57.2 / 58.4
+//      64     24   16.9 / 13.5    16.9 / 13.6         512    192  154.3 / 143.8  103.8 / 108.0
+//      64     48   19.1 / 20.9    18.0 / 21.2         768     96  124.4 / 113.1   85.9 / 87.2
+//     256     96   50.2 / 43.9    36.5 / 38.3        1024     96  150.8 / 145.7  108.2 / 101.7
+//     256    192   85.1 / 81.4    56.1 / 69.1        2048     48  159.8 / 153.0  117.9 / 106.5
+bool pays_line(int64_t units, int64_t tiles) {
+    if (units >= kLineUnits) return false;
+    const int64_t idle = units <= 256 ? 256 - units * 3 / 4 : (units + 255) / 256 * 256 - units;     // CUs
+    return tiles * idle > 33 * 256;
+}
 struct AttnPlan {
     int32_t tile_rows, row_tiles, splits, chunk;
     int64_t units;
@@ -115,7 +130,7 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
     int64_t parts = 0;
     p->ml_offset = p->desc_offset = p->bytes = 0;
     if (p->tile_rows < 128) {
-        const bool line = tiles > kShortTiles && p->units < kManyUnits && batch <= kLineSeqs;
+        const bool line = pays_line(p->units, tiles);
         const int64_t most = product_below(p->units, tiles, 4 * kRowsGroups) ? (p->units * tiles + 3) / 4 : kRowsGroups;
         p->splits = (int32_t)(!line ? p->units : most < kRowsGroups ? most : kRowsGroups);
         p->chunk = 0;
