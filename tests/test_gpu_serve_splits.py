@@ -1,0 +1,119 @@
+"""Attention over the paged NVFP4 cache: the ways the work is spread over the chip, against
+64 bits.  max_seq_len only sizes that split, so each case runs with a bound of one tile (a
+work-group per sequence and cached head) and with one far past its lengths (work-groups that
+share all tiles, cut units and their join)."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_quantization_amd as mxq
+from tests.gpu_util import announce, device
+from tests.test_gpu_serve import Case
+
+pytestmark = pytest.mark.gpu
+
+RNG = np.random.default_rng(77)
+SHORT = [int(n) for n in RNG.integers(0, 140, 300)]
+
+CASES = {
+    "rows first, pages of 64": dict(lens=[300, 64, 1], nq=[1, 1, 1], hq=8, hk=2, d=128, page=64, rows_first=True),
+    "rows first, pages of 128, drafts": dict(lens=[300, 129], nq=[5, 2], hq=8, hk=2, d=128, page=128, rows_first=True),
+    "rows first, d64": dict(lens=[300, 64, 700], nq=[1, 4, 3], hq=8, hk=2, d=64, page=64, rows_first=True),
+    "rows first, prompt": dict(lens=[200, 90], nq=[90, 90], hq=4, hk=2, d=64, page=64, rows_first=True),
+    "pages of 64, group 24": dict(lens=[700, 64, 65], nq=[1, 1, 1], hq=24, hk=1, d=128, page=64),
+    "pages of 128, d64, group 5 drafts": dict(lens=[513, 128, 4], nq=[5, 5, 4], hq=10, hk=2, d=64, page=128),
+    "pages of 64, d64": dict(lens=[64, 63, 500], nq=[1, 1, 1], hq=8, hk=1, d=64, page=64),
+    "pages of 32, group 17": dict(lens=[333, 32, 31], nq=[1, 1, 1], hq=17, hk=1, d=128, page=32),
+    "one long among short": dict(lens=SHORT[:100] + [9000] + SHORT[100:160], nq=[1] * 161, hq=2, hk=1, d=128, page=64),
+    "two long, drafts": dict(lens=[5000, 20, 7000, 1], nq=[3, 2, 3, 3], hq=8, hk=1, d=64, page=16),
+    "without queries between": dict(lens=SHORT, nq=[int(n % 3 != 1) for n in range(300)], hq=4, hk=2, d=64, page=16),
+    "first and last empty": dict(lens=[0, 0, 500, 0, 700, 0], nq=[1, 0, 1, 1, 1, 0], hq=8, hk=2, d=128, page=64),
+    "windows": dict(lens=[n * 9 for n in SHORT[:40]], nq=[1] * 40, hq=4, hk=2, d=128, page=16, window=200, sinks=4),
+    "sinks alone": dict(lens=[300, 80], nq=[1, 5], hq=4, hk=2, d=64, page=16, sinks=70),
+    "window past everything": dict(lens=[300, 80], nq=[2, 40], hq=4, hk=2, d=64, page=16, window=(1 << 31) - 1,
+                                   sinks=(1 << 31) - 1),
+    "sinks in the window's tile": dict(lens=[170, 140], nq=[1, 30], hq=4, hk=2, d=128, page=64, window=50, sinks=100),
+    "chunks in three parts": dict(lens=[520], nq=[256], hq=32, hk=16, d=64, page=64),
+    "chunks in many parts": dict(lens=[4000], nq=[9], hq=8, hk=2, d=128, page=16),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_both_splits(name):
+    dev = device()
+    c = Case(seed=len(name), **CASES[name])
+    for bound in (64, 1 << 22):
+        announce(f"splits {name} {bound}")
+        r = c.run(dev, max_seq_len=bound)()
+        torch.cuda.synchronize()
+        c.check(r)
+
+
+def test_more_units_than_the_line_takes():
+    dev = device()
+    announce("1100 sequences")
+    c = Case([n % 97 for n in range(1100)], [1] * 1100, 2, 1, 64, 16, seed=3)
+    r = c.run(dev, max_seq_len=1 << 22)()
+    torch.cuda.synchronize()
+    c.check(r)
+
+
+def test_two_streams_at_once():
+    """Two prepared calls, each with its own workspace, in flight together and in turns."""
+    dev = device()
+    cases = [Case([3000, 100], [1, 1], 8, 2, 128, 64, seed=1), Case([2500, 900, 10], [2, 1, 3], 8, 2, 64, 16, seed=2),
+             Case([1500], [30], 8, 2, 128, 64, seed=3)]
+    calls = [c.run(dev) for c in cases]
+    want = []
+    for call in calls:
+        r = call()
+        torch.cuda.synchronize()
+        want.append((r.out.clone(), r.lse.clone()))
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for call in calls:
+            call.out.out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for call, s in zip(calls, streams):
+                call(s)
+        torch.cuda.synchronize()
+        for call, (o, l) in zip(calls, want):
+            assert torch.equal(call.out.out, o) and torch.equal(call.out.lse, l)
+
+
+def test_cache_without_pages():
+    """No page can be read, so every sequence is empty: zeros, and a lse of -inf."""
+    dev = device()
+    for nq in (1, 40):
+        announce(f"no pages, {nq} queries")
+        cache = mxq.NVFP4KVCache.allocate(0, 64, 2, 128, 1.0, 1.0, device=dev)
+        q = torch.ones(nq, 8, 128, dtype=torch.bfloat16, device=dev)
+        r = mxq.mxq_attention_nvfp4(q, cache, torch.zeros(1, 9, dtype=torch.int32, device=dev),
+                                    torch.tensor([500], dtype=torch.int32, device=dev),
+                                    torch.tensor([0, nq], dtype=torch.int32, device=dev), nq, 5000, lse=True)
+        torch.cuda.synchronize()
+        assert not r.out.any() and bool(torch.isneginf(r.lse).all())
+
+
+def test_graph_of_cut_units():
+    """A captured call whose work-groups cut units, replayed while the lengths grow, with eager
+    calls of another workspace between."""
+    dev = device()
+    c = Case([3000, 40, 2000], [1, 1, 1], 8, 2, 128, 64, seed=5)
+    call, other = c.run(dev, poison=False, max_seq_len=4000), c.run(dev, poison=False, max_seq_len=4000)
+    lens, other_lens = call._tensors[4], other._tensors[4]
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in range(4):
+        for t in (lens, other_lens):
+            t.copy_(torch.tensor([2900 + 20 * i, 40 - i, 1000 + 300 * i], dtype=torch.int32))
+        r = other()
+        torch.cuda.synchronize()
+        call.out.out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(call.out.out, r.out) and torch.equal(call.out.lse, r.lse), f"replay {i}"
