@@ -244,7 +244,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
     __shared__ float2 join[4][NT * 16];
     // of the sequences on the line: length, first query row, queries, a unit's length on it
     __shared__ int4 seqs[kLineSeqs];
-    __shared__ uint32_t wave_length[4];
+    __shared__ int64_t wave_length[4];
     __shared__ int found;
     __shared__ int64_t found_before;
 
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
         end = at + n;
     } else {
         // four consecutive sequences a thread
-        uint32_t n[4], sum = 0;
+        uint32_t n[4], sum = 0;                             // (a unit is shorter than 2^26)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             n[j] = 0;
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             }
             sum += n[j];
         }
-        const uint32_t upto = wave_scan(sum);
+        const int64_t upto = wave_scan(sum & 0xFFFFu) + ((int64_t)wave_scan(sum >> 16) << 16);
         if (L.lane == 63) wave_length[wave] = upto;
         __syncthreads();
         int64_t mine = 0, line = 0;                         // before this thread's sequences; all
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
         }
         line *= a.c.kv_heads;
         // equal stretches of whole rounds of four waves
-        share = line >> 32 ? (line + gridDim.x - 1) / gridDim.x : (int64_t)(((uint32_t)line + gridDim.x - 1) / gridDim.x);
+        share = line >> 31 ? (line + gridDim.x - 1) / gridDim.x : (int64_t)(((uint32_t)line + gridDim.x - 1) / gridDim.x);
         share = max((share + 3) / 4 * 4, (int64_t)8);
         at = (int64_t)blockIdx.x * share;
         end = min(at + share, line);
