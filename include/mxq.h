@@ -443,7 +443,8 @@ mxq_status mxq_add_rmsnorm_quant_fp8(const uint16_t* x_bf16, int64_t ldx, const 
  * Requirements: head_dim 64 or 128; page_size a power of two, 16 .. 2^20 (else
  * MXQ_ERR_UNSUPPORTED); strides >= 0, code strides multiples of 16, scale strides of
  * head_dim/16 (else MXQ_ERR_MISALIGNED), token strides at most 2^24 (else
- * MXQ_ERR_UNSUPPORTED); codes 16-byte, scales 8-byte, globals 4-byte aligned; rows of different (page, head, row) do not overlap.
+ * MXQ_ERR_UNSUPPORTED); codes 16-byte, scales 8-byte, globals 4-byte aligned; rows of
+ * different (page, head, row) do not overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {
     uint8_t* k_codes;
@@ -547,7 +548,9 @@ mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_head
  * that share it must be ordered.
  * Requirements: q_heads a multiple of kv_heads; 1 <= batch <= 65535; ld_q, ld_out
  * multiples of 8 and at least q_heads * head_dim; q, out 16-byte aligned, the others
- * 4-byte; softmax_scale > 0 and finite; window, sinks >= 0; total_q * q_heads < 2^31.
+ * 4-byte; softmax_scale > 0 and finite; window, sinks >= 0; total_q * q_heads < 2^31;
+ * batch * kv_heads * ceil(max_q_len * q_heads / kv_heads / 128) < 2^24 (else
+ * MXQ_ERR_UNSUPPORTED).
  * total_q == 0 or max_q_len == 0 is a successful no-op.
  * ------------------------------------------------------------------------- */
 size_t mxq_attention_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,

@@ -261,9 +261,9 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
     if (!extent_ok(total_q, ld_q, width) || !extent_ok(total_q, ld_out, width) ||
         !extent_ok(batch, ld_table, table_pages) || table_pages > kMaxRows)
         return MXQ_ERR_UNSUPPORTED;
+    // (the join's grid needs no check: fewer than kLineUnits units, or kPromptGroups / 2 at most)
     AttnPlan p;
     if (!plan_attention(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len, max_seq_len, window, sinks, &p) ||
-        !product_below(p.units, 256ll * p.tile_rows, kMaxGridThreads) ||
         !product_below(p.tile_rows == 128 ? p.units * p.splits : p.splits, 256, kMaxGridThreads))
         return MXQ_ERR_UNSUPPORTED;
     if (p.bytes > 0) {

@@ -117,3 +117,31 @@ def test_graph_of_cut_units():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(call.out.out, r.out) and torch.equal(call.out.lse, r.lse), f"replay {i}"
+
+
+def test_one_prompt_in_a_wide_batch():
+    """One run of 8192 queries among single ones: most of the row tiles that the widths allow
+    for hold nothing (batch * row tiles * heads = 2^17 of them)."""
+    dev = device()
+    announce("wide batch")
+    rng = np.random.default_rng(6)
+    cache = mxq.NVFP4KVCache.allocate(8, 64, 8, 64, 1.0, 1.0, device=dev)
+    for t in (cache.k_codes, cache.v_codes):
+        t.copy_(torch.from_numpy(rng.integers(0, 256, t.shape, dtype=np.uint8)))
+    cache.k_scales.fill_(0x38)
+    cache.v_scales.fill_(0x38)
+    batch, run = 64, 8192
+    q = torch.from_numpy(rng.standard_normal((run + batch - 1, 32, 64), dtype=np.float32)).bfloat16().to(dev)
+    table = torch.arange(batch, dtype=torch.int32, device=dev)[:, None] % 8
+    lens = torch.full((batch,), 64, dtype=torch.int32, device=dev)
+    starts = torch.tensor([0] + [run + i for i in range(batch)], dtype=torch.int32, device=dev)
+    r = mxq.mxq_attention_nvfp4(q, cache, table, lens, starts, run, 64, lse=True)
+    alone = mxq.mxq_attention_nvfp4(q[run - 64:run], cache, table[:1], lens[:1],
+                                    torch.tensor([0, 64], dtype=torch.int32, device=dev), 64, 64, lse=True)
+    torch.cuda.synchronize()
+    assert not r.out[:run - 64].any() and bool(torch.isneginf(r.lse[:run - 64]).all())
+    assert torch.equal(r.out[run - 64:run], alone.out) and torch.equal(r.lse[run - 64:run], alone.lse)
+    singles = mxq.mxq_attention_nvfp4(q[run:], cache, table[1:], lens[1:],
+                                      torch.arange(batch, dtype=torch.int32, device=dev), 40, 64)
+    torch.cuda.synchronize()
+    assert torch.equal(r.out[run:], singles.out)
