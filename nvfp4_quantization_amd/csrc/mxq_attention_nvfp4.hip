@@ -380,7 +380,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
                 top = max(top, shfl_xor_u32(top, 16));
                 top = max(top, shfl_xor_u32(top, 32));
                 const float up = q_power(top, factor[n]);
-                factor[n] *= a.scale_log2 * kg;
+                factor[n] = score_factor(a, factor[n], kg);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) q[n][c] = q_operand(w[n][c], up);
             }

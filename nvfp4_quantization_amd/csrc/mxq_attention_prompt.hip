@@ -243,7 +243,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
         top = fold_pk(top);
         top = max(top, shfl_xor_u32(top, 32));
         const float up = q_power(top, factor);
-        factor *= a.scale_log2 * kg;
+        factor = score_factor(a, factor, kg);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) q[c] = q_operand(w[c], up);
         store_k<D>(k0, kr, my_tok, part);

@@ -145,3 +145,19 @@ def test_one_prompt_in_a_wide_batch():
                                       torch.arange(batch, dtype=torch.int32, device=dev), 40, 64)
     torch.cuda.synchronize()
     assert torch.equal(r.out[run:], singles.out)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("kg", [2.0 ** -126, 2.0 ** -60, 2.0 ** 100])
+def test_extreme_tensor_scales(nq, kg):
+    """Queries of zeros and of tiny and huge elements under K scales at the ends of their range:
+    masked scores stay masked, whatever the factor on them comes to."""
+    dev = device()
+    announce(f"extreme scales {nq} {kg}")
+    c = Case([100, 70], [nq, nq], 4, 2, 64, 16, seed=9)
+    c.kg[:] = kg
+    amp = torch.tensor([0.0, 2.0 ** -110, 1.0, 2.0 ** -60])[:, None]
+    c.q = (c.q.float() * amp * (2.0 ** -100 if kg > 1 else 1.0)).bfloat16()
+    r = c.run(dev)()
+    torch.cuda.synchronize()
+    c.check(r)
