@@ -188,9 +188,9 @@ template <int D>
 __device__ __forceinline__ void store_finished(const AttnArgs& a, const Seq& seq, int kvh, int64_t r, int d0, const f32x4& o,
                                                float m, float sum, float vg) {
     const int qi = (int)(r / a.group), head = kvh * a.group + (int)(r - (int64_t)qi * a.group);
-    const float inv = sum == 0.0f ? 0.0f : vg / sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;       // (vg / sum could leave the normal range)
     uint16_t* dst = a.out + (int64_t)(seq.start + qi) * a.ld_out + (int64_t)head * D + d0;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv * vg, o[1] * inv * vg), pack_bf16(o[2] * inv * vg, o[3] * inv * vg));
     if (a.lse && d0 == 0) a.lse[(int64_t)(seq.start + qi) * a.q_heads + head] = row_lse(m, sum);
 }
 // ... or as one part of it, in row `at` of the workspace.

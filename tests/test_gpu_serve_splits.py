@@ -161,3 +161,20 @@ def test_extreme_tensor_scales(nq, kg):
     r = c.run(dev)()
     torch.cuda.synchronize()
     c.check(r)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_smallest_v_scale(nq):
+    """V's tensor scale at the smallest normal number, many tokens: the output keeps its bits."""
+    dev = device()
+    announce(f"smallest v scale {nq}")
+    c = Case([190], [nq], 4, 2, 128, 16, seed=11)
+    plain = c.run(dev)()
+    ratio = (c.vg.astype(np.float64) / 2.0 ** -126)
+    c.vg[:] = 2.0 ** -126
+    r = c.run(dev)()
+    torch.cuda.synchronize()
+    scale = torch.from_numpy(np.repeat(ratio, 2))[None, :, None].to(dev)
+    want, got = plain.out.double(), r.out.double() * scale
+    # two roundings to BF16 (2^-8 each) and FP32 ones far below
+    assert bool(((got - want).abs() <= 2.0 ** -6.9 * want.abs() + 2.0 ** -30).all())
