@@ -24,12 +24,19 @@
 //    row) and read back transposed (ds_read_b64_tr_b4): a lane gets the 16 tokens of one
 //    output element.  Its scales are staged as FP16, a token pair per dword.
 //
-// Work split: with many units (sequence, cached head), a work-group each.  Otherwise the
-// 64-token tiles of all units lie on one line, and every work-group takes an equal stretch
-// of it, however ragged the lengths are: a unit inside one stretch is finished there, one
-// cut by a stretch's end leaves partial outputs (maximum, sum, unnormalized FP32 rows) in
-// the workspace for the join.  A work-group's four waves take every fourth tile of a unit
-// and join through LDS.
+// Work split: a work-group per unit (sequence, cached head), whose waves take its 64-token
+// tiles in turn and join through LDS; or, where that would leave much of the chip idle, the
+// tiles of all units on one line, of which every work-group takes an equal stretch, however
+// ragged the lengths are: a unit inside one stretch is finished there, one cut by a stretch's
+// end leaves partial outputs (maximum, sum, unnormalized FP32 rows) in the workspace for the
+// join.
+//
+// What bounds it: two sequences of 262144 tokens, 8 heads of 128 (604 MB of cache) take 102 us, 5
+// of them the join and about 6 the start (sequences, page table, first tile: three memory
+// latencies one after another), so the cache streams at 6.6 TB/s of the 7.0 that a plain read
+// reaches; 256 work-groups instead of 512 cost a third more, three a CU spill.  64 sequences
+// of up to 8192 tokens take 69 us (333 MB): there the longest units end last.  Few or short
+// sequences are latency: 1000 tokens 10.6 us, of which a call without work takes 8.4.
 #include "mxq_attention_nvfp4.hpp"
 
 namespace mxq {
@@ -213,6 +220,7 @@ __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[
 }
 
 // ---------------------------------------------------------------- the line of tiles
+constexpr int kWideUnits = 256;       // units of their own that get a CU, and eight waves, each
 constexpr int kLineSeqs = 1024;       // sequences of a call whose units share the line: fewer
 // A unit's length on the line: its tiles and kUnitCost more for what a unit costs beside them
 // (queries, the first loads' latency, the join of the waves: about one round of four
@@ -235,15 +243,15 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 
 }  // namespace
 
-template <int D, int NT, int G>
-__global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
+template <int D, int NT, int G, int W>
+__global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs a) {
     constexpr int kWave = WaveLds<D>::kBytes;
     constexpr int kJoin = (D / 16) * 64 * 16;               // a wave's outputs of one column tile
-    constexpr int kLds = 4 * kWave > 4 * kJoin ? 4 * kWave : 4 * kJoin;
+    constexpr int kLds = W * (kWave > kJoin ? kWave : kJoin);
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
-    __shared__ float2 join[4][NT * 16];
+    __shared__ float2 join[W][NT * 16];
     // of the sequences on the line: length, first query row, queries, a unit's length on it
-    __shared__ int4 seqs[kLineSeqs];
+    __shared__ int4 seqs[W == 4 ? kLineSeqs : 1];
     __shared__ int64_t wave_length[4];
     __shared__ int found;
     __shared__ int64_t found_before;
@@ -256,7 +264,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
     // ---- this work-group's stretch of the line [at, end), and the sequence it starts in
     int64_t at = 0, end, share = 0, before = 0;             // before: the line up to sequence b
     int b;
-    if (!a.desc) {                                          // a unit of its own
+    if (W == 8 || !a.desc) {                                // a unit of its own
         b = (int)(blockIdx.x / (unsigned)a.c.kv_heads);
         const Seq s = sequence(a, b);
         const int n = unit_length(a, s);
@@ -311,7 +319,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
 
     // ---- segment by segment: the part of one unit inside the stretch
     while (at < end) {
-        const int4 info = seqs[a.desc ? b : 0];
+        const int4 info = seqs[W == 4 && a.desc ? b : 0];
         const int n_unit = info.w;
         if (n_unit == 0) {                                  // (a sequence without queries)
             ++b;
@@ -352,7 +360,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             // table entries: loads come back in order, and so the queries are made ready while
             // the tile is on its way.
             const int32_t e = entries_of(i);
-            entries = entries_of(i + 4);
+            entries = entries_of(i + W);
             u32x4v w[NT][D / 32];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -398,7 +406,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             for (int dt = 0; dt < D / 16; ++dt) o[n][dt] = f32x4{0, 0, 0, 0};
         }
 
-        for (; i < stop; i += 4) {
+        for (; i < stop; i += W) {
             const int t0 = span.tile(i) * 64;
             // V and its scales to LDS; tokens past the sequence or of unreadable pages get
             // zero scales, so whatever lies there stays out
@@ -429,9 +437,9 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             stage_scales<D>(mine, v.s, valid, L);
             // (past the stretch the last tile again: a branch around a load would make every
             // later wait for loads a wait for all of them)
-            const Place<G> where = place<G>(a, entries, tile_of(i + 4));
+            const Place<G> where = place<G>(a, entries, tile_of(i + W));
             load_v<D, G>(head, where, off, L, v);
-            entries = entries_of(i + 8);
+            entries = entries_of(i + 2 * W);
             bad = where.bad;
 
             // scores of 64 tokens
@@ -500,7 +508,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
             }
         }
 
-        // ---- join the four waves
+        // ---- join the waves
         __syncthreads();                                    // the staging areas are free
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -530,22 +538,23 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(const AttnArgs a) {
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt) all[(wave * (D / 16) + dt) * 64 + L.lane] = o[n][dt];
             __syncthreads();
-            float top = kFloor, total = 0.0f, f[4];
+            float top = kFloor, total = 0.0f, f[W];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, join[w][n * 16 + L.col].x);
+            for (int w = 0; w < W; ++w) top = __builtin_fmaxf(top, join[w][n * 16 + L.col].x);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < W; ++w) {
                 f[w] = __builtin_amdgcn_exp2f(join[w][n * 16 + L.col].x - top);
                 total += join[w][n * 16 + L.col].y * f[w];
             }
             const int r = n * 16 + L.col;
             const bool live = r < rows;
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const int dt = wave * (D / 64) + j;
+            for (int j = 0; j < (D / 16 + W - 1) / W; ++j) {
+                const int dt = wave * (D / 16 >= W ? D / 16 / W : 1) + j;
+                if (dt >= D / 16) break;
                 f32x4 y = all[dt * 64 + L.lane] * f[0];
 #pragma unroll
-                for (int w = 1; w < 4; ++w) y += all[(w * (D / 16) + dt) * 64 + L.lane] * f[w];
+                for (int w = 1; w < W; ++w) y += all[(w * (D / 16) + dt) * 64 + L.lane] * f[w];
                 const int d0 = 16 * dt + 4 * L.g;
                 if (!live) continue;
                 if (whole)
@@ -682,13 +691,23 @@ __global__ __launch_bounds__(256) void k_attention_join_splits(const AttnArgs a)
     join_row<D, W>(a, seq, kvh, r0 + r, used, at, at + a.tile_rows, a.tile_rows);
 }
 
+// Units of their own get eight waves each while there is a CU for each: 256 units of 96
+// ragged tiles 34 us instead of 39, 8 units of 32 tiles 14.5 instead of 15.7; but 512 units of
+// 16 tiles 23 instead of 18.
+template <int D, int NT, int G>
+static void launch_rows_pages(const AttnArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)a.splits);
+    if (!a.desc && a.splits <= kWideUnits)
+        hipLaunchKernelGGL((k_attention_rows<D, NT, G, 8>), grid, dim3(512), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_attention_rows<D, NT, G, 4>), grid, dim3(256), 0, stream, a);
+}
 template <int D, int NT>
 static void launch_rows(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)a.splits);
     if (a.c.page_shift >= 6)
-        hipLaunchKernelGGL((k_attention_rows<D, NT, 1>), grid, dim3(256), 0, stream, a);
+        launch_rows_pages<D, NT, 1>(a, stream);
     else
-        hipLaunchKernelGGL((k_attention_rows<D, NT, 4>), grid, dim3(256), 0, stream, a);
+        launch_rows_pages<D, NT, 4>(a, stream);
 }
 hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
     if (a.c.head_dim == 128) {

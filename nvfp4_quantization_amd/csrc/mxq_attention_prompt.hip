@@ -22,6 +22,15 @@
 // read from LDS some products ahead.  The tile loop is unrolled over the two LDS
 // images, as separate arrays: with one array and a dynamic buffer index the compiler orders
 // every read after the other image's writes.
+//
+// What bounds it: a tile costs a wave 1024 cycles of matrix instructions and 1180 of vector
+// ones (half of it the 32 exponentials and their sums, a quarter the dequantization), of which
+// a matrix instruction hides all but its own issue, some 12 cycles; a CU's LDS is busy two
+// thirds of the time, an operand read from it feeding 32 rows.  512 queries of 32 heads of 128
+// over 65536 tokens take 568 us, 967 TFLOP/s (a plain 8192^3 product: 1109); two prompts of 4096
+// tokens 297 us, 925 TFLOP/s, and 368 us when the tiles of a sequence ran together, so that
+// the last sequence's longest rows started last.  64 rows a wave (half the operand reads, one
+// wave a SIMD) were slower.
 #include "mxq_attention_nvfp4.hpp"
 
 namespace mxq {
@@ -149,7 +158,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
     // later rows, which see more tiles, first for all sequences and heads: the last to start are
-    // the shortest (two prompts of 4096 tokens: see the measurements above)
+    // the shortest (two prompts of 4096 tokens 297 us against 368)
     const int split = (int)(blockIdx.x % (unsigned)a.splits);
     const int order = (int)(blockIdx.x / (unsigned)a.splits);
     const int bhs = a.batch * a.c.kv_heads;

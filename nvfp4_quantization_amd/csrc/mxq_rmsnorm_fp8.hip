@@ -8,6 +8,9 @@
 // The sum is carried in binary64: a square of a BF16 value has 16 significant bits, so
 // 53 bits hold the sums of a row's squares to 2^-38 or better in any order, and r (and
 // with it every code) does not depend on how the row is spread over the threads.
+//
+// What bounds it: memory.  16384 x 7168 with a residual (1.06 GB in and out) take 183 us, 5.8
+// TB/s; a row stays in registers between the sum and the encode.
 #include "mxq_device.hpp"
 #include "mxq_serve.hpp"
 

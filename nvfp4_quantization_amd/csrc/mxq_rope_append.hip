@@ -12,6 +12,10 @@
 // The cache rows are the row-wise NVFP4 encode of the grouped call (TransformerEngine
 // PR #2564: 1x16 E2M1 blocks with E4M3 scales) with a caller-supplied tensor scale per
 // head.
+//
+// What bounds it: memory.  8191 tokens of 32 + 8 + 8 heads of 128 with the values written
+// (211 MB) take 44 us, 4.8 TB/s, where a large copy reaches 5.3; a decoding step's 64
+// tokens take 4.2 us on the GPU, less than a call.
 #include "mxq_nvfp4_impl.hpp"
 #include "mxq_serve.hpp"
 

@@ -87,22 +87,23 @@ constexpr int64_t kLineUnits = 1024;           // the line's units, and so its s
 constexpr int64_t kPromptGroups = 256 * 2;
 static_assert(kRowsGroups <= mxq::kMaxParts, "a unit may be cut by every work-group");
 
-// Whether the line is worth its join and its cut units, about 33 tiles of a CU's time (11 us).
+// Whether the line is worth its join and its cut units, about 40 tiles of a CU's time (11 us).
 // With a work-group a unit the fullest CU has ceil(units / 256) units' tiles, with the line
 // every CU has units / 256; up to 256 units, where all start at once, sequences are taken to
 // fill three quarters of the longest.  Measured, line / unit in us (head_dim 128, batches of
 // equal lengths; of lengths from an eighth to the whole):
 //   units  tiles   equal          ragged            units  tiles   equal          ragged
-//      16     24   15.8 / 13.1    15.7 / 13.6         512     24   36.5 / 24.6    33.9 / 20.2
-//      16     48   16.3 / 20.8    15.9 / 20.8         512     96   88.0 / 76.4    57.2 / 58.4
-//      64     24   16.9 / 13.5    16.9 / 13.6         512    192  154.3 / 143.8  103.8 / 108.0
-//      64     48   19.1 / 20.9    18.0 / 21.2         768     96  124.4 / 113.1   85.9 / 87.2
-//     256     96   50.2 / 43.9    36.5 / 38.3        1024     96  150.8 / 145.7  108.2 / 101.7
-//     256    192   85.1 / 81.4    56.1 / 69.1        2048     48  159.8 / 153.0  117.9 / 106.5
+//       8     36   15.6 / 15.0    15.3 / 15.0         256    192   83.2 / 75.5    55.7 / 59.7
+//       8     56   15.3 / 20.2    15.9 / 20.2         384    192  120.1 / 127.2   77.6 / 92.0
+//      64     44   19.5 / 17.3    17.6 / 17.3         512     24   36.5 / 24.6    33.9 / 20.2
+//      64     72   21.3 / 24.8    21.0 / 24.4         512    192  154.3 / 143.8  103.8 / 108.0
+//     128     56   24.8 / 21.2    22.8 / 20.8         768     96  124.4 / 113.1   85.9 / 87.2
+//     128     72   27.7 / 25.2    24.9 / 24.8        1024     96  150.8 / 145.7  108.2 / 101.7
+//     256     96   49.8 / 41.7    36.8 / 34.0        2048     48  159.8 / 153.0  117.9 / 106.5
 bool pays_line(int64_t units, int64_t tiles) {
     if (units >= kLineUnits) return false;
     const int64_t idle = units <= 256 ? 256 - units * 3 / 4 : (units + 255) / 256 * 256 - units;     // CUs
-    return tiles * idle > 33 * 256;
+    return tiles * idle > 40 * 256;
 }
 struct AttnPlan {
     int32_t tile_rows, row_tiles, splits, chunk;
