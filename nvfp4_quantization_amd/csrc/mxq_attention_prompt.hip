@@ -358,9 +358,27 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    for (int i = first; i < last; i += 2) {
-        step(i, k0, k1, v0, v1);
-        if (i + 1 < last) step(i + 1, k1, k0, v1, v0);
+    // A wave without rows only stages its share of the next tile (64 ragged sequences of up to
+    // 8192 tokens with 40 rows a unit: 211 us against 257).
+    const auto stage = [&](int i, KImage<D>& kf, VImage<D>& vf) {
+        __syncthreads();
+        store_k<D>(kf, kr, my_tok, part);
+        store_v<D>(vf, vr, my_tok, valid(i + 1), part);
+        const Spot at = spot_of(entry, i + 2);
+        load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
+        load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
+        entry = entry_of(i + 3);
+    };
+    if (wave * kWaveRows < rows) {
+        for (int i = first; i < last; i += 2) {
+            step(i, k0, k1, v0, v1);
+            if (i + 1 < last) step(i + 1, k1, k0, v1, v0);
+        }
+    } else {
+        for (int i = first; i < last; i += 2) {
+            stage(i, k1, v1);
+            if (i + 1 < last) stage(i + 1, k0, v0);
+        }
     }
 
     l += shfl_xor_f32(l, 32);
