@@ -11,7 +11,7 @@ from typing import Optional
 
 import torch
 
-from . import _bf16_bits, _check, _ptr, _row_stride, _stream, lib
+from . import _bf16_bits, _check, _current_stream, _ptr, _row_stride, _stream, lib
 
 MXQ_ROPE_INTERLEAVED = 1
 
@@ -42,25 +42,37 @@ def _need(t: torch.Tensor, name: str, dtypes, device, dim: Optional[int] = None)
 
 
 _BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
+_ByRef = type(ctypes.byref(ctypes.c_int()))
 
 
 class _Prepared:
     """A call whose ctypes arguments are built once.  It runs on its tensors' device,
     whichever is current."""
 
-    def _launch(self, what: str, stream):
+    def _bind(self, what: str, device, tensors, *args):
+        """The C function (the library's own object keeps the declared types, this one takes
+        arguments that were converted to them here once), its arguments but the stream, and
+        the tensors behind them."""
+        types = getattr(lib(), what).argtypes
+        self._fn = lib()[what]
+        self._fn.restype = ctypes.c_int
+        assert len(args) == len(types) - 1
+        self._args = tuple(a if isinstance(a, (ctypes.c_void_p, _ByRef)) else t(a) for a, t in zip(args, types))
+        self._what, self._device, self._tensors = what, device, tensors
+
+    def _launch(self, stream):
         index = self._device.index
-        if index is None or index == torch.cuda.current_device():
-            self._run(what, stream)
+        if index == torch.cuda.current_device():
+            self._run(index, stream)
         else:
             with torch.cuda.device(index):
-                self._run(what, stream)
+                self._run(index, stream)
         return self.out
 
-    def _run(self, what, stream):
-        st = self._fn(*self._args, _stream(stream, *(self._tensors if stream is not None else ())))
+    def _run(self, index, stream):
+        st = self._fn(*self._args, _current_stream(index) if stream is None else _stream(stream, *self._tensors))
         if st:
-            _check(st, what)
+            _check(st, self._what)
 
 
 # ---------------------------------------------------------------------------- RMS norm -> FP8
@@ -102,15 +114,13 @@ class AddRMSNormFP8(_Prepared):
         y = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out_bf16 else None
         sr, sg = (1, m) if scale_transposed else (n // 128, 1)
         self.out = RMSNormFP8Result(q, scales, residual_out, y)
-        self._device = dev
-        self._tensors = (x, residual, residual_out, weight, y, q, scales)
-        self._fn = lib().mxq_add_rmsnorm_quant_fp8
-        self._args = (_ptr(x), _row_stride(x), _ptr(residual), _row_stride(residual), _ptr(residual_out),
-                      _row_stride(residual_out), _ptr(weight), float(eps), m, n, options, _ptr(y), n, _ptr(q), n,
-                      _ptr(scales), sr, sg)
+        self._bind("mxq_add_rmsnorm_quant_fp8", dev, (x, residual, residual_out, weight, y, q, scales),
+                   _ptr(x), _row_stride(x), _ptr(residual), _row_stride(residual), _ptr(residual_out),
+                   _row_stride(residual_out), _ptr(weight), float(eps), m, n, options, _ptr(y), n, _ptr(q), n,
+                   _ptr(scales), sr, sg)
 
     def __call__(self, stream=None) -> RMSNormFP8Result:
-        return self._launch("mxq_add_rmsnorm_quant_fp8", stream)
+        return self._launch(stream)
 
 
 def mxq_add_rmsnorm_quant_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -276,14 +286,13 @@ class RopeAppendNVFP4(_Prepared):
             raise ValueError(f"the rotary plan is on {rope.inv_freq.device}, expected {dev}")
         kv = [torch.empty((tokens, hk, d), dtype=torch.bfloat16, device=dev) if values else None for _ in range(2)]
         self.out = RopeAppendResult(q_out, *kv)
-        self._device, self._cache, self._rope = dev, cache, rope
-        self._tensors = (q, q_out, k, v, positions, slots, rope.inv_freq, *kv, *cache.tensors())
-        self._fn = lib().mxq_rope_append_nvfp4
-        self._args = (_ptr(q), ld_q, hq, _ptr(q_out), ld_qo, _ptr(k), ld_k, _ptr(v), ld_v, tokens, _ptr(positions),
-                      _ptr(slots), ctypes.byref(rope._c), ctypes.byref(cache._c), _ptr(kv[0]), _ptr(kv[1]))
+        self._cache, self._rope = cache, rope
+        self._bind("mxq_rope_append_nvfp4", dev, (q, q_out, k, v, positions, slots, rope.inv_freq, *kv, *cache.tensors()),
+                   _ptr(q), ld_q, hq, _ptr(q_out), ld_qo, _ptr(k), ld_k, _ptr(v), ld_v, tokens, _ptr(positions),
+                   _ptr(slots), ctypes.byref(rope._c), ctypes.byref(cache._c), _ptr(kv[0]), _ptr(kv[1]))
 
     def __call__(self, stream=None) -> RopeAppendResult:
-        return self._launch("mxq_rope_append_nvfp4", stream)
+        return self._launch(stream)
 
 
 def mxq_rope_append_nvfp4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -337,6 +346,9 @@ class AttentionNVFP4(_Prepared):
         if not seq_lens.is_contiguous() or not q_starts.is_contiguous() or (block_table.numel() > 0 and pages > 1
                                                                              and block_table.stride(1) != 1):
             raise ValueError("seq_lens, q_starts and the rows of block_table must be contiguous")
+        for name, value in (("window", window), ("sinks", sinks)):
+            if not 0 <= value < 1 << 31:
+                raise ValueError(f"{name} must be in [0, 2^31), got {value}")
         if max_seq_len is None:
             max_seq_len = pages * cache.page_size
         lse_t = torch.zeros((total, hq), dtype=torch.float32, device=dev) if lse else None
@@ -348,17 +360,17 @@ class AttentionNVFP4(_Prepared):
             _need(workspace, "workspace", (torch.uint8,), dev, 1)
         self.workspace = workspace
         self.out = AttentionResult(out, lse_t)
-        self._device, self._cache = dev, cache
-        self._tensors = (q, out, lse_t, block_table, seq_lens, q_starts, workspace, *cache.tensors())
-        self._fn = lib().mxq_attention_nvfp4
-        self._args = (_ptr(q), ld_q, hq, total, _ptr(out), ld_out, _ptr(lse_t), ctypes.byref(cache._c),
-                      _ptr(block_table), block_table.stride(0) if batch > 1 else pages, pages, _ptr(seq_lens),
-                      _ptr(q_starts), batch, max_q_len, max_seq_len,
-                      float(scale) if scale is not None else 1.0 / math.sqrt(d), window, sinks, _ptr(workspace),
-                      workspace.numel() if workspace is not None else 0)
+        self._cache = cache
+        self._bind("mxq_attention_nvfp4", dev,
+                   (q, out, lse_t, block_table, seq_lens, q_starts, workspace, *cache.tensors()),
+                   _ptr(q), ld_q, hq, total, _ptr(out), ld_out, _ptr(lse_t), ctypes.byref(cache._c),
+                   _ptr(block_table), block_table.stride(0) if batch > 1 else pages, pages, _ptr(seq_lens),
+                   _ptr(q_starts), batch, max_q_len, max_seq_len,
+                   float(scale) if scale is not None else 1.0 / math.sqrt(d), window, sinks, _ptr(workspace),
+                   workspace.numel() if workspace is not None else 0)
 
     def __call__(self, stream=None) -> AttentionResult:
-        return self._launch("mxq_attention_nvfp4", stream)
+        return self._launch(stream)
 
 
 def mxq_attention_nvfp4(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,

@@ -27,3 +27,16 @@ def test_c11_caller(tmp_path):
     r = subprocess.run([exe], env=env, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr
     assert "all checks passed" in r.stdout
+
+
+def test_widths_that_would_not_fit_are_refused():
+    """window and sinks are 32-bit in C: a larger one must not wrap into another mask."""
+    import torch
+    cache = mxq.NVFP4KVCache.allocate(2, 16, 1, 64, 1.0, 1.0, device="cpu")
+    args = (torch.zeros(1, 2, 64, dtype=torch.bfloat16), cache, torch.zeros(1, 2, dtype=torch.int32),
+            torch.ones(1, dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32), 1)
+    for name in ("window", "sinks"):
+        for value in (-1, 1 << 31, (1 << 32) + 5):
+            with pytest.raises(ValueError, match=name):
+                mxq.AttentionNVFP4(*args, **{name: value})
+    mxq.AttentionNVFP4(*args, window=(1 << 31) - 1, sinks=(1 << 31) - 1)
