@@ -653,13 +653,20 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int 
     store_finished<D>(a, seq, kvh, r, 4 * t, y, top, sum, vg);
 }
 
+// Rows of a unit on the line that can hold queries, a multiple of 4.
+__host__ __device__ __forceinline__ int join_rows(const AttnArgs& a) {
+    const int64_t rows = ((int64_t)a.max_q_len * a.group + 3) / 4 * 4;
+    return rows < a.tile_rows ? (int)rows : a.tile_rows;
+}
+
 // The units that the line's stretches cut (desc: where the unit begins, and its parts).
 // W = 4: a work-group per row; W = 1: a wave.
 template <int D, int W>
 __global__ __launch_bounds__(256) void k_attention_join_units(const AttnArgs a) {
     const int64_t item = (int64_t)blockIdx.x * (4 / W) + (threadIdx.x >> 6) / W;
-    const int64_t unit = item / a.tile_rows;                 // (tile_rows is a multiple of 4)
-    const int r = (int)(item - unit * a.tile_rows);
+    const int rows = join_rows(a);
+    const int64_t unit = item / rows;
+    const int r = (int)(item - unit * rows);
     int2 d = a.desc[unit];
     const int b = (int)(unit / a.c.kv_heads), kvh = (int)(unit - (int64_t)b * a.c.kv_heads);
     const Seq seq = sequence(a, b);
@@ -731,7 +738,7 @@ hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream) {
 constexpr int kWaveParts = 4;
 template <int D>
 static void launch_join(const AttnArgs& a, hipStream_t stream) {
-    const int64_t units = (int64_t)a.batch * a.row_tiles * a.c.kv_heads, rows = units * a.tile_rows;
+    const int64_t units = (int64_t)a.batch * a.row_tiles * a.c.kv_heads, rows = units * (a.desc ? join_rows(a) : a.tile_rows);
     const dim3 each((unsigned)rows), four((unsigned)(rows / 4));
     if (a.desc && units * kWaveParts < a.splits)
         hipLaunchKernelGGL((k_attention_join_units<D, 4>), each, dim3(256), 0, stream, a);
