@@ -66,18 +66,31 @@ struct Place {
     uint32_t bad;                     // bit t: group t's page may not be read
 };
 template <int G>
-__device__ __forceinline__ Place<G> place(const AttnArgs& a, int32_t entries, int tile) {
+__device__ __forceinline__ Place<G> place(const AttnArgs& a, int32_t entries, int tile, const Lane& L) {
     Place<G> p;
-    p.bad = 0;
-#pragma unroll
-    for (int t = 0; t < G; ++t) {
-        const int32_t e = __builtin_amdgcn_readlane(entries, t);
+    if constexpr (G == 1) {
+        const int32_t e = __builtin_amdgcn_readfirstlane(entries);
         const bool ok = (uint32_t)e < (uint32_t)a.c.num_pages;
-        p.bad |= ok ? 0u : 1u << t;
-        const int64_t page = ok ? e : 0;
-        const int64_t row = (tile * 64 + 16 * t) & ((1 << a.c.page_shift) - 1);
-        p.codes[t] = page * a.c.cs_page + row * a.c.cs_tok;
-        p.scales[t] = page * a.c.ss_page + row * a.c.ss_tok;
+        const int64_t page = ok ? e : 0, row = (tile * 64) & ((1 << a.c.page_shift) - 1);
+        p.bad = ok ? 0u : 1u;
+        p.codes[0] = page * a.c.cs_page + row * a.c.cs_tok;
+        p.scales[0] = page * a.c.ss_page + row * a.c.ss_tok;
+    } else {
+        // each lane its own group's offsets, then read from the first four: a third of the
+        // scalar instructions of four times the above
+        const bool ok = (uint32_t)entries < (uint32_t)a.c.num_pages;
+        const uint32_t page = ok ? (uint32_t)entries : 0u;
+        const uint32_t row = (uint32_t)(tile * 64 + 16 * (L.lane & 3)) & ((1u << a.c.page_shift) - 1);
+        const uint64_t codes = page * (uint64_t)a.c.cs_page + (uint64_t)row * (uint32_t)a.c.cs_tok;
+        const uint64_t scales = page * (uint64_t)a.c.ss_page + (uint64_t)row * (uint32_t)a.c.ss_tok;
+        p.bad = (uint32_t)__ballot(!ok) & 15u;
+#pragma unroll
+        for (int t = 0; t < G; ++t) {
+            p.codes[t] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)codes, t) |
+                                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(codes >> 32), t) << 32);
+            p.scales[t] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)scales, t) |
+                                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(scales >> 32), t) << 32);
+        }
     }
     return p;
 }
@@ -374,7 +387,7 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
             }
             const float kg = a.c.kg[kvh];
             __builtin_amdgcn_sched_barrier(0);
-            const Place<G> where = place<G>(a, e, tile_of(i));
+            const Place<G> where = place<G>(a, e, tile_of(i), L);
             load_v<D, G>(head, where, off, L, v);
             load_k<D, G>(head, where, off, k);
             bad = where.bad;
@@ -438,7 +451,7 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
             stage_scales<D>(mine, v.s, valid, L);
             // (past the stretch the last tile again: a branch around a load would make every
             // later wait for loads a wait for all of them)
-            const Place<G> where = place<G>(a, entries, tile_of(i + W));
+            const Place<G> where = place<G>(a, entries, tile_of(i + W), L);
             load_v<D, G>(head, where, off, L, v);
             entries = entries_of(i + 2 * W);
             bad = where.bad;
