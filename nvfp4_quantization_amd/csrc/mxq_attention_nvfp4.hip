@@ -277,15 +277,16 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
 
     // ---- this work-group's stretch of the line [at, end), and the sequence it starts in
     int64_t at = 0, end, share = 0, before = 0;             // before: the line up to sequence b
-    int b;
-    if (W == 8 || !a.desc) {                                // a unit of its own
+    const bool own = W == 8 || !a.desc;                     // a unit of its own
+    int b, own_head = 0;
+    if (own) {
         b = (int)(blockIdx.x / (unsigned)a.c.kv_heads);
+        own_head = (int)(blockIdx.x - (unsigned)b * (unsigned)a.c.kv_heads);
         const Seq s = sequence(a, b);
         const int n = unit_length(a, s);
         if (n == 0) return;
         seqs[0] = make_int4(s.len, s.start, s.nq, n);       // (every thread the same)
-        at = (int64_t)(blockIdx.x - (unsigned)b * (unsigned)a.c.kv_heads) * n;
-        end = at + n;
+        end = n;
     } else {
         // four consecutive sequences a thread
         uint32_t n[4], sum = 0;                             // (a unit is shorter than 2^26)
@@ -333,15 +334,18 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
 
     // ---- segment by segment: the part of one unit inside the stretch
     while (at < end) {
-        const int4 info = seqs[W == 4 && a.desc ? b : 0];
+        const int4 info = seqs[own ? 0 : b];
         const int n_unit = info.w;
         if (n_unit == 0) {                                  // (a sequence without queries)
             ++b;
             continue;
         }
-        const int64_t ahead = at - before;
-        const int kvh = __builtin_amdgcn_readfirstlane(ahead >> 32 ? (int)(ahead / n_unit) : (int)((uint32_t)ahead / (uint32_t)n_unit));
-        const int first = __builtin_amdgcn_readfirstlane((int)(ahead - (int64_t)kvh * n_unit));
+        int kvh = own_head, first = 0;
+        if (!own) {
+            const int64_t ahead = at - before;
+            kvh = __builtin_amdgcn_readfirstlane(ahead >> 32 ? (int)(ahead / n_unit) : (int)((uint32_t)ahead / (uint32_t)n_unit));
+            first = __builtin_amdgcn_readfirstlane((int)(ahead - (int64_t)kvh * n_unit));
+        }
         const int last = __builtin_amdgcn_readfirstlane((int)min((int64_t)n_unit, first + (end - at)));
         Seq seq;
         seq.len = __builtin_amdgcn_readfirstlane(info.x);
