@@ -36,7 +36,7 @@
 // latencies one after another), so the cache streams at 6.6 TB/s of the 7.0 that a plain read
 // reaches; 256 work-groups instead of 512 cost a third more, three a CU spill.  64 sequences
 // of up to 8192 tokens take 69 us (333 MB): there the longest units end last.  Few or short
-// sequences are latency: one of 1000 tokens takes 10 us on 8 CUs, 2 of them until lengths,
+// sequences are latency: one of 1000 tokens takes 9.8 us on 8 CUs, 2 of them until lengths,
 // page table and queries are there, 5 for two tiles a wave (the two waves of a SIMD take turns).
 #include "mxq_attention_nvfp4.hpp"
 
@@ -257,7 +257,9 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 
 }  // namespace
 
-template <int D, int NT, int G, int W>
+// LINE: the units lie on the line.  (A kernel apart from units of their own, which then need
+// 40 registers less: 64 drafts of four 55 -> 51 us.)
+template <int D, int NT, int G, int W, bool LINE>
 __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs a) {
     constexpr int kWave = WaveLds<D>::kBytes;
     constexpr int kJoin = (D / 16) * 64 * 16;               // a wave's outputs of one column tile
@@ -265,7 +267,7 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     __shared__ float2 join[W][NT * 16];
     // of the sequences on the line: length, first query row, queries, a unit's length on it
-    __shared__ int4 seqs[W == 4 ? kLineSeqs : 1];
+    __shared__ int4 seqs[LINE ? kLineSeqs : 1];
     __shared__ int64_t wave_length[4];
     __shared__ int found;
     __shared__ int64_t found_before;
@@ -277,9 +279,8 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
 
     // ---- this work-group's stretch of the line [at, end), and the sequence it starts in
     int64_t at = 0, end, share = 0, before = 0;             // before: the line up to sequence b
-    const bool own = W == 8 || !a.desc;                     // a unit of its own
     int b, own_head = 0;
-    if (own) {
+    if constexpr (!LINE) {                                  // a unit of its own
         b = (int)(blockIdx.x / (unsigned)a.c.kv_heads);
         own_head = (int)(blockIdx.x - (unsigned)b * (unsigned)a.c.kv_heads);
         const Seq s = sequence(a, b);
@@ -334,14 +335,14 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
 
     // ---- segment by segment: the part of one unit inside the stretch
     while (at < end) {
-        const int4 info = seqs[own ? 0 : b];
+        const int4 info = seqs[LINE ? b : 0];
         const int n_unit = info.w;
         if (n_unit == 0) {                                  // (a sequence without queries)
             ++b;
             continue;
         }
         int kvh = own_head, first = 0;
-        if (!own) {
+        if constexpr (LINE) {
             const int64_t ahead = at - before;
             kvh = __builtin_amdgcn_readfirstlane(ahead >> 32 ? (int)(ahead / n_unit) : (int)((uint32_t)ahead / (uint32_t)n_unit));
             first = __builtin_amdgcn_readfirstlane((int)(ahead - (int64_t)kvh * n_unit));
@@ -544,7 +545,7 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
         const bool whole = first == 0 && last == n_unit;
         // a cut unit's part: slot 1 of the work-group where it begins, slot 0 of those it goes on in
         const int64_t slot = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
-        if (first == 0 && tid == 0 && a.desc) {
+        if (LINE && first == 0 && tid == 0) {
             const int64_t rest = before + (int64_t)(kvh + 1) * n_unit - end;                 // past this stretch
             a.desc[(int64_t)b * a.c.kv_heads + kvh] =
                 make_int2((int)blockIdx.x, whole ? 0 : (int)((rest + share - 1) / share) + 1);
@@ -722,10 +723,12 @@ __global__ __launch_bounds__(256) void k_attention_join_splits(const AttnArgs a)
 template <int D, int NT, int G>
 static void launch_rows_pages(const AttnArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)a.splits);
-    if (!a.desc && a.splits <= kWideUnits)
-        hipLaunchKernelGGL((k_attention_rows<D, NT, G, 8>), grid, dim3(512), 0, stream, a);
+    if (a.desc)
+        hipLaunchKernelGGL((k_attention_rows<D, NT, G, 4, true>), grid, dim3(256), 0, stream, a);
+    else if (a.splits <= kWideUnits)
+        hipLaunchKernelGGL((k_attention_rows<D, NT, G, 8, false>), grid, dim3(512), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_attention_rows<D, NT, G, 4>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_rows<D, NT, G, 4, false>), grid, dim3(256), 0, stream, a);
 }
 template <int D, int NT>
 static void launch_rows(const AttnArgs& a, hipStream_t stream) {
