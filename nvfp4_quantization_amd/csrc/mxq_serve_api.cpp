@@ -84,6 +84,7 @@ mxq_status check_cache(const mxq_nvfp4_kv* c, mxq::KvCache* out) {
 //                kPromptGroups work-groups (two fit a CU).
 constexpr int64_t kRowsGroups = 256 * 2;
 constexpr int64_t kLineUnits = 1024;           // the line's units, and so its sequences, are fewer
+constexpr int64_t kMaxUnits = 1ll << 24;       // a launch's work-groups, 256 threads each, are fewer
 constexpr int64_t kPromptGroups = 256 * 2;
 static_assert(kRowsGroups <= mxq::kMaxParts, "a unit may be cut by every work-group");
 
@@ -121,7 +122,8 @@ bool plan_attention(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch,
     const int64_t group = q_heads / kv_heads, rows = max_q * group;
     p->tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
     p->row_tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
-    p->units = batch * p->row_tiles * kv_heads;
+    p->units = batch * p->row_tiles * kv_heads;                     // (below 2^48)
+    if (p->units >= kMaxUnits) return false;
     int64_t tiles = (max_len + 63) / 64;
     if (window > 0) {
         const int64_t near = (window + p->tile_rows / group + 62) / 64 + 1, far = (sinks + 63) / 64;
@@ -262,10 +264,10 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
     if (!extent_ok(total_q, ld_q, width) || !extent_ok(total_q, ld_out, width) ||
         !extent_ok(batch, ld_table, table_pages) || table_pages > kMaxRows)
         return MXQ_ERR_UNSUPPORTED;
-    // (the join's grid needs no check: fewer than kLineUnits units, or kPromptGroups / 2 at most)
+    // (units bound every grid: 512 threads each only up to kWideUnits; parts and the join only
+    // of fewer than kLineUnits units, or kPromptGroups / 2 at most)
     AttnPlan p;
-    if (!plan_attention(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len, max_seq_len, window, sinks, &p) ||
-        !product_below(p.tile_rows == 128 ? p.units * p.splits : p.splits, 256, kMaxGridThreads))
+    if (!plan_attention(q_heads, c.kv_heads, c.head_dim, batch, total_q, max_q_len, max_seq_len, window, sinks, &p))
         return MXQ_ERR_UNSUPPORTED;
     if (p.bytes > 0) {
         if (!workspace) return MXQ_ERR_INVALID_ARGUMENT;

@@ -1,0 +1,30 @@
+"""Limits of the serving calls on the host: shapes that a launch or a plan could not
+hold, and tensors that the binding must not hand to a kernel.  The C calls get fake device
+addresses, so they run where no GPU is visible."""
+import pytest
+
+import nvfp4_quantization_amd as mxq
+from tests.test_serve_boundary import HIP, L, UNSUPPORTED, attend, kv, no_gpu  # noqa: F401  (L: a fixture)
+
+
+def attend_wide(L, heads, batch, group=1):
+    """One query for `batch` sequences of `heads` cached heads of 64."""
+    c = kv(heads=heads, d=64, pages=1, c=(heads * 512, 512, 32), s=(heads * 64, 64, 4))
+    return attend(L, ld_q=heads * group * 64, ld_out=heads * group * 64, hq=heads * group, tq=1, cache=c, b=batch, mq=1)
+
+
+@no_gpu
+@pytest.mark.parametrize("heads,batch", [(257, 65535), (1024, 16384), (32768, 65535), (65538, 65535), (131072, 32768),
+                                         (131072, 32769)])
+@pytest.mark.parametrize("group", [1, 20])
+def test_units_past_a_launch_are_refused(L, heads, batch, group):
+    """batch * kv_heads from 2^24 on, 2^31, 2^32 and a little past them (where 32 bits would
+    wrap to no work-groups, or to a few): refused, and the size query asks for nothing."""
+    assert heads * batch >= 1 << 24
+    assert attend_wide(L, heads, batch, group) == UNSUPPORTED
+    assert mxq.mxq_attention_nvfp4_workspace_size(heads * group, heads, 64, batch, 1, 1, 64) == 0
+
+
+@no_gpu
+def test_units_up_to_the_limit_reach_the_launch(L):
+    assert attend_wide(L, 256, 65535) == HIP          # (which fails: there is no GPU)
