@@ -59,9 +59,12 @@ class _Prepared:
         assert len(args) == len(types) - 1
         self._args = tuple(a if isinstance(a, (ctypes.c_void_p, _ByRef)) else t(a) for a, t in zip(args, types))
         self._what, self._device, self._tensors = what, device, tensors
+        self._index = device.index if device.type == "cuda" else None
 
     def _launch(self, stream):
-        index = self._device.index
+        index = self._index
+        if index is None:
+            raise ValueError(f"{self._what}: the tensors are on {self._device}, expected a GPU")
         if index == torch.cuda.current_device():
             self._run(index, stream)
         else:

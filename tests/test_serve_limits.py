@@ -2,6 +2,7 @@
 hold, and tensors that the binding must not hand to a kernel.  The C calls get fake device
 addresses, so they run where no GPU is visible."""
 import pytest
+import torch
 
 import nvfp4_quantization_amd as mxq
 from tests.test_serve_boundary import HIP, L, UNSUPPORTED, attend, kv, no_gpu  # noqa: F401  (L: a fixture)
@@ -28,3 +29,23 @@ def test_units_past_a_launch_are_refused(L, heads, batch, group):
 @no_gpu
 def test_units_up_to_the_limit_reach_the_launch(L):
     assert attend_wide(L, 256, 65535) == HIP          # (which fails: there is no GPU)
+
+
+# ------------------------------------------------------------------ the binding
+def cpu_calls():
+    """One prepared call of each kind on tensors in host memory."""
+    cache = mxq.NVFP4KVCache.allocate(2, 16, 1, 64, 1.0, 1.0, device="cpu")
+    x = torch.zeros(2, 256, dtype=torch.bfloat16)
+    q = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    ints = torch.arange(3, dtype=torch.int32)
+    return [mxq.AddRMSNormFP8(x, torch.ones(256, dtype=torch.bfloat16)),
+            mxq.RopeAppendNVFP4(q, q, q, ints[:2], ints[:2].long(), mxq.rope_plan(64, device="cpu"), cache),
+            mxq.AttentionNVFP4(q, cache, ints[:2, None], ints[:2], ints, 1)]
+
+
+@pytest.mark.parametrize("stream", [None, 0, 1 << 20])
+def test_tensors_in_host_memory_are_refused(stream):
+    """Before a stream is looked up or anything is enqueued: a kernel would read host addresses."""
+    for call in cpu_calls():
+        with pytest.raises(ValueError, match="GPU"):
+            call(stream)
