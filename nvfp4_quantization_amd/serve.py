@@ -360,7 +360,8 @@ class AttentionNVFP4(_Prepared):
         if workspace is None and need > 0:
             workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         elif workspace is not None:
-            _need(workspace, "workspace", (torch.uint8,), dev, 1)
+            if not _need(workspace, "workspace", (torch.uint8,), dev, 1).is_contiguous():
+                raise ValueError("workspace must be contiguous")
         self.workspace = workspace
         self.out = AttentionResult(out, lse_t)
         self._cache = cache

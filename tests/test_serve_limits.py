@@ -49,3 +49,20 @@ def test_tensors_in_host_memory_are_refused(stream):
     for call in cpu_calls():
         with pytest.raises(ValueError, match="GPU"):
             call(stream)
+
+
+def attention_args(tokens=1, heads=4, pages=1):
+    cache = mxq.NVFP4KVCache.allocate(2, 16, 1, 64, 1.0, 1.0, device="cpu")
+    return (torch.zeros(tokens, heads, 64, dtype=torch.bfloat16), cache, torch.zeros(1, pages, dtype=torch.int32),
+            torch.ones(1, dtype=torch.int32), torch.tensor([0, tokens], dtype=torch.int32), tokens)
+
+
+def test_workspaces_with_gaps_or_repeats_are_refused():
+    """Their element count is not the bytes behind the first one: the kernels would write past
+    the end of a repeated byte, and into what lies between strided ones."""
+    need = mxq.mxq_attention_nvfp4_workspace_size(4, 1, 64, 1, 1, 1, 1 << 20)
+    assert need > 0
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            mxq.AttentionNVFP4(*attention_args(), max_seq_len=1 << 20, workspace=bad)
+    mxq.AttentionNVFP4(*attention_args(), max_seq_len=1 << 20, workspace=torch.zeros(need, dtype=torch.uint8))
