@@ -14,6 +14,7 @@ import torch
 from . import _bf16_bits, _check, _current_stream, _ptr, _row_stride, _stream, lib
 
 MXQ_ROPE_INTERLEAVED = 1
+_MAX_SEQ_LEN = (1 << 31) - 128                    # the longest estimate that the library takes
 
 
 class _KV(ctypes.Structure):
@@ -353,7 +354,7 @@ class AttentionNVFP4(_Prepared):
             if not 0 <= value < 1 << 31:
                 raise ValueError(f"{name} must be in [0, 2^31), got {value}")
         if max_seq_len is None:
-            max_seq_len = pages * cache.page_size
+            max_seq_len = min(pages * cache.page_size, _MAX_SEQ_LEN)
         lse_t = torch.zeros((total, hq), dtype=torch.float32, device=dev) if lse else None
         need = mxq_attention_nvfp4_workspace_size(hq, cache.kv_heads, d, batch, total, max_q_len, max_seq_len, window,
                                                   sinks)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import nvfp4_quantization_amd as mxq
-from tests.test_serve_boundary import HIP, L, UNSUPPORTED, attend, kv, no_gpu  # noqa: F401  (L: a fixture)
+from tests.test_serve_boundary import HIP, MISALIGNED, L, UNSUPPORTED, attend, kv, no_gpu  # noqa: F401  (L: a fixture)
 
 
 def attend_wide(L, heads, batch, group=1):
@@ -66,3 +66,14 @@ def test_workspaces_with_gaps_or_repeats_are_refused():
         with pytest.raises(ValueError, match="workspace"):
             mxq.AttentionNVFP4(*attention_args(), max_seq_len=1 << 20, workspace=bad)
     mxq.AttentionNVFP4(*attention_args(), max_seq_len=1 << 20, workspace=torch.zeros(need, dtype=torch.uint8))
+
+
+@no_gpu
+def test_tables_that_could_hold_more_than_a_sequence(L):
+    """The default length to plan for is what the table can hold, or the most that the library
+    takes: 32769 pages of 65536 tokens are past it."""
+    cache = mxq.NVFP4KVCache.allocate(1, 1 << 16, 1, 64, 1.0, 1.0, device="cpu")
+    q, _, table, *rest = attention_args(pages=32769)
+    call = mxq.AttentionNVFP4(q, cache, table, *rest)
+    assert call.workspace is not None
+    assert call._fn(*call._args, None) in (HIP, MISALIGNED)       # past the checks of shapes
