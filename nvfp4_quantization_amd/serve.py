@@ -11,7 +11,7 @@ from typing import Optional
 
 import torch
 
-from . import _bf16_bits, _check, _current_stream, _ptr, _row_stride, _stream, lib
+from . import _check, _current_stream, _ptr, _stream, lib
 
 MXQ_ROPE_INTERLEAVED = 1
 _MAX_SEQ_LEN = (1 << 31) - 128                    # the longest estimate that the library takes
@@ -117,11 +117,15 @@ class AddRMSNormFP8(_Prepared):
         scales = torch.empty((n // 128, m) if scale_transposed else (m, n // 128), dtype=torch.float32, device=dev)
         y = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out_bf16 else None
         sr, sg = (1, m) if scale_transposed else (n // 128, 1)
+
+        def rows(t):
+            """Row stride.  A dimension of one has none to speak of: torch may report any."""
+            return 0 if t is None else t.stride(0) if m > 1 else n
+
         self.out = RMSNormFP8Result(q, scales, residual_out, y)
         self._bind("mxq_add_rmsnorm_quant_fp8", dev, (x, residual, residual_out, weight, y, q, scales),
-                   _ptr(x), _row_stride(x), _ptr(residual), _row_stride(residual), _ptr(residual_out),
-                   _row_stride(residual_out), _ptr(weight), float(eps), m, n, options, _ptr(y), n, _ptr(q), n,
-                   _ptr(scales), sr, sg)
+                   _ptr(x), rows(x), _ptr(residual), rows(residual), _ptr(residual_out), rows(residual_out),
+                   _ptr(weight), float(eps), m, n, options, _ptr(y), n, _ptr(q), n, _ptr(scales), sr, sg)
 
     def __call__(self, stream=None) -> RMSNormFP8Result:
         return self._launch(stream)

@@ -77,3 +77,13 @@ def test_tables_that_could_hold_more_than_a_sequence(L):
     call = mxq.AttentionNVFP4(q, cache, table, *rest)
     assert call.workspace is not None
     assert call._fn(*call._args, None) in (HIP, MISALIGNED)       # past the checks of shapes
+
+
+@no_gpu
+@pytest.mark.parametrize("residual", [False, True])
+def test_one_row_has_no_stride(residual):
+    """torch reports any stride for a dimension of one: a column seen transposed is a row."""
+    column = torch.zeros(256, 1, dtype=torch.bfloat16)
+    assert column.t().stride() == (1, 1)
+    call = mxq.AddRMSNormFP8(column.t(), torch.ones(256, dtype=torch.bfloat16), column.t() if residual else None)
+    assert call._fn(*call._args, None) == HIP
