@@ -74,6 +74,16 @@ __device__ __forceinline__ void widen8(const uint4& w, float (&v)[8]) {
     }
 }
 
+// The divisions' corrected quotients need steps, inverses and residuals that are normal.  Under
+// a tensor scale g outside [2^-64, 2^64] both operands of each are brought there by this power
+// of two first: exactly, after their own roundings, or with a result (a scale or a code of
+// zero, or a saturated one) that no rounding can change.
+__device__ __forceinline__ float mid_power(float g) { return g < 0x1p-64f ? 0x1p64f : g > 0x1p64f ? 0x1p-64f : 1.0f; }
+// block_code() of a scaled fl(a * F(1/6)) and g.
+__device__ __forceinline__ uint32_t scale_code(float a6, float g, float yg) {
+    return e4m3_code(__builtin_elementwise_minimum(div_ieee(a6, g, yg), 448.0f)) & 0x7Fu;
+}
+
 // E2M1 value of a code's magnitude bits, signed.
 __device__ __forceinline__ float e2m1_value(uint32_t c) {
     const uint32_t m = c & 7u;
@@ -146,10 +156,14 @@ __global__ __launch_bounds__(256) void k_rope_append_nvfp4(const RopeAppendArgs 
         for (int i = 0; i < 8; ++i) m = __builtin_elementwise_maximum(m, __builtin_fabsf(y[i]));
         m = __builtin_elementwise_maximum(m, shfl_xor_f32(m, 1));
         const float g = (is_v ? a.c.vg : a.c.kg)[head];
-        const uint32_t sc = block_code(m, g, 1.0f / g);
-        const float d = e4m3_value(sc) * g;
+        const float up = mid_power(g), gu = g * up;
+        const uint32_t sc = scale_code(m * k_inv6() * up, gu, 1.0f / gu);
+        const float d = e4m3_value(sc) * g, du = d * up;
+        float yu[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) yu[i] = y[i] * up;
         const u32x4 none = {0, 0, 0, 0};
-        uint32_t codes = encode8<Enc::Div, true>(y, d, 1.0f / d, none, 0);
+        uint32_t codes = encode8<Enc::Div, true>(yu, du, 1.0f / du, none, 0);
         if (sc == 0 || sc == 0x7Fu) codes = 0;
         if (keep) {
             uint8_t* cp = (is_v ? a.c.vc : a.c.kc) + page * a.c.cs_page + head * a.c.cs_head + off * a.c.cs_tok;

@@ -1,0 +1,48 @@
+"""The serving calls at the ends of what their arguments may hold: tensor scales, scores and
+angles far from the ordinary, and tokens that a query does not see."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_quantization_amd as mxq
+from tests import serve_util as su
+from tests.gpu_util import announce, assert_same, device, host
+from tests.test_gpu_serve import Case, bf16
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ the append's tensor scales
+@pytest.mark.parametrize("g", [2.0 ** -126, 1.7 * 2.0 ** -126, 1.3 * 2.0 ** -120, 1.1 * 2.0 ** -100, 1.9 * 2.0 ** -75,
+                               1.2 * 2.0 ** 75, 1.5 * 2.0 ** 125, 1.3 * 2.0 ** 126, 1.999 * 2.0 ** 127])
+def test_append_tensor_scales(g):
+    """Blocks over the whole range of block scales (and below and above it) under every normal
+    tensor scale: the stated divisions, also where a step or an inverse is not normal."""
+    dev = device()
+    announce(f"append tensor scale {g}")
+    rng = np.random.default_rng(int(math.log2(g)) + 500)
+    t, hk, d = 64, 2, 128
+    # a block's largest value is 6 * scale * g: scales 2^-11 .. 2^10 as far as BF16 goes
+    amp = 6.0 * g * 2.0 ** rng.uniform(-11, 10, (t, hk, d // 16, 1))
+    y = np.clip(rng.uniform(-1, 1, (t, hk, d // 16, 16)) * amp, -3e38, 3e38).reshape(t, hk, d)
+    k = torch.from_numpy(y.astype(np.float32)).bfloat16()
+    v = (k.flip(0).float() * 0.5).bfloat16()
+    scale = torch.full((hk,), g, dtype=torch.float64).float()
+    cache = mxq.NVFP4KVCache.allocate(t // 16, 16, hk, d, 1.0, 1.0, device=dev)
+    cache.k_global.copy_(scale)
+    cache.v_global.copy_(scale)
+    got = mxq.mxq_rope_append_nvfp4(None, k.to(dev), v.to(dev), torch.zeros(t, dtype=torch.int32, device=dev),
+                                    torch.arange(t, device=dev), mxq.rope_plan(0, device=dev), cache, values=True)
+    torch.cuda.synchronize()
+    for name, x, codes, scales, values in (("k", k, cache.k_codes, cache.k_scales, got.k_values),
+                                           ("v", v, cache.v_codes, cache.v_scales, got.v_values)):
+        want_codes, want_scales = su.encode_rows(su.f32_of_bf16(x), scale.numpy())
+        assert_same(name + " scales", host(scales.transpose(1, 2).reshape(t, hk, d // 16)), want_scales)
+        assert_same(name + " codes", host(codes.transpose(1, 2).reshape(t, hk, d // 2)), want_codes)
+        with np.errstate(over="ignore"):
+            want = su.to_bf16(su.decode_rows(want_codes, want_scales).astype(np.float32) * scale.numpy()[None, :, None])
+        assert_same(name + " values", su.f32_of_bf16(values), want)
+
+
