@@ -468,7 +468,8 @@ typedef struct {
 /* Rotary positions.  Pair i (0 <= i < rot_dim/2) of a head turns by the angle
  *   theta = fl64(position * inv_freq[i]),
  * so a table of inverse frequencies in binary64 expresses every scaling of them for
- * long contexts; cos and sin are formed in binary64 (error below 2^-50) and
+ * long contexts; cos and sin are formed in binary64 (error below 2^-50 for |theta| < 2^45,
+ * which any position keeps to under frequencies below 2^14; NaN past it) and
  *   c = F(factor * cos(theta)),  s = F(factor * sin(theta))   (one round to binary32).
  * Pair i is elements (i, i + rot_dim/2) of the head, or (2i, 2i + 1) with
  * MXQ_ROPE_INTERLEAVED; with (a, b) its BF16 values the rotated pair is

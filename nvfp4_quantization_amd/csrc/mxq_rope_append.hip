@@ -4,7 +4,8 @@
 // Angles are formed in binary64 (theta = fl(position * inv_freq), so a position of a
 // million keeps its place on the circle to 2^-33) and reduced by Cody and Waite's method
 // (Software Manual for the Elementary Functions, 1980) with pi/2 in two parts: the FMA
-// keeps k * part exact, so the remainder in [-pi/4, pi/4] carries an error below 2^-52;
+// keeps k * part exact, so the remainder in [-pi/4, pi/4] carries an error below 2^-52 for
+// |theta| < 2^45 (others become NaN);
 // sine and cosine are their Taylor polynomials to r^17 and r^16, whose first left-out
 // terms are below 2^-56.  cos and sin are rounded to FP32 once, and one work-group's
 // heads share them through LDS.
@@ -25,8 +26,10 @@ namespace {
 
 constexpr int kMaxPairs = 64;         // rot_dim / 2 at head_dim 128
 
-// cos and sin of a finite theta (|theta| < 2^45).
+// cos and sin of theta; NaN unless |theta| < 2^45 (past 2^50 the multiple of pi/2 would not be
+// the nearest one any more, past 2^53 not a whole number's).
 __device__ __forceinline__ void sincos_stated(double theta, double& c, double& s) {
+    if (!(__builtin_fabs(theta) < 0x1p45)) theta = __builtin_nan("");
     const double k = __builtin_rint(theta * 0x1.45f306dc9c883p-1);              // 2/pi
     double r = __builtin_fma(-k, 0x1.921fb54442d18p+0, theta);                  // pi/2, high part
     r = __builtin_fma(-k, 0x1.1a62633145c07p-54, r);                            // and the rest

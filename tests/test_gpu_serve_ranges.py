@@ -46,3 +46,32 @@ def test_append_tensor_scales(g):
         assert_same(name + " values", su.f32_of_bf16(values), want)
 
 
+# ------------------------------------------------------------------ angles
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_angles_past_the_reduction(interleaved):
+    """Angles below 2^45 are turned by, whatever position and frequency make them up; from
+    there on, and for frequencies that are no numbers, the pair is NaN."""
+    dev = device()
+    announce(f"angles interleaved={interleaved}")
+    rng = np.random.default_rng(4)
+    freq = np.array([1.0, 2.0 ** 13 + 0.3, 2.0 ** 14, 2.0 ** 20, 1e30, 1e300, np.inf, np.nan])
+    pos = np.array([0, 1, 1000, -5, 2 ** 31 - 1, -2 ** 31, 123456789, 2 ** 30], np.int64).astype(np.int32)
+    q = bf16(rng, 8, 2, 64)
+    k = bf16(rng, 8, 1, 64)
+    cache = mxq.NVFP4KVCache.allocate(1, 16, 1, 64, 4.0, 4.0, device=dev)
+    plan = mxq.RopePlan(torch.from_numpy(freq).to(dev), interleaved=interleaved)
+    got = mxq.mxq_rope_append_nvfp4(q.to(dev), k.to(dev), k.to(dev), torch.from_numpy(pos).to(dev),
+                                    torch.arange(8, device=dev), plan, cache)
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        theta = pos.astype(np.float64)[:, None] * freq
+        bad = ~(np.abs(theta) < 2.0 ** 45)
+        want = su.rope_reference(su.f32_of_bf16(q), pos, freq, 1.0, interleaved)
+    pair = np.repeat(bad, 2, 1) if interleaved else np.concatenate([bad, bad], 1)
+    pair = np.broadcast_to(pair[:, None], (8, 2, 16))
+    a = su.f32_of_bf16(got.q)
+    assert np.array_equal(np.isnan(a[..., :16]), pair)
+    assert_same("angles in range", np.where(pair, 0, a[..., :16]), np.where(pair, 0, want[..., :16]))
+    assert_same("unrotated", a[..., 16:], want[..., 16:])
+
+
