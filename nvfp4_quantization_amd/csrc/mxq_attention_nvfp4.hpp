@@ -134,6 +134,11 @@ __device__ __forceinline__ bool has_nan_scale(uint32_t w) {
 }
 
 // ---------------------------------------------------------------- softmax
+// A row's maximum after a tile whose largest score is top (over all of the row's lanes).  By the
+// row itself, though the wave raises all its rows at once: another row's scores, which may be of
+// tokens that this one does not see, must not change a bit of it.
+__device__ __forceinline__ float raise(float m, float top) { return top > m + kSlack ? top : m; }
+
 // One step of 64 tokens for 16 query rows: raw scores x (lane column = row, 16 tokens a
 // lane) to FP16 weights p, with the row's maximum, its lane's share of the sum and, when
 // the maximum is raised, the outputs.  factor > 0 turns raw scores into base-2 exponents.
@@ -150,7 +155,7 @@ __device__ __forceinline__ void softmax_step(f32x4 (&x)[4], float factor, float&
     if (__any(top > m + kSlack)) {
         top = __builtin_fmaxf(top, shfl_xor_f32(top, 16));
         top = __builtin_fmaxf(top, shfl_xor_f32(top, 32));
-        const float raised = __builtin_fmaxf(m, top);
+        const float raised = raise(m, top);
         const float f = __builtin_amdgcn_exp2f(m - raised);
         m = raised;
         l *= f;

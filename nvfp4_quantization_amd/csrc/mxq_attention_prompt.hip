@@ -322,7 +322,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
         top *= factor;
         if (__any(top > m + kSlack)) {
             top = __builtin_fmaxf(top, shfl_xor_f32(top, 32));
-            const float raised = __builtin_fmaxf(m, top);
+            const float raised = raise(m, top);
             const float f = __builtin_amdgcn_exp2f(m - raised);
             m = raised;
             l *= f;

@@ -75,3 +75,31 @@ def test_append_angles_past_the_reduction(interleaved):
     assert_same("unrotated", a[..., 16:], want[..., 16:])
 
 
+# ------------------------------------------------------------------ what a query does not see
+@pytest.mark.parametrize("nq,hq", [(3, 8), (7, 8), (60, 8), (100, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_unseen_tokens_change_no_bit(nq, hq, d):
+    """The last query's own token gets the largest key along that query (its score raises the
+    running maximum wherever it is seen) and other values: no bit of an earlier query changes."""
+    dev = device()
+    announce(f"unseen nq={nq} hq={hq} d={d}")
+    changed = 0
+    for seed in range(4):
+        results = []
+        for other in (False, True):
+            c = Case([1400 + seed], [nq], hq, 2, d, 16, seed=seed, q_amp=0.3)
+            if other:
+                at = c.lens[0] - 1
+                page, row = c.table[0, at // 16], at % 16
+                for kv in range(2):
+                    code = 7 + 8 * (c.q[-1, kv * (hq // 2)].float().numpy() < 0).astype(np.uint8)
+                    c.kc[page, kv, row] = code[0::2] | (code[1::2] << 4)
+                c.ks[page, :, row] = 0x7E
+                c.vs[page, :, row] = 0x70
+            r = c.run(dev)()
+            torch.cuda.synchronize()
+            results.append((r.out.clone(), r.lse.clone()))
+        (a, la), (b, lb) = results
+        assert not torch.equal(a[-1], b[-1])
+        changed += int((a[:-1] != b[:-1]).sum()) + int((la[:-1] != lb[:-1]).sum())
+    assert changed == 0
