@@ -16,7 +16,7 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 
-constexpr float kFloor = -1e30f;      // the running maximum before any score (finite: no inf - inf)
+constexpr float kFloor = -0x1.fffffep+127f;     // the running maximum before any score (finite: no inf - inf)
 constexpr float kBias = 9.0f;         // weights are 2^(s - m + kBias): at most 2^(kSlack + kBias) = 2^14
 constexpr float kSlack = 5.0f;        // how far scores may exceed m before it is raised
 
@@ -139,6 +139,16 @@ __device__ __forceinline__ bool has_nan_scale(uint32_t w) {
 // tokens that this one does not see, must not change a bit of it.
 __device__ __forceinline__ float raise(float m, float top) { return top > m + kSlack ? top : m; }
 
+// Weights are 2^fma(x, factor, kBias - m): one rounding, of a small number, but m itself is a
+// rounded product, and from 2^24 on its rounding alone (all of a row's weights times 2 and more)
+// would leave FP16's range.  There the rounded product is taken for every score, as it was for
+// m: weights of a row with far() are 2^(fl(x factor) - m + kBias), the difference formed in place
+// of x.  (The floor and infinities stay out.)  The test costs a tile of heads of 64 1.5 to 2 %.
+__device__ __forceinline__ bool far(float m) {
+    constexpr uint32_t kNear = 0x4A800000u;                              // 2^22
+    return (__builtin_bit_cast(uint32_t, m) & 0x7FFFFFFFu) - kNear < 0x7F7FFFFFu - kNear;
+}
+
 // One step of 64 tokens for 16 query rows: raw scores x (lane column = row, 16 tokens a
 // lane) to FP16 weights p, with the row's maximum, its lane's share of the sum and, when
 // the maximum is raised, the outputs.  factor > 0 turns raw scores into base-2 exponents.
@@ -162,7 +172,17 @@ __device__ __forceinline__ void softmax_step(f32x4 (&x)[4], float factor, float&
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) o[dt] *= f;
     }
-    const float shift = kBias - m;
+    float shift = kBias - m;
+    if (__builtin_expect(__any(far(m)), 0)) {
+        const bool is_far = far(m);
+        const float by = is_far ? factor : 1.0f, less = is_far ? m : 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][e] = x[t][e] * by - less;
+        factor = is_far ? 1.0f : factor;
+        shift = is_far ? kBias : shift;
+    }
     float part[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {

@@ -332,12 +332,20 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 
         // Weights of 16 tokens at a time; their products with V between the weights of the
         // next 16.
-        const float shift = kBias - m;
+        float shift = kBias - m, scale = factor;
+        if (__builtin_expect(__any(far(m)), 0)) {
+            const bool is_far = far(m);
+            const float by = is_far ? factor : 1.0f, less = is_far ? m : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] = x[e >> 4][e & 15] * by - less;
+            scale = is_far ? 1.0f : factor;
+            shift = is_far ? kBias : shift;
+        }
         f16x8 p[2];
         const auto weights = [&](int f, int e) {                           // two of them
             const int k = 8 * f + e;
-            const f32x2 w = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[k >> 4][k & 15], factor, shift)),
-                             __builtin_amdgcn_exp2f(__builtin_fmaf(x[k >> 4][(k & 15) + 1], factor, shift))};
+            const f32x2 w = {__builtin_amdgcn_exp2f(__builtin_fmaf(x[k >> 4][k & 15], scale, shift)),
+                             __builtin_amdgcn_exp2f(__builtin_fmaf(x[k >> 4][(k & 15) + 1], scale, shift))};
             l += w.x + w.y;                            // before the rounding: lse is an output
             const f16x2 b = __builtin_convertvector(w, f16x2);
             p[f & 1][e] = b.x;

@@ -103,3 +103,44 @@ def test_unseen_tokens_change_no_bit(nq, hq, d):
         assert not torch.equal(a[-1], b[-1])
         changed += int((a[:-1] != b[:-1]).sum()) + int((la[:-1] != lb[:-1]).sum())
     assert changed == 0
+# ------------------------------------------------------------------ scores
+@pytest.mark.parametrize("nq,hq", [(1, 8), (5, 8), (3, 32), (60, 8)])
+@pytest.mark.parametrize("amp", [1e6, 1e8, 1e12, 1e31])
+@pytest.mark.parametrize("bound", [64, 1 << 22])
+def test_scores_past_a_weight_range(nq, hq, amp, bound):
+    """Scores so large that one step of FP32 at them is more than the weights' own range: where
+    the best token leads by more than the scores' rounding, the output is that token's value
+    and the log-sum its score."""
+    dev = device()
+    announce(f"scores nq={nq} hq={hq} amp={amp} bound={bound}")
+    d, hk = 128, 2
+    c = Case([700, 1, 130], [nq, 1, nq], hq, hk, d, 16, seed=nq, q_amp=amp)
+    r = c.run(dev, max_seq_len=bound)()
+    torch.cuda.synchronize()
+    out, lse = su.f32_of_bf16(r.out).astype(np.float64), host(r.lse).astype(np.float64)
+    q = su.f32_of_bf16(c.q).astype(np.float64)
+    checked = 0
+    for b, n in enumerate(c.lens):
+        at, off = c.table[b][np.arange(n) // 16], np.arange(n) % 16
+        for h in range(hq):
+            kv = h // (hq // hk)
+            k = su.decode_rows(c.kc[at, kv, off], c.ks[at, kv, off]) * float(c.kg[kv])
+            v = su.decode_rows(c.vc[at, kv, off], c.vs[at, kv, off]) * float(c.vg[kv])
+            for i in range(c.starts[b], c.starts[b + 1]):
+                seen = n - int(c.starts[b + 1]) + int(i) + 1
+                x = k[:seen] @ q[i, h] / math.sqrt(d)
+                # the scores' rounding (serve_util.attention_bounds): d + 8 of 2^-24 of sum |q k|
+                off_by = (d + 8) * 2.0 ** -24 * (np.abs(k[:seen]) @ np.abs(q[i, h])).max() / math.sqrt(d) + 2.0 ** -20
+                best = int(x.argmax())
+                lead = x[best] - np.delete(x, best).max() if seen > 1 else np.inf
+                assert np.isfinite(out[i, h]).all() and abs(lse[i, h] - x[best]) <= off_by + math.log(seen) + 2.0 ** -22 * abs(x[best])
+                if lead <= 2 * off_by + 40.0:
+                    continue
+                checked += 1
+                # the others' weights are below e^-40; its own is rounded to FP16 for the product and
+                # not in the sum (half a step: 2^-11), the output to BF16 (2^-8), the rest is FP32
+                e = np.abs(out[i, h] - v[best])
+                assert (e <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) * np.abs(v[best]) + 1e-12).all(), (e / np.abs(v[best])).max()
+    assert checked > 0.5 * q.shape[0] * hq
+
+
