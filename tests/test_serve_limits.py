@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import nvfp4_quantization_amd as mxq
-from tests.test_serve_boundary import HIP, MISALIGNED, L, UNSUPPORTED, attend, kv, no_gpu  # noqa: F401  (L: a fixture)
+from tests.test_serve_boundary import HIP, INVALID, MISALIGNED, UNSUPPORTED, WS_SMALL, A, L, attend, kv, no_gpu  # noqa: F401
 
 
 def attend_wide(L, heads, batch, group=1):
@@ -87,3 +87,17 @@ def test_one_row_has_no_stride(residual):
     assert column.t().stride() == (1, 1)
     call = mxq.AddRMSNormFP8(column.t(), torch.ones(256, dtype=torch.bfloat16), column.t() if residual else None)
     assert call._fn(*call._args, None) == HIP
+
+
+@no_gpu
+def test_long_work_is_cut(L):
+    """Few units over long contexts are cut, and then the workspace is checked."""
+    q = mxq.mxq_attention_nvfp4_workspace_size
+    for shape in [(64, 8, 128, 2, 2, 1, 262144), (32, 8, 128, 1, 512, 512, 65536), (8, 8, 64, 4, 16, 4, 100000),
+                  (4, 2, 128, 2, 6, 3, 1 << 20)]:
+        assert q(*shape) > 0, shape
+    need = q(4, 2, 128, 2, 6, 3, 1 << 20)
+    assert attend(L, ml=1 << 20, wsb=need) == HIP                 # taken, and no GPU to launch on
+    assert attend(L, ml=1 << 20, wsb=need - 1) == WS_SMALL
+    assert attend(L, ml=1 << 20, ws=None) == INVALID
+    assert attend(L, ml=1 << 20, ws=A + 128) == MISALIGNED
