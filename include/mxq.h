@@ -39,7 +39,8 @@
  *    MXQ_ERR_HIP (outputs are then undefined).  There is no fallback path: an
  *    unsupported request is an error, never a slower substitute.
  *  - Arithmetic is IEEE binary32 with one rounding per operation in the order
- *    stated below; every output is bit-exact with respect to that definition.
+ *    stated below; every output is bit-exact with respect to that definition, but
+ *    for those of mxq_attention_nvfp4, whose roundings are stated with it.
  *
  * Sources of the operations (page, then section):
  *  - onnxruntime PR #33644, QMoE dynamic FP8 activation quantization,
@@ -416,8 +417,8 @@ mxq_status mxq_group_rht_quant_nvfp4_noalloc(const uint16_t* x_bf16, int64_t k,
  *   weight_bf16   [n] BF16;  eps >= 0, finite
  *   y_bf16        [m][ld_y] BF16(y) as well (a router's input), or NULL
  *   q_e4m3, ldq, scales, scale strides: as mxq_quant_fp8_1x128
- * Requirements: n % 128 == 0, n <= MXQ_RMSNORM_MAX_N (else MXQ_ERR_UNSUPPORTED); BF16
- * strides multiples of 8, ldq of 16; pointers 16-byte aligned, scales 4-byte
+ * Requirements: n % 128 == 0, n <= MXQ_RMSNORM_MAX_N and m < 2^22 (else
+ * MXQ_ERR_UNSUPPORTED); BF16 strides multiples of 8, ldq of 16; pointers 16-byte aligned, scales 4-byte
  * aligned; options in {0, MXQ_FP8_UE8M0}.  m == 0 is a successful no-op.
  * ------------------------------------------------------------------------- */
 #define MXQ_RMSNORM_MAX_N 32768
@@ -506,7 +507,9 @@ typedef struct {
  *            included; or NULL
  * Requirements: strides multiples of 8 and at least heads * head_dim; BF16 pointers
  * 16-byte aligned, positions 4-, slots and inv_freq 8-byte aligned; at least one cached
- * head.  tokens == 0 is a successful no-op.
+ * head; tokens * (q_heads + 2 kv_heads) * head_dim / 8, the product of the last three
+ * rounded up to 256, below 2^32 (else MXQ_ERR_UNSUPPORTED).  tokens == 0 is a
+ * successful no-op.
  * ------------------------------------------------------------------------- */
 mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, uint16_t* q_out, int64_t ld_q_out,
                                  const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v, int64_t tokens,
@@ -521,9 +524,16 @@ mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_head
  * chunk or a whole prompt.  Query head h reads cached head h / (q_heads / kv_heads).
  * The query at position p sees token t iff
  *   t <= p  and  (window == 0 or t > p - window or t < sinks)
- * and out = softmax(softmax_scale * q . k) . v over the tokens it sees, with FP32 (or
- * wider) scores, maxima, sums and accumulators; 0 (and lse = -inf) where it sees none.
- * What a query does not see never reaches its output, whatever it holds (NaN scales
+ * and out = softmax(softmax_scale * q . k) . v over the tokens it sees; 0 (and lse =
+ * -inf) where it sees none.  Both products run on FP16 operands with FP32 accumulators;
+ * scores, maxima and sums are FP32.  K and V without their tensor scales are exact in
+ * FP16.  Q is taken times a power of two per row: elements down to 2^-31 of their row's
+ * largest are exact, smaller ones off by at most 2^-39 of it.  The softmax weights are
+ * rounded to FP16 (nearest-even) for the product with V, and not for their sum: each is
+ * off by at most 2^-11 of itself, or by 2^-34 of its row's largest weight where that is
+ * more.  out is rounded to BF16 once.  The order of the sums depends on the lengths and
+ * on max_seq_len, not on what the arrays hold, and a call repeats bit for bit.
+ * What a query does not see changes no bit of its output, whatever it holds (NaN scales
  * included).  A NaN K row it sees makes its output NaN; a NaN V block it sees makes
  * at least that block's 16 elements NaN.
  *

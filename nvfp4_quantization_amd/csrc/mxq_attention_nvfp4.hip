@@ -7,12 +7,12 @@
 //  * An E2M1 value times its E4M3 block scale has at most six significant bits and lies
 //    in [2^-10, 2688], so the dequantized K and V are exact in FP16: one conversion and
 //    one packed FP16 product per two elements.  Q is BF16 times a power of two per row
-//    (its largest element in [2^14, 2^15)), exact in FP16 but for elements 2^-28 below the
-//    row's largest.  Scores and outputs accumulate in FP32.
+//    (its largest element in [2^14, 2^15)): exact in FP16 down to 2^-31 of the row's largest,
+//    off by half its smallest step, 2^-39 of it, below.  Scores and outputs accumulate in FP32.
 //  * The tensor scales, the softmax scale and Q's power of two are one FP32 factor on the
 //    scores and one on the outputs.
 //  * Softmax: running maximum per row in FP32, raised only when a score exceeds it by more
-//    than 2^kSlack (the outputs are then rescaled); the weights 2^(s - m + kBias) are rounded to
+//    than kSlack (the outputs are then rescaled); the weights 2^(s - m + kBias) are rounded to
 //    FP16 (nearest-even) for the product with V, their FP32 values are summed.  With
 //    kBias = 9 a weight keeps all 11 bits down to 2^-23 of the row's largest and adds in
 //    down to 2^-33 of it.
@@ -31,12 +31,14 @@
 // end leaves partial outputs (maximum, sum, unnormalized FP32 rows) in the workspace for the
 // join.
 //
-// What bounds it: two sequences of 262144 tokens, 8 heads of 128 (604 MB of cache) take 102 us, 5
+// What bounds it: two sequences of 262144 tokens, 8 heads of 128 (604 MB of cache) take 103 us, 5
 // of them the join and about 6 the start (sequences, page table, first tile: three memory
 // latencies one after another), so the cache streams at 6.6 TB/s of the 7.0 that a plain read
 // reaches; 256 work-groups instead of 512 cost a third more, three a CU spill.  64 sequences
-// of up to 8192 tokens take 69 us (333 MB): there the longest units end last.  Few or short
-// sequences are latency: one of 1000 tokens takes 9.8 us on 8 CUs, 2 of them until lengths,
+// of up to 8192 tokens take 70 us (333 MB): there the longest units end last, and from 512 such
+// units on one far longer than the others is walked by one work-group a head, whatever it
+// takes (262144 tokens among 63 of 1000: 1335 us for 375 MB).  Few or short
+// sequences are latency: one of 1000 tokens takes 9.6 us on 8 CUs, 2 of them until lengths,
 // page table and queries are there, 5 for two tiles a wave (the two waves of a SIMD take turns).
 #include "mxq_attention_nvfp4.hpp"
 
@@ -127,8 +129,10 @@ __device__ __forceinline__ uint32_t here(uint32_t off) {
     asm("" : "+v"(off));
     return off;
 }
-// The cache's codes are read once by one work-group: loads that pass them through the L2
-// without keeping them ("non-temporal") take 107 us instead of 119 for 604 MB.
+// The cache's codes are mostly read once, by one work-group: loads that pass them through the L2
+// without keeping them ("non-temporal") take 97 us instead of 110 for 64 sequences of 8192
+// tokens (604 MB).  Where 7168 of those are pages that all sequences share (84 MB in all),
+// loads that keep them are a little faster: 73 us against 76.
 template <typename T>
 __device__ __forceinline__ T stream(const uint8_t* base, uint32_t off) {
     return __builtin_nontemporal_load(reinterpret_cast<const T*>(base + here(off)));

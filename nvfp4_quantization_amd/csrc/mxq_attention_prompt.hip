@@ -27,9 +27,9 @@
 // ones (half of it the 32 exponentials and their sums, a quarter the dequantization), of which
 // a matrix instruction hides all but its own issue, some 12 cycles; a CU's LDS is busy two
 // thirds of the time, an operand read from it feeding 32 rows.  512 queries of 32 heads of 128
-// over 65536 tokens take 568 us, 967 TFLOP/s (a plain 8192^3 product: 1109); two prompts of 4096
-// tokens 297 us, 925 TFLOP/s, and 368 us when the tiles of a sequence ran together, so that
-// the last sequence's longest rows started last.  64 rows a wave (half the operand reads, one
+// over 65536 tokens take 570 us, 961 TFLOP/s (a plain FP16 product of 8192^3: 1074 to 1109, by
+// card); two prompts of 4096 tokens 300 to 308 us, 892 to 916 TFLOP/s, and a quarter more when
+// the tiles of a sequence ran together, so that the last sequence's longest rows started last.  64 rows a wave (half the operand reads, one
 // wave a SIMD) were slower.
 #include "mxq_attention_nvfp4.hpp"
 
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
     // later rows, which see more tiles, first for all sequences and heads: the last to start are
-    // the shortest (two prompts of 4096 tokens 297 us against 368)
+    // the shortest (two prompts of 4096 tokens 298 us against 368 when it was brought in)
     const int split = (int)(blockIdx.x % (unsigned)a.splits);
     const int order = (int)(blockIdx.x / (unsigned)a.splits);
     const int bhs = a.batch * a.c.kv_heads;
@@ -367,7 +367,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
         }
     };
     // A wave without rows only stages its share of the next tile (64 ragged sequences of up to
-    // 8192 tokens with 40 rows a unit: 211 us against 257).
+    // 8192 tokens with 40 rows a unit: 211 us against 257).  The other two of four waves then do
+    // all products, so that these 336 MB take four times as long as their bytes.
     const auto stage = [&](int i, KImage<D>& kf, VImage<D>& vf) {
         __syncthreads();
         store_k<D>(kf, kr, my_tok, part);

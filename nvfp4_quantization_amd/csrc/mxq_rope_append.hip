@@ -15,8 +15,8 @@
 // head.
 //
 // What bounds it: memory.  8191 tokens of 32 + 8 + 8 heads of 128 with the values written
-// (211 MB) take 44 us, 4.8 TB/s, where a large copy reaches 5.3; a decoding step's 64
-// tokens take 4.2 us on the GPU, less than a call.
+// (211 MB) take 44 us, 4.8 TB/s, where a large copy reaches 5.4; a decoding step's 64
+// tokens take 4.3 us on the GPU, less than a call.
 #include "mxq_nvfp4_impl.hpp"
 #include "mxq_serve.hpp"
 
@@ -61,7 +61,7 @@ __device__ __forceinline__ void sincos_stated(double theta, double& c, double& s
 }
 
 // 16 bytes of an output that the call does not read again, past the L2 (8191 tokens of 48
-// head rows: 47.3 us against 49.8 with ordinary stores).
+// head rows: 44.6 us against 48.1 with ordinary stores).
 typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void put16(uint16_t* p, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     __builtin_nontemporal_store(u32x4s{x, y, z, w}, reinterpret_cast<u32x4s*>(p));
@@ -190,8 +190,9 @@ hipError_t launch_rope_append_nvfp4(const RopeAppendArgs& a, bool interleaved, h
     const int rows = a.q_heads + 2 * a.c.kv_heads, per = 256 / (a.c.head_dim / 8);
     const int steps = (rows + per - 1) / per;
     // few tokens: a work-group per 256 lanes of each, which forms the angles again (48 head
-    // rows, kernel times in us for one / several: 64 tokens 5.2 / 4.2, 512 6.1 / 5.8, 1024
-    // 8.4 / 8.9, 8191 37 / 40)
+    // rows, kernel times in us for one / several, with the values written: 64 tokens 5.0 / 4.3,
+    // 512 6.1 / 6.0, 1024 8.3 / 9.0, 8191 44.6 / 51.3; without them 4.7 / 3.8, 5.6 / 5.2,
+    // 7.3 / 8.4, 38.3 / 44.9)
     const int splits = a.tokens >= 1024 ? 1 : steps;
     const dim3 grid((unsigned)(a.tokens * splits));
     if (a.c.head_dim == 128) {

@@ -91,16 +91,29 @@ static_assert(kRowsGroups <= mxq::kMaxParts, "a unit may be cut by every work-gr
 // Whether the line is worth its join and its cut units, about 40 tiles of a CU's time (11 us).
 // With a work-group a unit the fullest CU has ceil(units / 256) units' tiles, with the line
 // every CU has units / 256; up to 256 units, where all start at once, sequences are taken to
-// fill three quarters of the longest.  Measured, line / unit in us (head_dim 128, batches of
-// equal lengths; of lengths from an eighth to the whole):
-//   units  tiles   equal          ragged            units  tiles   equal          ragged
-//       8     36   15.6 / 15.0    15.3 / 15.0         256    192   83.2 / 75.5    55.7 / 59.7
-//       8     56   15.3 / 20.2    15.9 / 20.2         384    192  120.1 / 127.2   77.6 / 92.0
-//      64     44   19.5 / 17.3    17.6 / 17.3         512     24   36.5 / 24.6    33.9 / 20.2
-//      64     72   21.3 / 24.8    21.0 / 24.4         512    192  154.3 / 143.8  103.8 / 108.0
-//     128     56   24.8 / 21.2    22.8 / 20.8         768     96  124.4 / 113.1   85.9 / 87.2
-//     128     72   27.7 / 25.2    24.9 / 24.8        1024     96  150.8 / 145.7  108.2 / 101.7
-//     256     96   49.8 / 41.7    36.8 / 34.0        2048     48  159.8 / 153.0  117.9 / 106.5
+// fill three quarters of the longest.  Measured, line / unit in us (8 query rows a cached head,
+// pages of 64; batches of equal lengths; of lengths from an eighth to the whole):
+//                 head_dim 128                     head_dim 64
+//   units  tiles  equal          ragged            equal          ragged          taken
+//       8     36   14.5 / 14.4    14.2 / 14.3       12.5 / 10.9    12.5 / 10.7    unit
+//       8     56   14.2 / 19.6    14.2 / 19.6       12.5 / 14.4    12.4 / 14.3    line
+//      64     44   17.7 / 17.0    16.3 / 16.8       15.0 / 12.4    14.4 / 12.1    unit
+//      64     72   19.9 / 24.4    19.6 / 24.1       15.8 / 17.4    16.0 / 17.1    line
+//     128     56   23.4 / 20.7    21.9 / 20.5       18.1 / 14.8    17.3 / 14.7    unit
+//     128     72   27.5 / 24.8    23.2 / 24.2       20.0 / 17.5    18.5 / 17.2    line
+//     256     96   49.2 / 41.2    32.0 / 32.8       31.5 / 24.5    23.3 / 21.8    unit
+//     256    192   83.1 / 74.7    54.6 / 59.9       51.6 / 43.3    35.1 / 38.0    line
+//     384    192  119.0 / 121.0   78.1 / 90.7       70.6 / 72.0    48.4 / 58.1    line
+//     512     24   34.2 / 24.6    29.6 / 20.2       24.8 / 14.5    22.9 / 13.7    unit
+//     512    192  153.4 / 142.8  101.1 / 109.4      92.3 / 82.2    62.8 / 63.7    unit
+//     768     96  122.1 / 111.1   80.8 / 88.8       76.1 / 61.0    51.5 / 47.5    unit
+//    1024     96  150.0 / 144.3  102.8 / 101.7     100.6 / 80.2    66.3 / 60.3    unit
+//    2048     48  157.7 / 149.4  111.9 / 100.7     101.4 / 81.9    74.8 / 58.0    unit
+// With 32 rows a head (head_dim 128) both take longer: 128 x 72 40.5 / 35.0 and 36.6 / 34.3, 384 x
+// 192 161 / 158 and 111 / 118.  So the rule is off by up to a seventh near its threshold (128 x
+// 72), and it sees lengths only as max_seq_len: it loses a tenth for 256 equal sequences'
+// units, and without bound where 512, 768 or from 1024 units on hold one far longer sequence
+// (262144 tokens among 63 of 1000, 64 heads over 8: 1335 us; among 62, 504 units, 78).
 bool pays_line(int64_t units, int64_t tiles) {
     if (units >= kLineUnits) return false;
     const int64_t idle = units <= 256 ? 256 - units * 3 / 4 : (units + 255) / 256 * 256 - units;     // CUs
