@@ -144,3 +144,42 @@ def test_scores_past_a_weight_range(nq, hq, amp, bound):
     assert checked > 0.5 * q.shape[0] * hq
 
 
+
+
+# ------------------------------------------------------------------ Q's power of two
+@pytest.mark.parametrize("nq", [1, 6, 40])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ratio", [-20, -29, -33])
+def test_small_elements_beside_a_large_one(ratio, d, nq):
+    """One element of Q, whose keys are zero, 2^-ratio times the others, which make the scores:
+    they are exact down to 2^-31 of it, and off by at most 2^-39 of it below."""
+    dev = device()
+    announce(f"ratio 2^{ratio} d={d} nq={nq}")
+    c = Case([150, 70], [nq, 1], 4, 2, d, 16, seed=5, spare=0)
+    c.kc[..., 0] &= 0xF0                                          # element 0 of every key
+    q = np.clip(c.q.float().numpy(), -2, 2) * 2.0 ** ratio
+    q[..., 0] = 1.5
+    c.q = torch.from_numpy(q).bfloat16()
+    scale = 2.0 ** -ratio / math.sqrt(d)
+    call = c.run(dev)
+    r = mxq.mxq_attention_nvfp4(c.q.to(dev), call._cache, torch.from_numpy(c.table).to(dev),
+                                torch.tensor(c.lens, dtype=torch.int32, device=dev), torch.from_numpy(c.starts).to(dev),
+                                nq, max(c.lens), scale=scale, lse=True)
+    torch.cuda.synchronize()
+    want, lse, _, _ = su.attention_reference(su.f32_of_bf16(c.q), c.kc, c.ks, c.vc, c.vs, c.kg, c.vg, c.table, c.lens,
+                                             c.starts, scale)
+    k = np.abs(su.decode_rows(c.kc, c.ks)) * c.kg.astype(np.float64)[None, :, None, None]
+    v = np.abs(su.decode_rows(c.vc, c.vs)) * c.vg.astype(np.float64)[None, :, None, None]
+    # serve_util.attention_bounds, with the largest sums of any token, and beside a score's FP32
+    # roundings Q's: half of FP16's smallest step, 2^-25, where the largest element is at least
+    # 2^14, for every element that is not exact (all below 2^-31: 8 bits from 2^-24 on)
+    small = 2.0 * 2.0 ** ratio
+    q_off = 0.0 if ratio >= -24 else 2.0 ** -39 * 1.5
+    delta = ((d + 8) * 2.0 ** -24 * small + q_off) * k.sum(-1).max() * scale + 2.0 ** -22
+    e = v.max() * (2 * delta + 2.0 ** -11) * 1.05 + 2.0 ** -34 * v.max() * 150
+    off = np.abs(su.f32_of_bf16(r.out) - want)
+    assert (off <= 2.0 ** -8 * (np.abs(want) + e) + e).all(), off.max()
+    assert (np.abs(host(r.lse) - lse) <= delta + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)).all()
+    # (scores of zero, as of elements that were lost, would not pass)
+    seen = [n - k + 1 + i for n, k in zip(c.lens, c.nq) for i in range(k)]
+    assert np.abs(lse - np.log(seen)[:, None]).max() > 2 * delta + 2.0 ** -18
