@@ -418,8 +418,8 @@ mxq_status mxq_group_rht_quant_nvfp4_noalloc(const uint16_t* x_bf16, int64_t k,
  *   y_bf16        [m][ld_y] BF16(y) as well (a router's input), or NULL
  *   q_e4m3, ldq, scales, scale strides: as mxq_quant_fp8_1x128
  * Requirements: n % 128 == 0, n <= MXQ_RMSNORM_MAX_N and m < 2^22 (else
- * MXQ_ERR_UNSUPPORTED); BF16 strides multiples of 8, ldq of 16; pointers 16-byte aligned, scales 4-byte
- * aligned; options in {0, MXQ_FP8_UE8M0}.  m == 0 is a successful no-op.
+ * MXQ_ERR_UNSUPPORTED); BF16 strides multiples of 8, ldq of 16; pointers 16-byte
+ * aligned, scales 4-byte aligned; options in {0, MXQ_FP8_UE8M0}.  m == 0 is a successful no-op.
  * ------------------------------------------------------------------------- */
 #define MXQ_RMSNORM_MAX_N 32768
 mxq_status mxq_add_rmsnorm_quant_fp8(const uint16_t* x_bf16, int64_t ldx, const uint16_t* residual, int64_t ld_res,

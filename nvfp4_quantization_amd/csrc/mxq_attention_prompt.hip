@@ -29,8 +29,8 @@
 // thirds of the time, an operand read from it feeding 32 rows.  512 queries of 32 heads of 128
 // over 65536 tokens take 570 us, 961 TFLOP/s (a plain FP16 product of 8192^3: 1074 to 1109, by
 // card); two prompts of 4096 tokens 300 to 308 us, 892 to 916 TFLOP/s, and a quarter more when
-// the tiles of a sequence ran together, so that the last sequence's longest rows started last.  64 rows a wave (half the operand reads, one
-// wave a SIMD) were slower.
+// the tiles of a sequence ran together, so that the last sequence's longest rows started last.
+// 64 rows a wave (half the operand reads, one wave a SIMD) were slower.
 #include "mxq_attention_nvfp4.hpp"
 
 namespace mxq {
