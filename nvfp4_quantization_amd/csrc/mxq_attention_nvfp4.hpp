@@ -111,11 +111,12 @@ __device__ __forceinline__ float q_power(uint32_t top, float& inverse) {
     inverse = __builtin_bit_cast(float, (uint32_t)(e - 14 + 127) << 23);
     return __builtin_bit_cast(float, (uint32_t)(14 - e + 127) << 23);
 }
-// The factor on a row's scores.  Kept normal and finite: a masked score is -inf, and times
-// zero (queries of zeros under a small tensor scale) it would be NaN.  A factor raised to
-// 2^-126 stands for scores below 2^-90.
+// The factor on a row's scores: in binary64, since two of the three may leave binary32's range
+// where their product with the third does not.  Kept normal and finite: a masked score is -inf,
+// and times zero (queries of zeros under a small tensor scale) it would be NaN.  A factor raised
+// to 2^-126 stands for scores below 2^-90.
 __device__ __forceinline__ float score_factor(const AttnArgs& a, float inverse, float kg) {
-    return __builtin_fminf(__builtin_fmaxf(inverse * kg * a.scale_log2, 0x1p-126f), 0x1.fffffep+127f);
+    return __builtin_fminf(__builtin_fmaxf((float)(inverse * (kg * a.scale_log2)), 0x1p-126f), 0x1.fffffep+127f);
 }
 __device__ __forceinline__ f16x8 q_operand(const u32x4v& w, float up) {
     const uint32_t p[4] = {w.x, w.y, w.z, w.w};

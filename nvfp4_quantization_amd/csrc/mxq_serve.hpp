@@ -76,7 +76,7 @@ struct AttnArgs {
     int32_t total_q;
     int32_t max_q_len;
     int32_t window, sinks;
-    float scale_log2;                 // softmax_scale * log2(e)
+    double scale_log2;                // softmax_scale * log2(e)
     KvCache c;
     // the plan: a unit is (sequence, row tile, cached head) with tile_rows query rows.
     // Rows form: `splits` work-groups share the line of all units' tiles (one row tile);

@@ -305,7 +305,7 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
     a.max_q_len = (int32_t)(max_q_len < total_q ? max_q_len : total_q);
     a.window = window;
     a.sinks = sinks;
-    a.scale_log2 = softmax_scale * 1.44269504088896341f;
+    a.scale_log2 = (double)softmax_scale * 1.44269504088896341;
     a.c = c;
     if (c.num_pages == 0) a.table_pages = 0;                 // no page can be read: no tokens
     a.tile_rows = p.tile_rows;

@@ -183,3 +183,27 @@ def test_small_elements_beside_a_large_one(ratio, d, nq):
     # (scores of zero, as of elements that were lost, would not pass)
     seen = [n - k + 1 + i for n, k in zip(c.lens, c.nq) for i in range(k)]
     assert np.abs(lse - np.log(seen)[:, None]).max() > 2 * delta + 2.0 ** -18
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("q_power,kg_power,scale_power", [(-30, -100, 119), (-90, -50, 127), (120, -126, -6), (100, -3, -109),
+                                                          (-60, 100, -50), (110, -110, -12), (0, -126, 114)])
+def test_factors_that_cancel(q_power, kg_power, scale_power, nq):
+    """Queries, K's tensor scale and the softmax scale at far ends of their ranges whose product
+    is ordinary: no step between loses bits of it."""
+    dev = device()
+    announce(f"factors 2^{q_power} 2^{kg_power} 2^{scale_power} nq={nq}")
+    c = Case([100, 70], [nq, nq], 4, 2, 64, 16, seed=13)
+    c.kg[:] = np.array([1.0, 1.37]) * 2.0 ** kg_power
+    c.q = (c.q.double() * 2.0 ** q_power).bfloat16()
+    scale = float(np.float32(2.0 ** scale_power * 1.3))
+    call = c.run(dev)
+    r = mxq.mxq_attention_nvfp4(c.q.to(dev), call._cache, torch.from_numpy(c.table).to(dev),
+                                torch.tensor(c.lens, dtype=torch.int32, device=dev), torch.from_numpy(c.starts).to(dev),
+                                nq, 100, scale=scale, lse=True)
+    torch.cuda.synchronize()
+    want, lse, bo, bl = su.attention_reference(su.f32_of_bf16(c.q), c.kc, c.ks, c.vc, c.vs, c.kg, c.vg, c.table, c.lens,
+                                               c.starts, scale)
+    assert 0.1 < (lse.max() - lse.min()) < 1e4
+    assert (np.abs(su.f32_of_bf16(r.out) - want) <= bo).all()
+    assert (np.abs(host(r.lse) - lse) <= bl).all()
