@@ -528,7 +528,8 @@ mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_head
  * -inf) where it sees none.  Both products run on FP16 operands with FP32 accumulators;
  * scores, maxima and sums are FP32.  K and V without their tensor scales are exact in
  * FP16.  Q is taken times a power of two per row: elements down to 2^-31 of their row's
- * largest are exact, smaller ones off by at most 2^-39 of it.  The softmax weights are
+ * largest are exact, smaller ones off by at most 2^-39 of it (of 2^-100 in a row whose
+ * largest is below that).  The softmax weights are
  * rounded to FP16 (nearest-even) for the product with V, and not for their sum: each is
  * off by at most 2^-11 of itself, or by 2^-34 of its row's largest weight where that is
  * more.  out is rounded to BF16 once.  The order of the sums depends on the lengths and
