@@ -529,11 +529,11 @@ mxq_status mxq_rope_append_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_head
  * scores, maxima and sums are FP32.  K and V without their tensor scales are exact in
  * FP16.  Q is taken times a power of two per row: elements down to 2^-31 of their row's
  * largest are exact, smaller ones off by at most 2^-39 of it (of 2^-100 in a row whose
- * largest is below that).  The softmax weights are
- * rounded to FP16 (nearest-even) for the product with V, and not for their sum: each is
- * off by at most 2^-11 of itself, or by 2^-34 of its row's largest weight where that is
- * more.  out is rounded to BF16 once.  The order of the sums depends on the lengths and
- * on max_seq_len, not on what the arrays hold, and a call repeats bit for bit.
+ * largest is below that).  The softmax weights are rounded to FP16 (nearest-even) for
+ * the product with V, and not for their sum: each is off by at most 2^-11 of itself, or
+ * by 2^-34 of its row's largest weight where that is more.  out is rounded to BF16 once.
+ * The order of the sums depends on the lengths and on max_seq_len, not on what the
+ * arrays hold, and a call repeats bit for bit.
  * What a query does not see changes no bit of its output, whatever it holds (NaN scales
  * included).  A NaN K row it sees makes its output NaN; a NaN V block it sees makes
  * at least that block's 16 elements NaN.
