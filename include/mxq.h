@@ -22,6 +22,9 @@
  *   mxq_rope_append_nvfp4      rotary positions on Q and K, then K and V into a paged
  *                              NVFP4 cache
  *   mxq_attention_nvfp4        causal attention of ragged queries over that cache
+ *   mxq_page_keys_nvfp4        the mean key of every page that an append has filled
+ *   mxq_select_pages_nvfp4     the pages each query attends, by the scores of their mean keys
+ *   mxq_attention_pages_nvfp4  causal attention over listed pages alone
  *
  * Conventions shared by every entry point
  *  - Pointers named *_bf16 / codes / scales / workspace are DEVICE pointers; the
@@ -40,7 +43,8 @@
  *    unsupported request is an error, never a slower substitute.
  *  - Arithmetic is IEEE binary32 with one rounding per operation in the order
  *    stated below; every output is bit-exact with respect to that definition, but
- *    for those of mxq_attention_nvfp4, whose roundings are stated with it.
+ *    for those of the mxq_attention_* calls, whose roundings are stated with
+ *    mxq_attention_nvfp4.
  *
  * Sources of the operations (page, then section):
  *  - onnxruntime PR #33644, QMoE dynamic FP8 activation quantization,
@@ -576,6 +580,98 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
                                int64_t max_q_len, int64_t max_seq_len, float softmax_scale,
                                int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Mean keys of full pages, for the selection below: kept beside a cache, one per
+ * page and cached head, as 8-bit integers with an FP32 scale.
+ *   codes    device int8  [num_pages][kv_heads][head_dim], 16-byte aligned
+ *   scales   device FP32  [num_pages][kv_heads], 4-byte aligned
+ * The mean key is codes * scales.  Requirements: head_dim 64 or 128; page_size a
+ * power of two, 16 .. 512 (else MXQ_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int8_t* codes;
+    float* scales;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+} mxq_page_keys;
+
+/* The mean keys of the pages whose last row is among `slots`: with the slots of an
+ * append, called after it, every page that it filled (rows of a sequence arrive in
+ * order, so a page is full when its last row is written).  Slots that are negative or not
+ * below num_pages * page_size are padding, other rows change nothing.  For one page and
+ * head, over its page_size rows of K, with g = k_global[head]:
+ *   S[d]   = sum of 1024 * E2M1value(code) * E4M3value(scale)      (whole numbers, exact)
+ *   a      = max |S[d]|
+ *   codes[d] = the whole number nearest to 127 S[d] / a, the even one of two; 0 if a == 0
+ *   scales = F(fl64(fl64(a g) fl64(1 / (130048 page_size))))       (130048 = 127 * 1024)
+ * A page with a NaN block scale gets codes 0 and a NaN scale.
+ *   slots    device int64[tokens], 8-byte aligned
+ * The cache's and keys' num_pages, page_size, kv_heads and head_dim are the same (else
+ * MXQ_ERR_INVALID_ARGUMENT).  tokens == 0 is a successful no-op. */
+mxq_status mxq_page_keys_nvfp4(const mxq_nvfp4_kv* cache, const int64_t* slots, int64_t tokens,
+                               const mxq_page_keys* keys, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The pages that each query attends, for each cached head (its q_heads / kv_heads query
+ * heads share them).  Sequences, queries and positions as in mxq_attention_nvfp4: the
+ * query at position p sees pages 0 .. c = p / page_size of its sequence (counted along
+ * its row of block_table).  pages[query][head] holds them all, ascending, where
+ * c < top; else `top` of them, ascending: the first `first`, the last `last` (c among
+ * them) and of the others those with the highest scores, lower ones before higher ones
+ * where scores are equal.  Unused entries are -1.  The score of a page with mean key
+ * (codes, scale) for the group's query heads h:
+ *   s_h   = fl(max |q_h| * F(1/127));  i_h[d] = the whole number nearest to
+ *           fl(q_h[d] / s_h), the even one of two, held to [-127, 127]
+ *           (a row of zeros, or with an infinity or NaN: s_h = 0, i_h = 0)
+ *   score = fl(max over h of fl((sum of i_h[d] codes[d]) * s_h) * scale)
+ * (the sums are exact).  A NaN score, and that of a page number outside [0, num_pages),
+ * is below all others.  Only pages that are full are scored: `last` is at least 1.
+ *
+ *   q        [total_q][ld_q] BF16, head h at h * head_dim
+ *   pages    device int32 [total_q][kv_heads][top], 4-byte aligned; rows of queries
+ *            that belong to no sequence are left as they were
+ *   max_seq_len  an estimate of the longest cached length, which sizes what is held
+ *            of the scores (longer sequences are still right, only slower)
+ * block_table, table_pages, seq_lens and q_starts as in mxq_attention_nvfp4.
+ * Requirements: q_heads a multiple of kv_heads; 1 <= batch <= 65535; ld_q a multiple of
+ * 8 and at least q_heads * head_dim; q 16-byte aligned; first >= 0, last >= 1,
+ * first + last <= top; top <= 65536; total_q * q_heads < 2^31 and total_q * kv_heads
+ * below 2^24 (else MXQ_ERR_UNSUPPORTED).  total_q == 0 is a successful no-op.
+ * ------------------------------------------------------------------------- */
+mxq_status mxq_select_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q,
+                                  const mxq_page_keys* keys, const int32_t* block_table, int64_t ld_table,
+                                  int64_t table_pages, const int32_t* seq_lens, const int32_t* q_starts,
+                                  int64_t batch, int64_t max_seq_len, int32_t top, int32_t first, int32_t last,
+                                  int32_t* pages, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Causal attention over listed pages: the query at position p and the query heads of
+ * cached head k attend the tokens t <= p of the pages pages[query][k][0 .. top - 1] of
+ * their sequence (counted along its row of block_table, as mxq_select_pages_nvfp4 writes
+ * them); out = 0 and lse = -inf where there is none.  Entries that are negative or above
+ * p / page_size add nothing, in any place; a page that is listed twice counts twice.  The
+ * arithmetic, its roundings, what NaN scales and unreadable pages do, and the other
+ * arguments are those of mxq_attention_nvfp4; a query's list may be as long as it likes,
+ * and entries after the last that counts cost nothing.
+ *   pages    device int32 [total_q][kv_heads][top], 4-byte aligned
+ * workspace: device memory of mxq_attention_pages_nvfp4_workspace_size(...) bytes, as there.
+ * Requirements: those of mxq_attention_nvfp4 on q, out, the cache, the sequences and the
+ * scale; 1 <= top <= 65536, top * page_size <= 2^30 and total_q * kv_heads *
+ * ceil(q_heads / kv_heads / 32) below 2^24 (else MXQ_ERR_UNSUPPORTED).  total_q == 0 is a
+ * successful no-op.
+ * ------------------------------------------------------------------------- */
+size_t mxq_attention_pages_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                                int32_t page_size, int64_t total_q, int32_t top);
+
+mxq_status mxq_attention_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q,
+                                     uint16_t* out, int64_t ld_out, float* lse, const mxq_nvfp4_kv* cache,
+                                     const int32_t* block_table, int64_t ld_table, int64_t table_pages,
+                                     const int32_t* seq_lens, const int32_t* q_starts, int64_t batch,
+                                     const int32_t* pages, int32_t top, float softmax_scale, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 
 #ifdef __cplusplus

@@ -40,202 +40,11 @@
 // takes (262144 tokens among 63 of 1000: 1335 us for 375 MB).  Few or short
 // sequences are latency: one of 1000 tokens takes 9.6 us on 8 CUs, 2 of them until lengths,
 // page table and queries are there, 5 for two tiles a wave (the two waves of a SIMD take turns).
-#include "mxq_attention_nvfp4.hpp"
+#include "mxq_attention_tile.hpp"
 
 namespace mxq {
 
 namespace {
-
-struct Lane {
-    int lane, g, col;                 // g = lane / 16, col = lane % 16
-};
-
-// ---------------------------------------------------------------- a tile's loads
-// A tile's 64 tokens lie in G groups that share a page each: one where pages hold 64 tokens
-// or more, else four of 16 (a page of 32 holds two).  The group addresses are uniform.
-//
-// The table entries of a tile's groups, group lane % 4 in each lane (past the sequence the
-// last token's page: nothing of such tokens is used).
-__device__ __forceinline__ int32_t page_entries(const AttnArgs& a, const int32_t* table, int len, int tile, const Lane& L) {
-    return table[min(tile * 64 + 16 * (L.lane & 3), len - 1) >> a.c.page_shift];
-}
-
-// Where the groups lie (page 0 for a page that may not be read).
-template <int G>
-struct Place {
-    int64_t codes[G], scales[G];
-    uint32_t bad;                     // bit t: group t's page may not be read
-};
-template <int G>
-__device__ __forceinline__ Place<G> place(const AttnArgs& a, int32_t entries, int tile, const Lane& L) {
-    Place<G> p;
-    if constexpr (G == 1) {
-        const int32_t e = __builtin_amdgcn_readfirstlane(entries);
-        const bool ok = (uint32_t)e < (uint32_t)a.c.num_pages;
-        const int64_t page = ok ? e : 0, row = (tile * 64) & ((1 << a.c.page_shift) - 1);
-        p.bad = ok ? 0u : 1u;
-        p.codes[0] = page * a.c.cs_page + row * a.c.cs_tok;
-        p.scales[0] = page * a.c.ss_page + row * a.c.ss_tok;
-    } else {
-        // each lane its own group's offsets, then read from the first four: four times the
-        // above took 170 scalar instructions a tile, and drafts on pages of 16 25.1 us, not
-        // 22.7; one group's are as fast in the scalar unit
-        const bool ok = (uint32_t)entries < (uint32_t)a.c.num_pages;
-        const uint32_t page = ok ? (uint32_t)entries : 0u;
-        const uint32_t row = (uint32_t)(tile * 64 + 16 * (L.lane & 3)) & ((1u << a.c.page_shift) - 1);
-        const uint64_t codes = page * (uint64_t)a.c.cs_page + (uint64_t)row * (uint32_t)a.c.cs_tok;
-        const uint64_t scales = page * (uint64_t)a.c.ss_page + (uint64_t)row * (uint32_t)a.c.ss_tok;
-        p.bad = (uint32_t)__ballot(!ok) & 15u;
-#pragma unroll
-        for (int t = 0; t < G; ++t) {
-            p.codes[t] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)codes, t) |
-                                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(codes >> 32), t) << 32);
-            p.scales[t] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)scales, t) |
-                                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(scales >> 32), t) << 32);
-        }
-    }
-    return p;
-}
-
-// The cached head's arrays.
-struct Base {
-    const uint8_t *kc, *ks, *vc, *vs;
-};
-
-// This lane's bytes inside a group: K's codes D / 4 g .. of token col (of the tile's 16 t +
-// col with one group) and their scales; V's 16 codes-bytes of token lane / 4 (D = 64: lane /
-// 2) and load j's; the scales of token `lane`.
-template <int D, int G>
-struct Offsets {
-    uint32_t k[5 - G], ks[5 - G], v[G == 1 ? D / 32 : 1], vs;
-    __device__ __forceinline__ Offsets(const AttnArgs& a, const Lane& L) {
-        const uint32_t cs = (uint32_t)a.c.cs_tok, ss = (uint32_t)a.c.ss_tok;
-#pragma unroll
-        for (int t = 0; t < 5 - G; ++t) {
-            k[t] = (uint32_t)(16 * t + L.col) * cs + L.g * (D / 8);
-            ks[t] = (uint32_t)(16 * t + L.col) * ss + (D == 128 ? 4 * (L.g >> 1) : 0);
-        }
-        const int tok = D == 128 ? L.lane >> 2 : (L.lane >> 1) & (G == 1 ? 31 : 15);
-#pragma unroll
-        for (int j = 0; j < (G == 1 ? D / 32 : 1); ++j)
-            v[j] = (uint32_t)((D == 128 ? 16 : 32) * j + tok) * cs + 16 * (L.lane & (D == 128 ? 3 : 1));
-        vs = (uint32_t)(G == 1 ? L.lane : L.col) * ss;
-    }
-};
-
-// A lane's offset that the compiler does not know: it would widen it once, ahead of the loop,
-// and hold and add 64 bits in vector registers instead of the load's own base and offset.
-__device__ __forceinline__ uint32_t here(uint32_t off) {
-    asm("" : "+v"(off));
-    return off;
-}
-// The cache's codes are mostly read once, by one work-group: loads that pass them through the L2
-// without keeping them ("non-temporal") take 97 us instead of 110 for 64 sequences of 8192
-// tokens (604 MB).  Where 7168 of those are pages that all sequences share (84 MB in all),
-// loads that keep them are a little faster: 73 us against 76.
-template <typename T>
-__device__ __forceinline__ T stream(const uint8_t* base, uint32_t off) {
-    return __builtin_nontemporal_load(reinterpret_cast<const T*>(base + here(off)));
-}
-
-// (Named members: an array indexed in the score loop would end up in scratch.)
-template <int D>
-struct KRegs {
-    KWords<D> w0, w1, w2, w3;
-    uint32_t s0, s1, s2, s3;
-};
-// A dword with the scales (D = 128: of lanes g and g ^ 1; D = 64: of all four), shifted down
-// at its use: the compiler would copy the result of a smaller load, and wait for it there.
-__device__ __forceinline__ uint32_t k_scales(const uint8_t* p, uint32_t off) {
-    return *reinterpret_cast<const uint32_t*>(p + here(off));
-}
-template <int D, int G>
-__device__ __forceinline__ void load_k(const Base& a, const Place<G>& p, const Offsets<D, G>& o, KRegs<D>& r) {
-    // (which group and which offset: one of the two is always the first)
-    constexpr bool kOne = G == 1;
-    r.w0 = stream<KWords<D>>(a.kc + p.codes[0], o.k[0]);
-    r.w1 = stream<KWords<D>>(a.kc + p.codes[kOne ? 0 : 1], o.k[kOne ? 1 : 0]);
-    r.w2 = stream<KWords<D>>(a.kc + p.codes[kOne ? 0 : 2], o.k[kOne ? 2 : 0]);
-    r.w3 = stream<KWords<D>>(a.kc + p.codes[kOne ? 0 : 3], o.k[kOne ? 3 : 0]);
-    r.s0 = k_scales(a.ks + p.scales[0], o.ks[0]);
-    r.s1 = k_scales(a.ks + p.scales[kOne ? 0 : 1], o.ks[kOne ? 1 : 0]);
-    r.s2 = k_scales(a.ks + p.scales[kOne ? 0 : 2], o.ks[kOne ? 2 : 0]);
-    r.s3 = k_scales(a.ks + p.scales[kOne ? 0 : 3], o.ks[kOne ? 3 : 0]);
-}
-
-template <int D>
-struct VRegs {
-    u32x4v w[D / 32];
-    uint32_t s[D / 64];
-};
-template <int D, int G>
-__device__ __forceinline__ void load_v(const Base& a, const Place<G>& p, const Offsets<D, G>& o, const Lane& L, VRegs<D>& r) {
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-        if constexpr (G == 1)
-            r.w[j] = stream<u32x4v>(a.vc + p.codes[0], o.v[j]);
-        else if constexpr (D == 128)
-            r.w[j] = stream<u32x4v>(a.vc + p.codes[j], o.v[0]);
-        else
-            r.w[j] = stream<u32x4v>(a.vc + (L.lane < 32 ? p.codes[2 * j] : p.codes[2 * j + 1]), o.v[0]);
-    }
-    int64_t s = p.scales[0];
-    if constexpr (G == 4) {
-        const int64_t lo = L.g & 1 ? p.scales[1] : p.scales[0], hi = L.g & 1 ? p.scales[3] : p.scales[2];
-        s = L.g & 2 ? hi : lo;
-    }
-    const uint8_t* vs = a.vs + s + here(o.vs);
-    if constexpr (D == 128) {
-        const u32x2v w = *reinterpret_cast<const u32x2v*>(vs);
-        r.s[0] = w.x, r.s[1] = w.y;
-    } else {
-        r.s[0] = *reinterpret_cast<const uint32_t*>(vs);
-    }
-}
-
-// ---------------------------------------------------------------- LDS of one wave
-// V codes: load j's 64 x 16 bytes at j * kVJ (16 bytes of padding keep the tokens that a
-// transposing read touches in different banks); V scales as FP16 [D/16][64 tokens], lane
-// group g's 16 tokens together; a byte per token for NaN V blocks.
-constexpr int kVJ = 1024 + 16;
-template <int D>
-struct WaveLds {
-    static constexpr int kScales = (D / 32) * kVJ;
-    static constexpr int kNan = kScales + (D / 16) * 128;
-    static constexpr int kBytes = kNan + 64;
-};
-// The byte of V's LDS image where element tile dt of lane group g's token k starts.
-template <int D>
-__device__ __forceinline__ int v_addr(int g, int k, int dt) {
-    const int token = 16 * (k >> 2) + 4 * g + (k & 3);
-    if constexpr (D == 128) return (token >> 4) * kVJ + (token & 15) * 64 + 8 * dt;
-    return (token >> 5) * kVJ + (token & 31) * 32 + 8 * dt;
-}
-
-// The 16 tokens of element 16 dt + col of lane group g: codes, and the scales of half u.
-template <int D>
-__device__ __forceinline__ i32x2 v_codes(uint8_t* lds, const Lane& L, int dt) {
-    return __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i32x2*)(lds + v_addr<D>(L.g, L.col, dt)));
-}
-template <int D>
-__device__ __forceinline__ f16x8 v_scales(const uint8_t* lds, const Lane& L, int dt, int u) {
-    return *reinterpret_cast<const f16x8*>(lds + WaveLds<D>::kScales + dt * 128 + L.g * 32 + u * 16);
-}
-
-// FP16 scales of this lane's token into LDS (zero for a token that is not valid).
-template <int D>
-__device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[D / 64], bool valid, const Lane& L) {
-    f16* const p = reinterpret_cast<f16*>(lds + WaveLds<D>::kScales) + 16 * ((L.lane >> 2) & 3) + 4 * L.g + (L.lane & 3);
-#pragma unroll
-    for (int w = 0; w < D / 64; ++w) {
-        const uint32_t s = valid ? vs[w] : 0u;
-        const f16x2 a = e4m3_pair(s, false), b = e4m3_pair(s, true);
-        p[(4 * w + 0) * 64] = a.x;
-        p[(4 * w + 1) * 64] = a.y;
-        p[(4 * w + 2) * 64] = b.x;
-        p[(4 * w + 3) * 64] = b.y;
-    }
-}
 
 // ---------------------------------------------------------------- the line of tiles
 constexpr int kWideUnits = 256;       // units of their own that get a CU, and eight waves, each
@@ -593,86 +402,6 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
             ++b;
         }
     }
-}
-
-// Joins a query row's parts: W waves per row (a work-group has four).  Lanes first turn the
-// parts' maxima and sums into weights (LDS), then each wave adds every W-th part, all of a
-// lane's loads independent of one another.  parts: at most kMaxParts; part 0 at `first`, the
-// others `step` apart from `rest` on (rows).
-template <int D, int W>
-__device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int kvh, int64_t r, int parts, int64_t first,
-                                         int64_t rest, int64_t step) {
-    constexpr int kRows = 4 / W;                             // rows of a work-group
-    __shared__ float weight[kRows][kMaxParts];
-    __shared__ float wave_sum[4], wave_top[4];
-    __shared__ float part[4][D];
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int mine = tid / (64 * W), t = tid % (64 * W), w0 = wave % W;
-    const auto row_of = [&](int s) { return s == 0 ? first : rest + (s - 1) * step; };
-    // (the first parts' rows are on their way while the weights are made)
-    constexpr int kAhead = 8;
-    float ahead[kAhead][D / 64];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-        const float* src = a.part_o + row_of(min(w0 + W * j, parts - 1)) * D + lane * (D / 64);
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) ahead[j][e] = src[e];
-    }
-    const float vg = a.c.vg[kvh];
-    float2 ml[kMaxParts / (64 * W)];
-    float top = kFloor;
-#pragma unroll
-    for (int j = 0; j < kMaxParts / (64 * W); ++j) {
-        const int s = t + 64 * W * j;
-        ml[j] = s < parts ? a.part_ml[row_of(s)] : make_float2(kFloor, 0.0f);
-        top = __builtin_fmaxf(top, ml[j].x);
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) top = __builtin_fmaxf(top, shfl_xor_f32(top, o));
-    if (W > 1) {
-        if (lane == 0) wave_top[wave] = top;
-        __syncthreads();
-        top = __builtin_fmaxf(__builtin_fmaxf(wave_top[0], wave_top[1]), __builtin_fmaxf(wave_top[2], wave_top[3]));
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kMaxParts / (64 * W); ++j) {
-        const float f = __builtin_amdgcn_exp2f(ml[j].x - top);
-        weight[mine][t + 64 * W * j] = f;
-        sum += ml[j].y * f;
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) sum += shfl_xor_f32(sum, o);
-    if (W > 1) {
-        if (lane == 0) wave_sum[wave] = sum;
-        __syncthreads();
-        sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
-    }
-    float v[D / 64] = {};
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-        const float w = w0 + W * j < parts ? weight[mine][w0 + W * j] : 0.0f;
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) v[e] += w0 + W * j < parts ? ahead[j][e] * w : 0.0f;
-    }
-#pragma unroll 8
-    for (int s = w0 + W * kAhead; s < parts; s += W) {
-        const float w = weight[mine][s];
-        const float* src = a.part_o + row_of(s) * D + lane * (D / 64);
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) v[j] += src[j] * w;
-    }
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) part[wave][lane * (D / 64) + j] = v[j];
-    if (W > 1) __syncthreads();
-    if (t >= D / 4) return;
-    f32x4 y;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int d = 4 * t + j;
-        y[j] = W > 1 ? (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]) : part[wave][d];
-    }
-    store_finished<D>(a, seq, kvh, r, 4 * t, y, top, sum, vg);
 }
 
 // Rows of a unit on the line that can hold queries, a multiple of 4.

@@ -36,6 +36,33 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
     return s;
 }
 
+// The sequence and the position of one query (b = -1: a row of no sequence), searched by a whole
+// wave, 64 sequences a step.
+struct Query {
+    int b, pos;
+};
+template <typename Args>
+__device__ __forceinline__ Query query_of(const Args& a, int page_shift, int row) {
+    const int lane = (int)threadIdx.x & 63;
+    int lo = 0, n = a.batch;                                 // the last one that starts at or before row
+    for (int step = 64; step > 1;) {
+        step = (n + 63) >> 6;
+        const bool before = lane * step < n && a.q_starts[lo + lane * step] <= row;
+        const int k = __popcll(__ballot(before));
+        if (k == 0) return Query{-1, -1};
+        lo += (k - 1) * step;
+        n = min(step, n - (k - 1) * step);
+    }
+    const int64_t q0 = min(max(a.q_starts[lo], 0), a.total_q), q1 = min(max(a.q_starts[lo + 1], 0), a.total_q);
+    if (row < q0 || row >= q1) return Query{-1, -1};
+    const int64_t cap = min((int64_t)a.table_pages << page_shift, (int64_t)0x7FFFFF00);
+    const int64_t len = min((int64_t)max(a.seq_lens[lo], 0), cap);
+    Query r;
+    r.b = __builtin_amdgcn_readfirstlane(lo);
+    r.pos = __builtin_amdgcn_readfirstlane((int)max(len - (q1 - row), (int64_t)-1));
+    return r;
+}
+
 // The 64-token tiles that queries q_first .. q_last of a sequence see: with a window the
 // tiles of the first `sinks` tokens, then those from the first query's window on.
 struct Span {

@@ -1,6 +1,6 @@
 // mxq_serve.hpp -- launch descriptors of the serving calls (RMS norm -> FP8, rotary
-// append, attention over the NVFP4 cache), shared by mxq_serve_api.cpp and the kernel
-// translation units.
+// append, attention over the NVFP4 cache, page selection), shared by the host entry points
+// (mxq_serve_api.cpp, mxq_pages_api.cpp) and the kernel translation units.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -91,5 +91,46 @@ struct AttnArgs {
 hipError_t launch_attention_rows(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_prompt(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_join(const AttnArgs& a, hipStream_t stream);
+
+// ---------------------------------------------------------------- pages: mean keys, selection
+struct PageKeysArgs {
+    KvCache c;
+    const int64_t* slots;
+    int64_t tokens;
+    int8_t* codes;                    // [num_pages][kv_heads][head_dim]
+    float* scales;                    // [num_pages][kv_heads]
+    int32_t chunk;                    // slots a wave looks at, 1 .. 64
+};
+hipError_t launch_page_keys(const PageKeysArgs& a, hipStream_t stream);
+
+struct SelectArgs {
+    const uint16_t* q;
+    int64_t ld_q;
+    const int8_t* codes;
+    const float* scales;
+    int64_t num_pages;
+    const int32_t* table;
+    int64_t ld_table;
+    const int32_t* seq_lens;
+    const int32_t* q_starts;
+    int32_t* out;                     // [total_q][kv_heads][top]
+    int32_t table_pages, batch, total_q;
+    int32_t kv_heads, head_dim, group, page_shift;
+    int32_t top, first, last;
+    int32_t window;                   // candidates whose scores are held at a time
+};
+hipError_t launch_select_pages(const SelectArgs& a, hipStream_t stream);
+
+// Attention over listed pages: a unit is (query, cached head, tile of tile_rows rows of its
+// group), its list in `splits` pieces.  Parts: [piece][query row][head].
+struct PagesAttnArgs : AttnArgs {
+    const int32_t* pages;             // [total_q][kv_heads][top]
+    int32_t top;
+    int32_t waves;                    // of a work-group
+};
+hipError_t launch_attention_pages(const PagesAttnArgs& a, hipStream_t stream);
+
+// Joins `splits` parts of every query row and head, [part][query row][head].
+hipError_t launch_attention_join_rows(const AttnArgs& a, hipStream_t stream);
 
 }  // namespace mxq
