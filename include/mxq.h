@@ -22,6 +22,7 @@
  *   mxq_rope_append_nvfp4      rotary positions on Q and K, then K and V into a paged
  *                              NVFP4 cache
  *   mxq_attention_nvfp4        causal attention of ragged queries over that cache
+ *   mxq_attention_prefix_nvfp4 the same where groups of sequences share long prefixes
  *   mxq_page_keys_nvfp4        the mean key of every page that an append has filled
  *   mxq_select_pages_nvfp4     the pages each query attends, by the scores of their mean keys
  *   mxq_attention_pages_nvfp4  causal attention over listed pages alone
@@ -580,6 +581,44 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
                                int64_t max_q_len, int64_t max_seq_len, float softmax_scale,
                                int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The same attention (without a window) where groups of sequences share long prefixes: a
+ * system prompt, a document.  Each prefix is attended once for all queries of its group,
+ * so its tokens are read and dequantized once, not once per sequence.  Group g is the
+ * sequences group_starts[g] .. group_starts[g + 1] - 1; the first prefix_lens[b] tokens of
+ * sequence b are read through the pages of its group's first sequence (that row of
+ * block_table), the others through its own:
+ *   out = softmax(softmax_scale * q . k) . v over all tokens t <= p,
+ * 0 (and lse = -inf) where there are none.  The sequences of a group may share prefixes of
+ * different lengths, 0 among them; a prefix may end anywhere in a page, may be longer
+ * than the sequence's own seq_lens[b] (the query at position p then sees its first p + 1
+ * tokens), and what a sequence's own row of block_table says of shared tokens is not read.
+ * Arithmetic, roundings, NaN scales, unreadable pages and the other arguments as in
+ * mxq_attention_nvfp4; the order of the sums depends on the lengths, the groups and the
+ * estimates.
+ *   group_starts device int32[groups + 1], ascending; the first counts as 0 and the last
+ *                as batch
+ *   prefix_lens  device int32[batch]; held to [0, table_pages * page_size]
+ *   max_prefix_len, max_own_len  estimates of the longest prefix and the most tokens
+ *                behind one, which size the split (longer ones are still right)
+ * workspace: device memory of mxq_attention_prefix_nvfp4_workspace_size(...) bytes, as
+ * there (never 0 but for calls that do nothing or are refused).
+ * Requirements: as there; 1 <= groups <= 4096; in total fewer than 2^24 work-groups (two
+ * pieces of all rows: about total_q * q_heads / 128 + batch * kv_heads; else
+ * MXQ_ERR_UNSUPPORTED).  total_q == 0 or max_q_len == 0 is a successful no-op.
+ * ------------------------------------------------------------------------- */
+size_t mxq_attention_prefix_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,
+                                                 int64_t groups, int64_t total_q, int64_t max_q_len,
+                                                 int64_t max_prefix_len, int64_t max_own_len);
+
+mxq_status mxq_attention_prefix_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q,
+                                      uint16_t* out, int64_t ld_out, float* lse, const mxq_nvfp4_kv* cache,
+                                      const int32_t* block_table, int64_t ld_table, int64_t table_pages,
+                                      const int32_t* seq_lens, const int32_t* q_starts, int64_t batch,
+                                      const int32_t* group_starts, const int32_t* prefix_lens, int64_t groups,
+                                      int64_t max_q_len, int64_t max_prefix_len, int64_t max_own_len,
+                                      float softmax_scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Mean keys of full pages, for the selection below: kept beside a cache, one per

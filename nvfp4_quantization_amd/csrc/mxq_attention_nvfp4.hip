@@ -57,17 +57,6 @@ __device__ __forceinline__ int unit_length(const AttnArgs& a, const Seq& s) {
     const int nq = min(s.nq, a.max_q_len);
     return nq > 0 ? tile_span(a, s, 0, nq - 1).n + kUnitCost : 0;
 }
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);       // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);       // lane 15 of the row before, rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);       // lane 31, rows 2 and 3
-    return v;
-}
-
 }  // namespace
 
 // LINE: the units lie on the line.  (A kernel apart from units of their own, which then need

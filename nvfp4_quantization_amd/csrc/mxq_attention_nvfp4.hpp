@@ -36,10 +36,21 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
     return s;
 }
 
-// The sequence and the position of one query (b = -1: a row of no sequence), searched by a whole
-// wave, 64 sequences a step.
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);       // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);       // lane 15 of the row before, rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);       // lane 31, rows 2 and 3
+    return v;
+}
+
+// The sequence, the position and the place in its run of one query (b = -1: a row of no
+// sequence), searched by a whole wave, 64 sequences a step.
 struct Query {
-    int b, pos;
+    int b, pos, index;
 };
 template <typename Args>
 __device__ __forceinline__ Query query_of(const Args& a, int page_shift, int row) {
@@ -49,17 +60,18 @@ __device__ __forceinline__ Query query_of(const Args& a, int page_shift, int row
         step = (n + 63) >> 6;
         const bool before = lane * step < n && a.q_starts[lo + lane * step] <= row;
         const int k = __popcll(__ballot(before));
-        if (k == 0) return Query{-1, -1};
+        if (k == 0) return Query{-1, -1, 0};
         lo += (k - 1) * step;
         n = min(step, n - (k - 1) * step);
     }
     const int64_t q0 = min(max(a.q_starts[lo], 0), a.total_q), q1 = min(max(a.q_starts[lo + 1], 0), a.total_q);
-    if (row < q0 || row >= q1) return Query{-1, -1};
+    if (row < q0 || row >= q1) return Query{-1, -1, 0};
     const int64_t cap = min((int64_t)a.table_pages << page_shift, (int64_t)0x7FFFFF00);
     const int64_t len = min((int64_t)max(a.seq_lens[lo], 0), cap);
     Query r;
     r.b = __builtin_amdgcn_readfirstlane(lo);
     r.pos = __builtin_amdgcn_readfirstlane((int)max(len - (q1 - row), (int64_t)-1));
+    r.index = __builtin_amdgcn_readfirstlane((int)(row - q0));
     return r;
 }
 

@@ -197,7 +197,7 @@ __global__ __launch_bounds__(256) void k_attention_join_rows(const AttnArgs a) {
     if (row >= all) return;
     const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads);
     const Query at = query_of(a, a.c.page_shift, token);
-    if (at.b < 0) return;
+    if (at.b < 0 || at.index >= a.max_q_len) return;
     const int kvh = head / a.group;
     join_row<D, W>(a, Seq{0, token, 1}, kvh, head - kvh * a.group, a.splits, row, row + all, all);
 }

@@ -31,7 +31,10 @@
 // card); two prompts of 4096 tokens 300 to 308 us, 892 to 916 TFLOP/s, and a quarter more when
 // the tiles of a sequence ran together, so that the last sequence's longest rows started last.
 // 64 rows a wave (half the operand reads, one wave a SIMD) were slower.
+#include <type_traits>
+
 #include "mxq_attention_nvfp4.hpp"
+#include "mxq_attention_ranges.hpp"
 
 namespace mxq {
 
@@ -148,40 +151,62 @@ __device__ __forceinline__ void store_v(VImage<D>& lds, const Part<D>& r, int t,
 
 }  // namespace
 
-// A wave holds 32 query rows (lane column = row), a work-group 128.
-template <int D>
-__global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
+// A wave holds 32 query rows (lane column = row), a work-group 128.  RANGES: the units of
+// attention with shared prefixes (mxq_attention_ranges.hpp), whose rows see ranges of tokens.
+template <int D, bool RANGES>
+__global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditional_t<RANGES, PrefixAttnArgs, AttnArgs> a) {
     constexpr int kWaveRows = 32, kRowTile = 4 * kWaveRows;
     __shared__ KImage<D> k0, k1;
     __shared__ VImage<D> v0, v1;
+    __shared__ int limits[RANGES ? kRowTile : 1];
 
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
-    // later rows, which see more tiles, first for all sequences and heads: the last to start are
-    // the shortest (two prompts of 4096 tokens 298 us against 368 when it was brought in)
-    const int split = (int)(blockIdx.x % (unsigned)a.splits);
-    const int order = (int)(blockIdx.x / (unsigned)a.splits);
-    const int bhs = a.batch * a.c.kv_heads;
-    const int rt = a.row_tiles - 1 - order / bhs, bh = order % bhs;
-    const int b = bh / a.c.kv_heads, kvh = bh - b * a.c.kv_heads;
-    const int64_t unit = ((int64_t)b * a.row_tiles + rt) * a.c.kv_heads + kvh;
-    const Seq seq = sequence(a, b);
-    const int64_t r0 = (int64_t)rt * kRowTile;
-    const int rows = (int)min(min((int64_t)seq.nq, (int64_t)a.max_q_len) * a.group - r0, (int64_t)kRowTile);
-    if (rows <= 0) return;
-    const Span span = tile_span(a, seq, (int)(r0 / a.group), (int)((r0 + rows - 1) / a.group));
-    const int used = splits_used(a, span.n);
-    if (split >= used) return;
-    const int first = split * a.chunk, last = split == used - 1 ? span.n : first + a.chunk;
+    int split, b, kvh, rows, first, last, used;
+    int64_t unit, r0;
+    Seq seq;
+    Span span;
+    RangeUnit range;
+    if constexpr (RANGES) {
+        range = range_unit<kRowTile>(a, (int)blockIdx.x, limits);
+        if (range.rows <= 0) return;
+        kvh = range.kvh, rows = range.rows, r0 = 0;
+        first = range.first, last = range.last;
+        seq = Seq{range.len, range.start, 0};
+        span = Span{0, range.body, last, 0, 0};
+    } else {
+        // later rows, which see more tiles, first for all sequences and heads: the last to start are
+        // the shortest (two prompts of 4096 tokens 298 us against 368 when it was brought in)
+        split = (int)(blockIdx.x % (unsigned)a.splits);
+        const int order = (int)(blockIdx.x / (unsigned)a.splits);
+        const int bhs = a.batch * a.c.kv_heads;
+        const int rt = a.row_tiles - 1 - order / bhs, bh = order % bhs;
+        b = bh / a.c.kv_heads, kvh = bh - b * a.c.kv_heads;
+        unit = ((int64_t)b * a.row_tiles + rt) * a.c.kv_heads + kvh;
+        seq = sequence(a, b);
+        r0 = (int64_t)rt * kRowTile;
+        rows = (int)min(min((int64_t)seq.nq, (int64_t)a.max_q_len) * a.group - r0, (int64_t)kRowTile);
+        if (rows <= 0) return;
+        span = tile_span(a, seq, (int)(r0 / a.group), (int)((r0 + rows - 1) / a.group));
+        used = splits_used(a, span.n);
+        if (split >= used) return;
+        first = split * a.chunk, last = split == used - 1 ? span.n : first + a.chunk;
+    }
 
     // Q as the second operand of S^T = K Q^T: lane (col, h) holds elements 16 c + 8 h .. + 7 of
     // its row (the first row again past the last)
     f16x8 q[D / 16];
     const int row = wave * kWaveRows + col;
     const bool live = row < rows;
-    const int qi = (int)((r0 + (live ? row : 0)) / a.group);
-    const int head = kvh * a.group + (int)(r0 + (live ? row : 0) - (int64_t)qi * a.group);
-    const int pos = live ? max(seq.len - seq.nq + qi, -1) : -1;
+    int qi, head, pos, count = 0;                      // RANGES: the last token, and how many
+    if constexpr (RANGES) {
+        const RangeRow mine = range_row(a, range, limits, row);
+        qi = mine.query - range.start, head = mine.head, pos = mine.hi, count = mine.count;
+    } else {
+        qi = (int)((r0 + (live ? row : 0)) / a.group);
+        head = kvh * a.group + (int)(r0 + (live ? row : 0) - (int64_t)qi * a.group);
+        pos = live ? max(seq.len - seq.nq + qi, -1) : -1;
+    }
     float factor = 0.0f;
 
     f32x16 o[D / 32];
@@ -190,7 +215,11 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
 
-    const int32_t* const table = a.table + (int64_t)b * a.ld_table;
+    const int32_t* table;
+    if constexpr (RANGES)
+        table = range.table;
+    else
+        table = a.table + (int64_t)b * a.ld_table;
     const int my_tok = tid >> 2, part = tid & 3;
     const uint32_t code_at = (uint32_t)((my_tok & 15) * a.c.cs_tok + part * (D / 8));
     const uint32_t scale_at = (uint32_t)((my_tok & 15) * a.c.ss_tok + part * (D / 64));
@@ -202,8 +231,11 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
     const auto spot_of = [&](int32_t entry, int i) { return spot(a, __builtin_amdgcn_readfirstlane(entry), token(i), kvh); };
     const auto valid = [&](int i) { return token(i) + (my_tok & 15) < seq.len; };
     // the positions of this wave's rows, for its masks
-    const int w_lo = max(seq.len - seq.nq + (int)((r0 + wave * kWaveRows) / a.group), -1);
-    const int w_hi = max(seq.len - seq.nq + (int)((r0 + min(wave * kWaveRows + kWaveRows - 1, rows - 1)) / a.group), -1);
+    int w_lo = 0, w_hi = 0;
+    if constexpr (!RANGES) {
+        w_lo = max(seq.len - seq.nq + (int)((r0 + wave * kWaveRows) / a.group), -1);
+        w_hi = max(seq.len - seq.nq + (int)((r0 + min(wave * kWaveRows + kWaveRows - 1, rows - 1)) / a.group), -1);
+    }
 
     constexpr int kProducts = D / 8, kAhead = 4;       // with K, and with V, per tile
     const int k_lane = col * kPitchK<D> + 16 * h;
@@ -303,7 +335,17 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
             entry = entry_of(i + 3);
         }
         // masks only where an edge crosses the tile for this wave's rows
-        if (t0 + 63 > w_lo || (a.window && t0 <= (int64_t)w_hi - a.window))
+        if constexpr (RANGES) {
+            if (t0 + 63 > range.min_hi || t0 < range.low) {
+                int ago = pos - t0 - 4 * h;
+                asm("" : "+v"(ago));                   // (or a difference per element is held across the tiles)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const bool seen = (uint32_t)(ago - (8 * (e >> 2) + (e & 3))) < (uint32_t)count;
+                    x[e >> 4][e & 15] = seen ? x[e >> 4][e & 15] : -__builtin_inff();
+                }
+            }
+        } else if (t0 + 63 > w_lo || (a.window && t0 <= (int64_t)w_hi - a.window))
             each_seen<32>(a, pos, t0 + 4 * h, [](int e) { return 8 * (e >> 2) + (e & 3); },
                           [&](int e, bool seen) { x[e >> 4][e & 15] = seen ? x[e >> 4][e & 15] : -__builtin_inff(); });
         if (noted.x | noted.y | noted.z | noted.w) {   // (rare) note the NaN V blocks this lane sees
@@ -313,7 +355,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
                 const uint32_t w = *reinterpret_cast<const uint32_t*>(vn.nan + 4 * (tok - t0));
                 const uint32_t blocks = D == 128 ? (w & 3u) | (w >> 6 & 0xCu) | (w >> 12 & 0x30u) | (w >> 18 & 0xC0u)
                                                  : (w & 1u) | (w >> 7 & 2u) | (w >> 14 & 4u) | (w >> 21 & 8u);
-                nan_blocks |= sees(a, pos, tok) ? blocks : 0u;
+                const bool seen = RANGES ? in_range(pos, count, tok) : sees(a, pos, tok);
+                nan_blocks |= seen ? blocks : 0u;
             }
         }
         float top = x[0][0];
@@ -406,7 +449,9 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
             const f32x4 y = {o[dt][e], o[dt][e + 1], o[dt][e + 2], o[dt][e + 3]};
-            if (used == 1)
+            if constexpr (RANGES)
+                store_part<D>(a, ((int64_t)range.part * a.total_q + seq.start + qi) * a.q_heads + head, 32 * dt + 2 * e + 4 * h, y, m, l);
+            else if (used == 1)
                 store_finished<D>(a, seq, kvh, r0 + row, 32 * dt + 2 * e + 4 * h, y, m, l, vg);
             else
                 store_part<D>(a, (unit * a.splits + split) * kRowTile + row, 32 * dt + 2 * e + 4 * h, y, m, l);
@@ -416,9 +461,17 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const AttnArgs a) {
 hipError_t launch_attention_prompt(const AttnArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.batch * a.row_tiles * a.c.kv_heads * a.splits));
     if (a.c.head_dim == 128)
-        hipLaunchKernelGGL(k_attention_prompt<128>, grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_prompt<128, false>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL(k_attention_prompt<64>, grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_prompt<64, false>), grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+hipError_t launch_attention_ranges_prompt(const PrefixAttnArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.prefix_blocks + a.own_blocks));
+    if (a.c.head_dim == 128)
+        hipLaunchKernelGGL((k_attention_prompt<128, true>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_attention_prompt<64, true>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -70,6 +70,53 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
     return true;
 }
 
+// How attention with shared prefixes splits its work.  A group's rows over its prefix, and a
+// sequence's over its own tokens, come in tiles of 16, 32 or 128: the first two by the waves'
+// own tiles (both in one launch, of one size), 128 by the form for many rows.  Pieces of both
+// until the launch fills the chip.
+constexpr int64_t kMaxGroups = 4096;
+constexpr int64_t kGroups = 512;               // work-groups that the chip holds at once
+constexpr int64_t kMaxBlocks = 1 << 24;        // of 256 threads
+struct PrefixPlan {
+    int32_t prefix_rows, own_rows, row_tiles, prefix_splits, own_splits;
+    int64_t prefix_blocks, own_blocks;
+    size_t ml_offset, bytes;
+};
+int64_t pieces(int64_t units, int64_t tiles, int64_t least, int64_t most) {
+    int64_t s = kGroups / units;
+    if (s > tiles / least) s = tiles / least;
+    return s < 1 ? 1 : s > most ? most : s;
+}
+bool plan_prefix(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, int64_t groups, int64_t total_q, int64_t max_q,
+                 int64_t max_prefix, int64_t max_own, PrefixPlan* p) {
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (d != 64 && d != 128) || batch < 1 || batch > kMaxBatch ||
+        groups < 1 || groups > kMaxGroups || total_q < 1 || max_q < 1 || max_prefix < 0 || max_own < 0 ||
+        !product_below(total_q, q_heads, 1ll << 31))
+        return false;
+    if (max_q > total_q) max_q = total_q;
+    if (max_prefix > (1ll << 31)) max_prefix = 1ll << 31;
+    if (max_own > (1ll << 31)) max_own = 1ll << 31;
+    const auto size = [](int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 128; };
+    const int64_t group = q_heads / kv_heads, per_group = (total_q * group + groups - 1) / groups;
+    p->own_rows = size(max_q * group);
+    p->prefix_rows = p->own_rows == 128 ? 128 : size(per_group);
+    if (p->prefix_rows < 128) p->prefix_rows = p->own_rows = p->prefix_rows > p->own_rows ? p->prefix_rows : p->own_rows;
+    p->row_tiles = (int32_t)((max_q * group + p->own_rows - 1) / p->own_rows);
+    const int64_t own_units = batch * p->row_tiles * kv_heads;                                  // (below 2^48)
+    const int64_t prefix_units = (total_q * group / p->prefix_rows + groups) * kv_heads;        // at most
+    const int64_t usual = (per_group + p->prefix_rows - 1) / p->prefix_rows * groups * kv_heads;
+    if (own_units >= kMaxBlocks || prefix_units >= kMaxBlocks) return false;
+    p->prefix_splits = (int32_t)pieces(usual, (max_prefix + 63) / 64, 4, 256);
+    p->own_splits = (int32_t)pieces(own_units, (max_own + 63) / 64 + 1, 8, 128);
+    p->prefix_blocks = prefix_units * p->prefix_splits;
+    p->own_blocks = own_units * p->own_splits;
+    if (p->prefix_blocks + p->own_blocks >= kMaxBlocks) return false;
+    const int64_t parts = total_q * q_heads * (p->prefix_splits + p->own_splits);
+    p->ml_offset = (size_t)(parts * d * 4);
+    p->bytes = (size_t)round256((int64_t)p->ml_offset + parts * 8);
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -193,7 +240,7 @@ mxq_status mxq_attention_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_
     a.batch = (int32_t)batch;
     a.q_heads = q_heads;
     a.group = q_heads / c.kv_heads;
-    a.total_q = (int32_t)total_q;
+    a.total_q = a.max_q_len = (int32_t)total_q;
     a.scale_log2 = (double)softmax_scale * 1.44269504088896341;
     a.c = c;
     a.tile_rows = p.tile_rows;
@@ -208,6 +255,88 @@ mxq_status mxq_attention_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_
     if (mxq::launch_attention_pages(a, hs) != hipSuccess) return MXQ_ERR_HIP;
     if (p.splits > 1 && mxq::launch_attention_join_rows(a, hs) != hipSuccess) return MXQ_ERR_HIP;
     return MXQ_OK;
+}
+
+size_t mxq_attention_prefix_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,
+                                                 int64_t groups, int64_t total_q, int64_t max_q_len, int64_t max_prefix_len,
+                                                 int64_t max_own_len) {
+    PrefixPlan p;
+    return plan_prefix(q_heads, kv_heads, head_dim, batch, groups, total_q, max_q_len, max_prefix_len, max_own_len, &p) ? p.bytes
+                                                                                                                         : 0;
+}
+
+mxq_status mxq_attention_prefix_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q, uint16_t* out,
+                                      int64_t ld_out, float* lse, const mxq_nvfp4_kv* cache, const int32_t* block_table,
+                                      int64_t ld_table, int64_t table_pages, const int32_t* seq_lens, const int32_t* q_starts,
+                                      int64_t batch, const int32_t* group_starts, const int32_t* prefix_lens, int64_t groups,
+                                      int64_t max_q_len, int64_t max_prefix_len, int64_t max_own_len, float softmax_scale,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+    mxq::KvCache c;
+    mxq_status st = check_cache(cache, &c);
+    if (st != MXQ_OK) return st;
+    if (q_heads < 1 || q_heads % c.kv_heads != 0 || total_q < 0 || batch < 1 || groups < 1 || max_q_len < 0 ||
+        max_prefix_len < 0 || max_own_len < 0 || table_pages < 0 || ld_table < table_pages)
+        return MXQ_ERR_INVALID_ARGUMENT;
+    if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return MXQ_ERR_INVALID_ARGUMENT;
+    const int64_t width = (int64_t)q_heads * c.head_dim;
+    if (ld_q < width || ld_out < width) return MXQ_ERR_INVALID_ARGUMENT;
+    if (ld_q % 8 != 0 || ld_out % 8 != 0) return MXQ_ERR_MISALIGNED;
+    if (total_q == 0 || max_q_len == 0) return MXQ_OK;
+    if (!q || !out || !group_starts || !prefix_lens) return MXQ_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(group_starts, 4) || !aligned(prefix_lens, 4))
+        return MXQ_ERR_MISALIGNED;
+    st = check_sequences(total_q, q_heads, block_table, ld_table, table_pages, seq_lens, q_starts, batch);
+    if (st != MXQ_OK) return st;
+    PrefixPlan p;
+    if (!extent_ok(total_q, ld_q, width) || !extent_ok(total_q, ld_out, width) || max_q_len > kMaxRows ||
+        !plan_prefix(q_heads, c.kv_heads, c.head_dim, batch, groups, total_q, max_q_len, max_prefix_len, max_own_len, &p))
+        return MXQ_ERR_UNSUPPORTED;
+    if (!workspace) return MXQ_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < p.bytes) return MXQ_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 256)) return MXQ_ERR_MISALIGNED;
+    mxq::PrefixAttnArgs a{};
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.ld_q = ld_q;
+    a.ld_out = ld_out;
+    a.table = block_table;
+    a.ld_table = ld_table;
+    a.seq_lens = seq_lens;
+    a.q_starts = q_starts;
+    a.table_pages = c.num_pages == 0 ? 0 : (int32_t)table_pages;         // no page: no tokens
+    a.batch = (int32_t)batch;
+    a.q_heads = q_heads;
+    a.group = q_heads / c.kv_heads;
+    a.total_q = (int32_t)total_q;
+    a.max_q_len = (int32_t)(max_q_len < total_q ? max_q_len : total_q);
+    a.scale_log2 = (double)softmax_scale * 1.44269504088896341;
+    a.c = c;
+    a.row_tiles = p.row_tiles;
+    a.splits = p.own_splits + p.prefix_splits;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.ml_offset);
+    a.group_starts = group_starts;
+    a.prefix_lens = prefix_lens;
+    a.groups = (int32_t)groups;
+    a.own_splits = p.own_splits;
+    a.prefix_splits = p.prefix_splits;
+    a.prefix_blocks = (int32_t)p.prefix_blocks;
+    a.own_blocks = (int32_t)p.own_blocks;
+    a.tile_rows = p.own_rows;
+    hipStream_t const hs = static_cast<hipStream_t>(stream);
+    if (p.own_rows == p.prefix_rows) {
+        if ((p.own_rows == 128 ? mxq::launch_attention_ranges_prompt(a, hs) : mxq::launch_attention_ranges_rows(a, hs)) != hipSuccess)
+            return MXQ_ERR_HIP;
+    } else {
+        mxq::PrefixAttnArgs part = a;
+        part.own_blocks = 0;
+        if (mxq::launch_attention_ranges_prompt(part, hs) != hipSuccess) return MXQ_ERR_HIP;
+        part = a;
+        part.prefix_blocks = 0;
+        if (mxq::launch_attention_ranges_rows(part, hs) != hipSuccess) return MXQ_ERR_HIP;
+    }
+    return mxq::launch_attention_join_rows(a, hs) == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
 }
 
 }  // extern "C"

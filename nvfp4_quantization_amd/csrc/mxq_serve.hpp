@@ -130,6 +130,22 @@ struct PagesAttnArgs : AttnArgs {
 };
 hipError_t launch_attention_pages(const PagesAttnArgs& a, hipStream_t stream);
 
+// Attention with shared prefixes: per group of sequences, its rows over the first tokens that
+// they share, read through its first sequence's pages (units (group, row tile, cached head)
+// first), and per sequence its own tokens from there on (units (sequence, row tile, cached
+// head)), each in pieces.  Parts: [own pieces, then prefix pieces][query row][head]; splits
+// counts both.
+struct PrefixAttnArgs : AttnArgs {
+    const int32_t* group_starts;
+    const int32_t* prefix_lens;       // per sequence
+    int32_t groups;
+    int32_t own_splits, prefix_splits;
+    int32_t prefix_blocks;            // the launch's first work-groups take units of the prefixes ...
+    int32_t own_blocks;               // ... and these units of sequences' own tokens
+};
+hipError_t launch_attention_ranges_rows(const PrefixAttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_ranges_prompt(const PrefixAttnArgs& a, hipStream_t stream);
+
 // Joins `splits` parts of every query row and head, [part][query row][head].
 hipError_t launch_attention_join_rows(const AttnArgs& a, hipStream_t stream);
 

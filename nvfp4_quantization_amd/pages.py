@@ -1,5 +1,5 @@
-"""The serving calls for long and shared contexts: mean keys of a cache's pages, the pages
-each query attends, and attention over those alone.  Prepared calls (classes) and the functions
+"""The serving calls for long and shared contexts: attention with shared prefixes; mean keys
+of a cache's pages, the pages each query attends, and attention over those alone.  Prepared calls (classes) and the functions
 of the C names, as in serve.py."""
 from __future__ import annotations
 
@@ -56,6 +56,65 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, dev) -> Optional[to
     if not _need(workspace, "workspace", (torch.uint8,), dev, 1).is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace
+
+
+# ---------------------------------------------------------------------------- shared prefixes
+def mxq_attention_prefix_nvfp4_workspace_size(q_heads: int, kv_heads: int, head_dim: int, batch: int, groups: int,
+                                              total_q: int, max_q_len: int, max_prefix_len: int, max_own_len: int) -> int:
+    return int(lib().mxq_attention_prefix_nvfp4_workspace_size(q_heads, kv_heads, head_dim, batch, groups, total_q, max_q_len,
+                                                               max_prefix_len, max_own_len))
+
+
+class AttentionPrefixNVFP4(_Prepared):
+    """A prepared attention call where groups of sequences share prefixes.  group_starts:
+    int32 [groups + 1], the first sequence of each group and batch; prefix_lens: int32
+    [batch], the tokens of each sequence that are read through the pages of its group's
+    first.  max_prefix_len, max_own_len (default: what the table can hold) bound the longest
+    prefix and the most tokens behind one, to plan the split for.  The rest as
+    AttentionNVFP4, without a window."""
+
+    def __init__(self, q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 q_starts: torch.Tensor, group_starts: torch.Tensor, prefix_lens: torch.Tensor, max_q_len: int,
+                 max_prefix_len: Optional[int] = None, max_own_len: Optional[int] = None, scale: Optional[float] = None,
+                 lse: bool = False, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+        dev, d = cache.device, cache.head_dim
+        ld_q = _head_rows(q, "q", None, d, dev)
+        total, hq = q.shape[0], q.shape[1]
+        out, ld_out, lse_t = _outputs(q, out, lse, d, dev)
+        batch, pages, ld_table = _sequences(block_table, seq_lens, q_starts, dev)
+        _need(group_starts, "group_starts", (torch.int32,), dev, 1)
+        _need(prefix_lens, "prefix_lens", (torch.int32,), dev, 1)
+        groups = group_starts.shape[0] - 1
+        if groups < 1 or prefix_lens.shape[0] != batch:
+            raise ValueError("group_starts is [groups + 1], prefix_lens [batch]")
+        if not group_starts.is_contiguous() or not prefix_lens.is_contiguous():
+            raise ValueError("group_starts and prefix_lens must be contiguous")
+        held = min(pages * cache.page_size, _MAX_SEQ_LEN)
+        max_prefix_len = held if max_prefix_len is None else max_prefix_len
+        max_own_len = held if max_own_len is None else max_own_len
+        need = mxq_attention_prefix_nvfp4_workspace_size(hq, cache.kv_heads, d, batch, groups, total, max_q_len,
+                                                         max_prefix_len, max_own_len)
+        self.workspace = workspace = _workspace(workspace, need, dev)
+        self.out, self._cache = AttentionResult(out, lse_t), cache
+        self._bind("mxq_attention_prefix_nvfp4", dev,
+                   (q, out, lse_t, block_table, seq_lens, q_starts, group_starts, prefix_lens, workspace, *cache.tensors()),
+                   _ptr(q), ld_q, hq, total, _ptr(out), ld_out, _ptr(lse_t), ctypes.byref(cache._c), _ptr(block_table),
+                   ld_table, pages, _ptr(seq_lens), _ptr(q_starts), batch, _ptr(group_starts), _ptr(prefix_lens), groups,
+                   max_q_len, max_prefix_len, max_own_len, float(scale) if scale is not None else 1.0 / math.sqrt(d),
+                   _ptr(workspace), workspace.numel() if workspace is not None else 0)
+
+    def __call__(self, stream=None) -> AttentionResult:
+        return self._launch(stream)
+
+
+def mxq_attention_prefix_nvfp4(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                               q_starts: torch.Tensor, group_starts: torch.Tensor, prefix_lens: torch.Tensor,
+                               max_q_len: int, max_prefix_len: Optional[int] = None, max_own_len: Optional[int] = None,
+                               scale: Optional[float] = None, lse: bool = False, out: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None, stream=None) -> AttentionResult:
+    """Causal attention of sequences whose groups share prefixes, each attended once."""
+    return AttentionPrefixNVFP4(q, cache, block_table, seq_lens, q_starts, group_starts, prefix_lens, max_q_len,
+                                max_prefix_len, max_own_len, scale, lse, out, workspace)(stream)
 
 
 # ---------------------------------------------------------------------------- mean keys

@@ -169,3 +169,57 @@ def test_binding_checks():
             mxq.SelectPagesNVFP4(q, keys_, table, lens, starts, top=4)
         with pytest.raises((TypeError, ValueError)):
             mxq.AttentionPagesNVFP4(q, cache, table, lens, starts, lists)
+
+
+# ------------------------------------------------------------------ shared prefixes
+def prefix(L, q=A, ld_q=1024, hq=8, total=4, out=A, ld_out=1024, lse=A, c=None, table=A, ld_table=5, table_pages=5, lens=A,
+           starts=A, batch=3, groups_at=A, prefix_at=A, groups=2, max_q=2, max_prefix=40, max_own=40, scale=0.1, ws=A,
+           ws_bytes=1 << 40):
+    return L.mxq_attention_prefix_nvfp4(q, ld_q, hq, total, out, ld_out, lse, ctypes.byref(c or kv()), table, ld_table,
+                                        table_pages, lens, starts, batch, groups_at, prefix_at, groups, max_q, max_prefix,
+                                        max_own, scale, ws, ws_bytes, None)
+
+
+@no_gpu
+def test_attention_prefix_errors(L):
+    assert prefix(L, total=0) == OK and prefix(L, max_q=0) == OK
+    for over in (dict(total=-1), dict(hq=0), dict(hq=7), dict(batch=0), dict(groups=0), dict(groups=-1), dict(max_q=-1),
+                 dict(max_prefix=-1), dict(max_own=-1), dict(table_pages=-1), dict(ld_table=4), dict(scale=0.0),
+                 dict(scale=float("nan")), dict(scale=float("inf")), dict(ld_q=1016), dict(ld_out=1016), dict(q=None),
+                 dict(out=None), dict(lens=None), dict(starts=None), dict(table=None), dict(groups_at=None),
+                 dict(prefix_at=None), dict(ws=None), dict(c=kv(k_codes=None))):
+        assert prefix(L, **over) == INVALID, over
+    for over in (dict(ld_q=1028), dict(ld_out=1028), dict(q=A + 8), dict(out=A + 8), dict(lse=A + 2), dict(groups_at=A + 2),
+                 dict(prefix_at=A + 1), dict(lens=A + 1), dict(starts=A + 2), dict(table=A + 2), dict(ws=A + 128)):
+        assert prefix(L, **over) == MISALIGNED, over
+    for over in (dict(batch=65536), dict(groups=4097), dict(total=1 << 28), dict(c=kv(head_dim=96)), dict(ld_q=1 << 40),
+                 dict(ld_out=1 << 40), dict(max_q=1 << 31), dict(total=1 << 27, max_q=1 << 27, batch=65535)):
+        assert prefix(L, **over) == UNSUPPORTED, over
+    need = mxq.mxq_attention_prefix_nvfp4_workspace_size(8, 2, 128, 3, 2, 4, 2, 40, 40)
+    assert need > 0 and need % 256 == 0
+    assert prefix(L, ws_bytes=need - 1) == WS_SMALL
+
+
+def test_attention_prefix_workspace_size(L):
+    size = mxq.mxq_attention_prefix_nvfp4_workspace_size
+    base = (8, 2, 128, 3, 2, 4, 2, 40, 40)
+    assert size(*base) >= 2 * 4 * 8 * (128 * 4 + 8)                      # a part of each kind at least
+    for i, v in ((0, 0), (1, 3), (2, 96), (3, 0), (3, 65536), (4, 0), (4, 4097), (5, 0), (5, 1 << 30), (6, 0), (7, -1), (8, -1)):
+        assert size(*base[:i], v, *base[i + 1:]) == 0
+    # no estimate, however large, plans more parts than a row's join takes
+    for tokens in (1, 1 << 20, 1 << 40, (1 << 63) - 1):
+        assert size(8, 2, 64, 1, 1, 1, 1, tokens, tokens) <= 512 * 8 * (64 * 4 + 8) + 255
+
+
+def test_prefix_binding_checks():
+    cache, _, q, seqs = cpu_case()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
+    good = (i32(0, 2), i32(4, 4), 2)
+    with pytest.raises(ValueError, match="expected a GPU"):
+        mxq.mxq_attention_prefix_nvfp4(q, cache, *seqs, *good)
+    for bad in ((i32(0), i32(4, 4), 2), (i32(0, 2), i32(4), 2), (i32(0, 2).long(), i32(4, 4), 2), (i32(0, 2), i32(4, 4).float(), 2),
+                (i32(0, 9, 2)[::2], i32(4, 4), 2), (i32(0, 2), i32(4, 4, 4)[::2], 2), ([0, 2], i32(4, 4), 2)):
+        with pytest.raises((TypeError, ValueError)):
+            mxq.AttentionPrefixNVFP4(q, cache, *seqs, *bad)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        mxq.AttentionPrefixNVFP4(q, cache, *seqs, *good, workspace=torch.zeros(512, dtype=torch.uint8)[::2])
