@@ -675,16 +675,21 @@ mxq_status mxq_page_keys_nvfp4(const mxq_nvfp4_kv* cache, const int64_t* slots, 
  *   max_seq_len  an estimate of the longest cached length, which sizes what is held
  *            of the scores (longer sequences are still right, only slower)
  * block_table, table_pages, seq_lens and q_starts as in mxq_attention_nvfp4.
+ * workspace: device memory of mxq_select_pages_nvfp4_workspace_size(...) bytes for the
+ * same shape (0: none needed, may be NULL), 256-byte aligned, any contents, as there.
  * Requirements: q_heads a multiple of kv_heads; 1 <= batch <= 65535; ld_q a multiple of
  * 8 and at least q_heads * head_dim; q 16-byte aligned; first >= 0, last >= 1,
  * first + last <= top; top <= 65536; total_q * q_heads < 2^31 and total_q * kv_heads
  * below 2^24 (else MXQ_ERR_UNSUPPORTED).  total_q == 0 is a successful no-op.
  * ------------------------------------------------------------------------- */
+size_t mxq_select_pages_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t page_size, int64_t batch,
+                                             int64_t total_q, int64_t max_seq_len);
+
 mxq_status mxq_select_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q,
                                   const mxq_page_keys* keys, const int32_t* block_table, int64_t ld_table,
                                   int64_t table_pages, const int32_t* seq_lens, const int32_t* q_starts,
                                   int64_t batch, int64_t max_seq_len, int32_t top, int32_t first, int32_t last,
-                                  int32_t* pages, void* stream);
+                                  int32_t* pages, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Causal attention over listed pages: the query at position p and the query heads of

@@ -31,6 +31,7 @@ EXPORTED = ("mxq_status_string", "mxq_version", "mxq_quant_fp8_1x128", "mxq_hada
             "mxq_quant_fp8_blockwise", "mxq_hadamard_quant_fp8_ex", "mxq_group_rht_quant_nvfp4_noalloc",
             "mxq_add_rmsnorm_quant_fp8", "mxq_rope_append_nvfp4", "mxq_attention_nvfp4_workspace_size",
             "mxq_attention_nvfp4", "mxq_page_keys_nvfp4", "mxq_select_pages_nvfp4",
+            "mxq_select_pages_nvfp4_workspace_size",
             "mxq_attention_pages_nvfp4_workspace_size", "mxq_attention_pages_nvfp4",
             "mxq_attention_prefix_nvfp4_workspace_size", "mxq_attention_prefix_nvfp4")
 MXQ_FP8_UE8M0 = 1
@@ -120,7 +121,10 @@ def lib() -> ctypes.CDLL:
         L.mxq_page_keys_nvfp4.restype = ctypes.c_int
         L.mxq_page_keys_nvfp4.argtypes = [p, p, i64, p, p]
         L.mxq_select_pages_nvfp4.restype = ctypes.c_int
-        L.mxq_select_pages_nvfp4.argtypes = [p, i64, i32, i64, p, p, i64, i64, p, p, i64, i64, i32, i32, i32, p, p]
+        L.mxq_select_pages_nvfp4.argtypes = [p, i64, i32, i64, p, p, i64, i64, p, p, i64, i64, i32, i32, i32, p, p,
+                                             ctypes.c_size_t, p]
+        L.mxq_select_pages_nvfp4_workspace_size.restype = ctypes.c_size_t
+        L.mxq_select_pages_nvfp4_workspace_size.argtypes = [i32, i32, i32, i64, i64, i64]
         L.mxq_attention_pages_nvfp4_workspace_size.restype = ctypes.c_size_t
         L.mxq_attention_pages_nvfp4_workspace_size.argtypes = [i32, i32, i32, i32, i64, i32]
         L.mxq_attention_pages_nvfp4.restype = ctypes.c_int
@@ -571,4 +575,4 @@ from .serve import (  # noqa: E402  (the serving calls use the helpers above)
 from .pages import (  # noqa: E402
     AttentionPagesNVFP4, AttentionPrefixNVFP4, PageKeys, PageKeysNVFP4, SelectPagesNVFP4, mxq_attention_pages_nvfp4,
     mxq_attention_pages_nvfp4_workspace_size, mxq_attention_prefix_nvfp4, mxq_attention_prefix_nvfp4_workspace_size,
-    mxq_page_keys_nvfp4, mxq_select_pages_nvfp4)
+    mxq_page_keys_nvfp4, mxq_select_pages_nvfp4, mxq_select_pages_nvfp4_workspace_size)

@@ -51,27 +51,39 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 // sequence), searched by a whole wave, 64 sequences a step.
 struct Query {
     int b, pos, index;
+    int len, left;                    // the sequence's length; queries of its run from this one on
 };
 template <typename Args>
 __device__ __forceinline__ Query query_of(const Args& a, int page_shift, int row) {
     const int lane = (int)threadIdx.x & 63;
-    int lo = 0, n = a.batch;                                 // the last one that starts at or before row
-    for (int step = 64; step > 1;) {
-        step = (n + 63) >> 6;
-        const bool before = lane * step < n && a.q_starts[lo + lane * step] <= row;
-        const int k = __popcll(__ballot(before));
-        if (k == 0) return Query{-1, -1, 0};
-        lo += (k - 1) * step;
-        n = min(step, n - (k - 1) * step);
+    // A query a sequence, or one sequence, is usual: that place is looked at beside the first
+    // step's (a memory latency less where it is right).
+    const int guess = min(row, a.batch - 1);
+    int lo = 0, n = a.batch, s0 = a.q_starts[guess], s1 = a.q_starts[guess + 1], held = a.seq_lens[guess];
+    int start = a.q_starts[min(lane * ((n + 63) >> 6), n)];
+    if (row < s0 || row >= s1) {
+        for (int step = 64; step > 1;) {                     // the last one that starts at or before row
+            step = (n + 63) >> 6;
+            if (n < a.batch) start = a.q_starts[min(lo + lane * step, a.batch)];
+            const int k = __popcll(__ballot(lane * step < n && start <= row));
+            if (k == 0) return Query{-1, -1, 0, 0, 0};
+            lo += (k - 1) * step;
+            n = min(step, n - (k - 1) * step);
+        }
+        s0 = a.q_starts[lo], s1 = a.q_starts[lo + 1], held = a.seq_lens[lo];
+    } else {
+        lo = guess;
     }
-    const int64_t q0 = min(max(a.q_starts[lo], 0), a.total_q), q1 = min(max(a.q_starts[lo + 1], 0), a.total_q);
-    if (row < q0 || row >= q1) return Query{-1, -1, 0};
+    const int64_t q0 = min(max(s0, 0), a.total_q), q1 = min(max(s1, 0), a.total_q);
+    if (row < q0 || row >= q1) return Query{-1, -1, 0, 0, 0};
     const int64_t cap = min((int64_t)a.table_pages << page_shift, (int64_t)0x7FFFFF00);
-    const int64_t len = min((int64_t)max(a.seq_lens[lo], 0), cap);
+    const int64_t len = min((int64_t)max(held, 0), cap);
     Query r;
     r.b = __builtin_amdgcn_readfirstlane(lo);
     r.pos = __builtin_amdgcn_readfirstlane((int)max(len - (q1 - row), (int64_t)-1));
     r.index = __builtin_amdgcn_readfirstlane((int)(row - q0));
+    r.len = __builtin_amdgcn_readfirstlane((int)len);
+    r.left = __builtin_amdgcn_readfirstlane((int)(q1 - row));
     return r;
 }
 

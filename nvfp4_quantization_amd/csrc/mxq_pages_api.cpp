@@ -41,6 +41,40 @@ int32_t log2_of(int32_t page_size) {
     return shift;
 }
 
+// How the selection spreads its work: queries of a work-group (for one cached head), and what is
+// held of their scores in LDS.  Several where sequences have long runs of queries, which then
+// share the mean keys that are read: two tiles of 16 rows, four of groups of more than 8 heads
+// (a query a wave then: 2000 queries of 8 heads of 128 over 1024 pages 63 us against 79 with four
+// tiles and 86 with eight; of 16 heads over 938 pages 34 with four, 58 with two).  Few queries with
+// many candidates: their scores are made by more work-groups, through the workspace (one query, 8
+// cached heads: 2048 candidates 13.5 us against 17.9, 8192 16 against 41).
+constexpr int64_t kHeldScores = 14336;         // 56 KB, of one query
+constexpr int64_t kHeldScoresRun = 12288;      // 48 KB, of several (whose waves need more beside them)
+struct SelectPlan {
+    int32_t window, tokens, waves, splits;
+    int64_t order_stride;
+    size_t bytes;
+};
+SelectPlan plan_select(int64_t group, int64_t kv_heads, int64_t page_size, int64_t batch, int64_t total_q, int64_t max_seq_len) {
+    SelectPlan p{};
+    const int64_t most = ((max_seq_len + page_size - 1) / page_size + 255) / 256 * 256;
+    const int64_t window = most < 256 ? 256 : most > kHeldScores ? kHeldScores : most;
+    int64_t padded = 1;
+    while (padded < group && padded < 16) padded *= 2;
+    int64_t tokens = group > 16 ? 1 : group > 8 ? 4 : 32 / padded;
+    while (tokens > 1 && (tokens * batch > total_q || tokens * window > kHeldScoresRun || total_q * kv_heads < tokens * 512)) tokens /= 2;
+    const int64_t units = total_q * kv_heads;
+    p.window = (int32_t)window;
+    p.tokens = (int32_t)tokens;
+    p.waves = tokens == 1 && units <= 256 ? 16 : 4;
+    if (p.waves == 16 && units <= 64 && window >= 1024) {
+        p.order_stride = window;
+        p.splits = (int32_t)(512 / units < window / 256 ? 512 / units : window / 256);
+        p.bytes = (size_t)round256(units * window * 4);
+    }
+    return p;
+}
+
 // How attention over listed pages splits its work: a unit is (query, cached head, 16 or 32 rows
 // of its group).
 struct PagesPlan {
@@ -142,10 +176,19 @@ mxq_status mxq_page_keys_nvfp4(const mxq_nvfp4_kv* cache, const int64_t* slots, 
     return mxq::launch_page_keys(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
 }
 
+size_t mxq_select_pages_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t page_size, int64_t batch,
+                                             int64_t total_q, int64_t max_seq_len) {
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || page_size < 16 || page_size > kMaxPageTokens ||
+        (page_size & (page_size - 1)) || batch < 1 || batch > kMaxBatch || total_q < 1 || max_seq_len < 0 ||
+        max_seq_len > kMaxRows || !product_below(total_q, q_heads, 1ll << 31))
+        return 0;
+    return plan_select(q_heads / kv_heads, kv_heads, page_size, batch, total_q, max_seq_len).bytes;
+}
+
 mxq_status mxq_select_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads, int64_t total_q, const mxq_page_keys* keys,
                                   const int32_t* block_table, int64_t ld_table, int64_t table_pages, const int32_t* seq_lens,
                                   const int32_t* q_starts, int64_t batch, int64_t max_seq_len, int32_t top, int32_t first,
-                                  int32_t last, int32_t* pages, void* stream) {
+                                  int32_t last, int32_t* pages, void* workspace, size_t workspace_bytes, void* stream) {
     mxq_status st = check_keys(keys);
     if (st != MXQ_OK) return st;
     if (q_heads < 1 || q_heads % keys->kv_heads != 0 || total_q < 0 || batch < 1 || max_seq_len < 0 || table_pages < 0 ||
@@ -161,11 +204,14 @@ mxq_status mxq_select_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_hea
     st = check_sequences(total_q, q_heads, block_table, ld_table, table_pages, seq_lens, q_starts, batch);
     if (st != MXQ_OK) return st;
     if (!extent_ok(total_q, ld_q, width) || !product_below(total_q * keys->kv_heads, top, kMaxElems) ||
-        !product_below(total_q, 256ll * keys->kv_heads, kMaxGridThreads))
+        max_seq_len > kMaxRows || !product_below(total_q, 256ll * keys->kv_heads, kMaxGridThreads))  // (1024 threads only for few)
         return MXQ_ERR_UNSUPPORTED;
-    int64_t window = (max_seq_len + keys->page_size - 1) / keys->page_size;
-    if (window > table_pages) window = table_pages;
-    window = window < 256 ? 256 : window > 15360 ? 15360 : window;      // 60 KB
+    const SelectPlan p = plan_select(q_heads / keys->kv_heads, keys->kv_heads, keys->page_size, batch, total_q, max_seq_len);
+    if (p.bytes > 0) {
+        if (!workspace) return MXQ_ERR_INVALID_ARGUMENT;
+        if (workspace_bytes < p.bytes) return MXQ_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned(workspace, 256)) return MXQ_ERR_MISALIGNED;
+    }
     mxq::SelectArgs a{};
     a.q = q;
     a.ld_q = ld_q;
@@ -187,7 +233,12 @@ mxq_status mxq_select_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_hea
     a.top = top;
     a.first = first;
     a.last = last;
-    a.window = (int32_t)window;
+    a.window = p.window;
+    a.tokens = p.tokens;
+    a.waves = p.waves;
+    a.orders = static_cast<uint32_t*>(p.bytes ? workspace : nullptr);
+    a.order_stride = (int32_t)p.order_stride;
+    a.splits = p.splits;
     return mxq::launch_select_pages(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
 }
 

@@ -117,7 +117,11 @@ struct SelectArgs {
     int32_t table_pages, batch, total_q;
     int32_t kv_heads, head_dim, group, page_shift;
     int32_t top, first, last;
-    int32_t window;                   // candidates whose scores are held at a time
+    int32_t window;                   // candidates whose scores are held of a query at a time, a multiple of 256
+    int32_t tokens;                   // queries of a work-group
+    int32_t waves;                    // of a work-group: 4, or 16 for one query
+    uint32_t* orders;                 // null, or workspace: [query][cached head][order_stride] scores, made
+    int32_t order_stride, splits;     // by `splits` work-groups each where there are no more candidates
 };
 hipError_t launch_select_pages(const SelectArgs& a, hipStream_t stream);
 

@@ -167,6 +167,11 @@ def mxq_page_keys_nvfp4(cache: NVFP4KVCache, slots: torch.Tensor, keys: PageKeys
 
 
 # ---------------------------------------------------------------------------- selection
+def mxq_select_pages_nvfp4_workspace_size(q_heads: int, kv_heads: int, page_size: int, batch: int, total_q: int,
+                                          max_seq_len: int) -> int:
+    return int(lib().mxq_select_pages_nvfp4_workspace_size(q_heads, kv_heads, page_size, batch, total_q, max_seq_len))
+
+
 class SelectPagesNVFP4(_Prepared):
     """A prepared selection of pages.  q: [total_q][q_heads][d] BF16 (rotated); block_table,
     seq_lens, q_starts: as for attention.  Each query and cached head gets at most `top`
@@ -178,7 +183,7 @@ class SelectPagesNVFP4(_Prepared):
 
     def __init__(self, q: torch.Tensor, keys: PageKeys, block_table: torch.Tensor, seq_lens: torch.Tensor,
                  q_starts: torch.Tensor, top: int, first: int = 1, last: int = 2, max_seq_len: Optional[int] = None,
-                 out: Optional[torch.Tensor] = None):
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
         dev, d = keys.device, keys.head_dim
         ld_q = _head_rows(q, "q", None, d, dev)
         total, hq = q.shape[0], q.shape[1]
@@ -192,10 +197,13 @@ class SelectPagesNVFP4(_Prepared):
         _need(out, "out", (torch.int32,), dev, 3)
         if tuple(out.shape) != shape or not out.is_contiguous():
             raise ValueError(f"out must be {list(shape)}, contiguous")
+        need = mxq_select_pages_nvfp4_workspace_size(hq, keys.kv_heads, keys.page_size, batch, total, max_seq_len)
+        self.workspace = workspace = _workspace(workspace, need, dev)
         self.out, self._keys = out, keys
-        self._bind("mxq_select_pages_nvfp4", dev, (q, keys.codes, keys.scales, block_table, seq_lens, q_starts, out),
+        self._bind("mxq_select_pages_nvfp4", dev, (q, keys.codes, keys.scales, block_table, seq_lens, q_starts, out, workspace),
                    _ptr(q), ld_q, hq, total, ctypes.byref(keys._c), _ptr(block_table), ld_table, pages, _ptr(seq_lens),
-                   _ptr(q_starts), batch, max_seq_len, top, first, last, _ptr(out))
+                   _ptr(q_starts), batch, max_seq_len, top, first, last, _ptr(out), _ptr(workspace),
+                   workspace.numel() if workspace is not None else 0)
 
     def __call__(self, stream=None) -> torch.Tensor:
         return self._launch(stream)
@@ -204,9 +212,9 @@ class SelectPagesNVFP4(_Prepared):
 def mxq_select_pages_nvfp4(q: torch.Tensor, keys: PageKeys, block_table: torch.Tensor, seq_lens: torch.Tensor,
                            q_starts: torch.Tensor, top: int, first: int = 1, last: int = 2,
                            max_seq_len: Optional[int] = None, out: Optional[torch.Tensor] = None,
-                           stream=None) -> torch.Tensor:
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The pages that each query attends, for each cached head."""
-    return SelectPagesNVFP4(q, keys, block_table, seq_lens, q_starts, top, first, last, max_seq_len, out)(stream)
+    return SelectPagesNVFP4(q, keys, block_table, seq_lens, q_starts, top, first, last, max_seq_len, out, workspace)(stream)
 
 
 # ---------------------------------------------------------------------------- attention over them

@@ -445,3 +445,27 @@ def test_decoding_with_selected_pages(graph):
         assert_same("pages", host(select.out), pages)
         want = cu.attention_over(c, cu.listed_tokens(c, pages), 1 / math.sqrt(d))
         cu.check_attention(f32(attend.out.out), host(attend.out.lse), want)
+
+
+# runs of queries long enough that a work-group takes several, whose scores share the keys
+@pytest.mark.parametrize("lens,nq,hq,hk,d,page,top,first,last", [
+    ([3000, 700], [500, 44], 4, 4, 64, 16, 20, 1, 2),                    # one row a head: 64 queries
+    ([1500, 900], [300, 260], 8, 4, 128, 16, 12, 0, 1),                  # two
+    ([2500], [530], 24, 6, 64, 16, 70, 2, 4),                            # four; just 64 to choose
+    ([2600, 40, 1999], [300, 40, 211], 18, 3, 128, 16, 80, 1, 3),        # six of eight; more than 64
+    ([1999, 1200], [251, 300], 22, 2, 64, 16, 9, 1, 2),                  # eleven of sixteen
+    ([5200], [1100], 16, 1, 128, 16, 40, 1, 2),
+    ([9000, 40], [300, 1], 4, 4, 64, 16, 30, 1, 2),                      # scores of 512 candidates a query
+])
+def test_select_long_runs(lens, nq, hq, hk, d, page, top, first, last):
+    dev = device()
+    announce(f"select runs lens={lens} nq={nq} hq={hq} hk={hk} d={d} page={page} top={top} first={first} last={last}")
+    c = cu.Sequences(lens, nq, hq, hk, d, page, seed=sum(lens), before=5, behind=3)
+    codes, scales = random_keys(c, 1)
+    run_select(c, codes, scales, top, first, last, dev)
+    run_select(c, codes, scales, top, first, last, dev, max_seq_len=page)
+    codes[:, :, 1:] = 0                                                  # ties: a score of few values
+    run_select(c, np.sign(codes), np.ones_like(scales), top, first, last, dev)
+    c.table[:, ::7] = c.pages
+    scales[::5] = np.nan
+    run_select(c, codes, scales, top, first, last, dev)

@@ -42,9 +42,9 @@ def page_keys(L, c=None, slots=A, tokens=4, k=None):
 
 
 def select(L, q=A, ld_q=1024, hq=8, total=4, k=None, table=A, ld_table=5, pages=5, lens=A, starts=A, batch=2, max_len=80,
-           top=4, first=1, last=2, out=A):
+           top=4, first=1, last=2, out=A, ws=None, ws_bytes=0):
     return L.mxq_select_pages_nvfp4(q, ld_q, hq, total, ctypes.byref(k or keys()), table, ld_table, pages, lens, starts, batch,
-                                    max_len, top, first, last, out, None)
+                                    max_len, top, first, last, out, ws, ws_bytes, None)
 
 
 def attend(L, q=A, ld_q=1024, hq=8, total=400, out=A, ld_out=1024, lse=A, c=None, table=A, ld_table=5, table_pages=5, lens=A,
@@ -86,8 +86,20 @@ def test_select_errors(L):
         assert select(L, **over) == MISALIGNED, over
     for over in (dict(top=65537), dict(batch=65536), dict(total=1 << 28), dict(total=1 << 23), dict(k=keys(page_size=1024)),
                  dict(k=keys(head_dim=32)), dict(ld_q=1 << 40), dict(ld_table=1 << 40),
-                 dict(pages=1 << 31, ld_table=1 << 31)):
+                 dict(pages=1 << 31, ld_table=1 << 31), dict(max_len=1 << 31)):
         assert select(L, **over) == UNSUPPORTED, over
+    # one query of a long sequence: its scores go through the workspace
+    need = mxq.mxq_select_pages_nvfp4_workspace_size(8, 2, 16, 1, 1, 100000)
+    assert need > 0 and need % 256 == 0
+    long = dict(total=1, batch=1, max_len=100000)
+    assert select(L, **long) == INVALID
+    assert select(L, **long, ws=A, ws_bytes=need - 1) == WS_SMALL
+    assert select(L, **long, ws=A + 128, ws_bytes=need) == MISALIGNED
+    size = mxq.mxq_select_pages_nvfp4_workspace_size
+    assert size(8, 2, 16, 64, 64, 1000) == 0
+    for args in ((0, 1, 16, 1, 1, 99999), (8, 3, 16, 1, 1, 99999), (8, 2, 24, 1, 1, 99999), (8, 2, 1024, 1, 1, 1 << 30),
+                 (8, 2, 16, 0, 1, 99999), (8, 2, 16, 1, 0, 99999), (8, 2, 16, 1, 1, -1), (8, 2, 16, 1, 1, 1 << 31)):
+        assert size(*args) == 0
 
 
 @no_gpu
