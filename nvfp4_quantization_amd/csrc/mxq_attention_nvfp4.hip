@@ -416,7 +416,8 @@ __global__ __launch_bounds__(256) void k_attention_join_units(const AttnArgs a) 
     if (d.y == 0) return;                                    // finished by its work-group
     const int64_t at = 2 * (int64_t)d.x;
     const int parts = d.y;
-    join_row<D, W>(a, seq, kvh, r, parts, (at + 1) * a.tile_rows + r, (at + 2) * a.tile_rows + r, 2 * (int64_t)a.tile_rows);
+    join_row<D, W>(a, seq, kvh, r, parts, (at + 1) * a.tile_rows + r, (at + 2) * a.tile_rows + r, 2 * (int64_t)a.tile_rows,
+                   [] { return true; });
 }
 
 // The units that the form for many rows split.  W as above.
@@ -436,7 +437,7 @@ __global__ __launch_bounds__(256) void k_attention_join_splits(const AttnArgs a)
     const int used = splits_used(a, tile_span(a, seq, (int)(r0 / a.group), (int)(r1 / a.group)).n);
     if (used <= 1) return;                                   // written by the first kernel
     const int64_t at = unit * a.splits * a.tile_rows + r;
-    join_row<D, W>(a, seq, kvh, r0 + r, used, at, at + a.tile_rows, a.tile_rows);
+    join_row<D, W>(a, seq, kvh, r0 + r, used, at, at + a.tile_rows, a.tile_rows, [] { return true; });
 }
 
 // Units of their own get eight waves each while there is a CU for each: 256 units of 96

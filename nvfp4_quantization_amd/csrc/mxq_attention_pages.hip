@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 8 / W) void k_attention_pages(
     waves_meet<D, NT, W>(wave, L, m, l, o, nan_blocks, join);
     if constexpr (W == 1) __syncthreads();
     const Seq seq{0, token, 1};
-    waves_join<D, NT, W>(lds, wave, L, rows, o, join, [&](int r, int d0, const f32x4& y, float top, float total) {
+    waves_join<D, NT, W>([&](int w) { return lds + w * kJoin; }, wave, L, rows, o, join, [&](int r, int d0, const f32x4& y, float top, float total) {
         const int in_group = rt * (NT * 16) + r;
         if (a.splits == 1)
             store_finished<D>(a, seq, kvh, in_group, d0, y, top, total, vg);
@@ -196,22 +196,25 @@ __global__ __launch_bounds__(256) void k_attention_join_rows(const AttnArgs a) {
     const int64_t row = (int64_t)blockIdx.x * (4 / W) + (threadIdx.x >> 6) / W, all = (int64_t)a.total_q * a.q_heads;
     if (row >= all) return;
     const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads);
-    const Query at = query_of(a, a.c.page_shift, token);
-    if (at.b < 0 || at.index >= a.max_q_len) return;
     const int kvh = head / a.group;
-    join_row<D, W>(a, Seq{0, token, 1}, kvh, head - kvh * a.group, a.splits, row, row + all, all);
+    join_row<D, W>(a, Seq{0, token, 1}, kvh, head - kvh * a.group, a.splits, row, row + all, all, [&] {
+        const Query at = query_of(a, a.c.page_shift, token);
+        return at.b >= 0 && at.index < a.max_q_len;
+    });
 }
 
 hipError_t launch_attention_join_rows(const AttnArgs& a, hipStream_t stream) {
     const int64_t rows = (int64_t)a.total_q * a.q_heads;
     const dim3 each((unsigned)rows), four((unsigned)((rows + 3) / 4));
+    // few rows get four waves each (128 of 10 parts 20.8 us in all against 19.9), many a wave (4096 of
+    // 17: 62.8 against 59.3)
     if (a.c.head_dim == 128) {
-        if (a.splits > 4)
+        if (a.splits > 64 || (a.splits > 4 && rows < 1024))
             hipLaunchKernelGGL((k_attention_join_rows<128, 4>), each, dim3(256), 0, stream, a);
         else
             hipLaunchKernelGGL((k_attention_join_rows<128, 1>), four, dim3(256), 0, stream, a);
     } else {
-        if (a.splits > 4)
+        if (a.splits > 64 || (a.splits > 4 && rows < 1024))
             hipLaunchKernelGGL((k_attention_join_rows<64, 4>), each, dim3(256), 0, stream, a);
         else
             hipLaunchKernelGGL((k_attention_join_rows<64, 1>), four, dim3(256), 0, stream, a);

@@ -33,8 +33,7 @@
 // 64 rows a wave (half the operand reads, one wave a SIMD) were slower.
 #include <type_traits>
 
-#include "mxq_attention_nvfp4.hpp"
-#include "mxq_attention_ranges.hpp"
+#include "mxq_attention_ranges_rows.hpp"
 
 namespace mxq {
 
@@ -151,10 +150,17 @@ __device__ __forceinline__ void store_v(VImage<D>& lds, const Part<D>& r, int t,
 
 }  // namespace
 
-// A wave holds 32 query rows (lane column = row), a work-group 128.  RANGES: the units of
-// attention with shared prefixes (mxq_attention_ranges.hpp), whose rows see ranges of tokens.
-template <int D, bool RANGES>
-__global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditional_t<RANGES, PrefixAttnArgs, AttnArgs> a) {
+// How the prompt form is used: for whole sequences; for the units of attention with shared
+// prefixes (mxq_attention_ranges.hpp), whose rows see ranges of tokens; for those of the prefixes,
+// and beside them units of up to 16 or 32 rows over sequences' own tokens, a wave a tile, with pages
+// of 64 tokens and more or of fewer.  (In one launch: the products of the former run beside the
+// latter's loads.)
+enum PromptUse { kSequences, kRanges, kRanges16, kRanges16Short, kRanges32, kRanges32Short };
+
+// A wave holds 32 query rows (lane column = row), a work-group 128.
+template <int D, PromptUse USE>
+__global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditional_t<USE != kSequences, PrefixAttnArgs, AttnArgs> a) {
+    constexpr bool RANGES = USE != kSequences;
     constexpr int kWaveRows = 32, kRowTile = 4 * kWaveRows;
     __shared__ KImage<D> k0, k1;
     __shared__ VImage<D> v0, v1;
@@ -167,6 +173,19 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
     Seq seq;
     Span span;
     RangeUnit range;
+    if constexpr (USE > kRanges) {
+        if ((int)blockIdx.x >= a.prefix_blocks) {
+            constexpr int kNT = USE == kRanges16 || USE == kRanges16Short ? 1 : 2;
+            constexpr int kG = USE == kRanges16 || USE == kRanges32 ? 1 : 4;
+            constexpr int kArea = WaveLds<D>::kBytes > D * 64 ? WaveLds<D>::kBytes : D * 64;
+            static_assert(2 * kArea <= (int)sizeof(k0.b), "two waves' areas to an image of K");
+            __shared__ float2 join[4][kNT * 16];
+            const RangeUnit own = range_unit<kNT * 16>(a, (int)blockIdx.x, limits);
+            if (own.rows > 0)
+                range_rows<D, kNT, kG, 4>(a, own, limits, [&](int w) { return (w < 2 ? k0.b : k1.b) + (w & 1) * kArea; }, join);
+            return;
+        }
+    }
     if constexpr (RANGES) {
         range = range_unit<kRowTile>(a, (int)blockIdx.x, limits);
         if (range.rows <= 0) return;
@@ -461,17 +480,31 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
 hipError_t launch_attention_prompt(const AttnArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.batch * a.row_tiles * a.c.kv_heads * a.splits));
     if (a.c.head_dim == 128)
-        hipLaunchKernelGGL((k_attention_prompt<128, false>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_prompt<128, kSequences>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_attention_prompt<64, false>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_prompt<64, kSequences>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
-hipError_t launch_attention_ranges_prompt(const PrefixAttnArgs& a, hipStream_t stream) {
+template <int D>
+static void launch_ranges_prompt(const PrefixAttnArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)(a.prefix_blocks + a.own_blocks));
-    if (a.c.head_dim == 128)
-        hipLaunchKernelGGL((k_attention_prompt<128, true>), grid, dim3(256), 0, stream, a);
+    const bool pages64 = a.c.page_shift >= 6;
+    if (a.tile_rows == 128)
+        hipLaunchKernelGGL((k_attention_prompt<D, kRanges>), grid, dim3(256), 0, stream, a);
+    else if (a.tile_rows == 16 && pages64)
+        hipLaunchKernelGGL((k_attention_prompt<D, kRanges16>), grid, dim3(256), 0, stream, a);
+    else if (a.tile_rows == 16)
+        hipLaunchKernelGGL((k_attention_prompt<D, kRanges16Short>), grid, dim3(256), 0, stream, a);
+    else if (pages64)
+        hipLaunchKernelGGL((k_attention_prompt<D, kRanges32>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_attention_prompt<64, true>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_prompt<D, kRanges32Short>), grid, dim3(256), 0, stream, a);
+}
+hipError_t launch_attention_ranges_prompt(const PrefixAttnArgs& a, hipStream_t stream) {
+    if (a.c.head_dim == 128)
+        launch_ranges_prompt<128>(a, stream);
+    else
+        launch_ranges_prompt<64>(a, stream);
     return hipGetLastError();
 }
 

@@ -318,8 +318,9 @@ __device__ __forceinline__ void waves_meet(int wave, const Lane& L, const float 
         if (L.g == 0) join[wave][n * 16 + L.col] = make_float2(m[n], l[n]);
     }
 }
-template <int D, int NT, int W, typename Store>
-__device__ __forceinline__ void waves_join(uint8_t* lds, int wave, const Lane& L, int rows, const f32x4 (&o)[NT][D / 16],
+// area(wave): LDS of D / 16 KB each.
+template <int D, int NT, int W, typename Area, typename Store>
+__device__ __forceinline__ void waves_join(Area&& area, int wave, const Lane& L, int rows, const f32x4 (&o)[NT][D / 16],
                                            const float2 (&join)[W][NT * 16], Store&& store) {
     if constexpr (W == 1) {                                  // (a wave alone: from its registers)
 #pragma unroll
@@ -333,10 +334,10 @@ __device__ __forceinline__ void waves_join(uint8_t* lds, int wave, const Lane& L
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        f32x4* const all = reinterpret_cast<f32x4*>(lds);
+        const auto at = [&](int w, int dt) { return reinterpret_cast<f32x4*>(area(w)) + dt * 64 + L.lane; };
         if (n) __syncthreads();
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) all[(wave * (D / 16) + dt) * 64 + L.lane] = o[n][dt];
+        for (int dt = 0; dt < D / 16; ++dt) *at(wave, dt) = o[n][dt];
         __syncthreads();
         float top = kFloor, total = 0.0f, f[W];
 #pragma unroll
@@ -350,9 +351,9 @@ __device__ __forceinline__ void waves_join(uint8_t* lds, int wave, const Lane& L
         for (int j = 0; j < (D / 16 + W - 1) / W; ++j) {
             const int dt = wave * (D / 16 >= W ? D / 16 / W : 1) + j;
             if (dt >= D / 16) break;
-            f32x4 y = all[dt * 64 + L.lane] * f[0];
+            f32x4 y = *at(0, dt) * f[0];
 #pragma unroll
-            for (int w = 1; w < W; ++w) y += all[(w * (D / 16) + dt) * 64 + L.lane] * f[w];
+            for (int w = 1; w < W; ++w) y += *at(w, dt) * f[w];
             const int d0 = 16 * dt + 4 * L.g;
             if (n * 16 + L.col < rows) store(n * 16 + L.col, d0, y, top, total);
         }
@@ -363,10 +364,11 @@ __device__ __forceinline__ void waves_join(uint8_t* lds, int wave, const Lane& L
 // Joins a query row's parts: W waves per row (a work-group has four).  Lanes first turn the
 // parts' maxima and sums into weights (LDS), then each wave adds every W-th part, all of a
 // lane's loads independent of one another.  parts: at most kMaxParts; part 0 at `first`, the
-// others `step` apart from `rest` on (rows).
-template <int D, int W>
+// others `step` apart from `rest` on (rows).  live(): whether the row is one (asked once the
+// first parts are on their way).
+template <int D, int W, typename Live>
 __device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int kvh, int64_t r, int parts, int64_t first,
-                                         int64_t rest, int64_t step) {
+                                         int64_t rest, int64_t step, Live&& live) {
     constexpr int kRows = 4 / W;                             // rows of a work-group
     __shared__ float weight[kRows][kMaxParts];
     __shared__ float wave_sum[4], wave_top[4];
@@ -399,6 +401,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int 
         __syncthreads();
         top = __builtin_fmaxf(__builtin_fmaxf(wave_top[0], wave_top[1]), __builtin_fmaxf(wave_top[2], wave_top[3]));
     }
+    if (!live()) return;
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < kMaxParts / (64 * W); ++j) {

@@ -19,48 +19,88 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// The maximum over aligned sets of N lanes (8 or 16), in all of them.
+template <int N>
+__device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
+    static_assert(N == 8 || N == 16, "");
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));            // lane ^ 1
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));            // lane ^ 2
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));           // mirrored halves of 16
+    if constexpr (N == 16) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));
+    return v;
+}
+// The maximum over a wave (uniform).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max_lanes<16>(v);
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, true));     // the row before, rows 1 and 3
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, true));     // lane 31, rows 2 and 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // ---------------------------------------------------------------- mean keys
-// One page of one head, by a wave: D / 32 lanes hold a token's 32 codes each.
+// One page of one head, by a wave: D / 16 lanes hold a token's 16-element blocks.
 template <int D>
 __device__ __forceinline__ void page_key(const PageKeysArgs& a, int page, int head, int lane) {
-    constexpr int kLanes = D / 32, kStep = 64 / kLanes;     // lanes of a token, tokens of a load
+    constexpr int kLanes = D / 16, kStep = 64 / kLanes;     // lanes of a token, tokens of a load
     const int size = 1 << a.c.page_shift;
-    const uint8_t* const codes = a.c.kc + page * a.c.cs_page + head * a.c.cs_head + 16 * (lane % kLanes);
-    const uint8_t* const scales = a.c.ks + page * a.c.ss_page + head * a.c.ss_head + 2 * (lane % kLanes);
+    const uint8_t* const codes = a.c.kc + page * a.c.cs_page + head * a.c.cs_head + 8 * (lane % kLanes);
+    const uint8_t* const scales = a.c.ks + page * a.c.ss_page + head * a.c.ss_head + lane % kLanes;
     const float g = a.c.kg[head];
-    int sum[32] = {};
+    const uint32_t code_step = (uint32_t)a.c.cs_tok, scale_step = (uint32_t)a.c.ss_tok;
+    // four tokens a lane at a time, the next four on their way
+    u32x2v w[4];
+    uint32_t s[4];
+    const auto load = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t t = (uint32_t)min(t0 + kStep * i + lane / kLanes, size - 1);
+            w[i] = *reinterpret_cast<const u32x2v*>(codes + t * (uint64_t)code_step);
+            s[i] = scales[t * (uint64_t)scale_step];
+        }
+    };
+    load(0);
+    int sum[16] = {};
     bool bad = false;
     for (int t0 = 0; t0 < size; t0 += 4 * kStep) {
-        u32x4v w[4];
-        uint32_t s[4];
+        u32x2v x[4];
+        uint32_t by[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = min(t0 + kStep * i + lane / kLanes, size - 1);
-            w[i] = *reinterpret_cast<const u32x4v*>(codes + t * a.c.cs_tok);
-            s[i] = *reinterpret_cast<const uint16_t*>(scales + t * a.c.ss_tok);
+            x[i] = w[i];
+            by[i] = t0 + kStep * i + lane / kLanes < size ? s[i] : 0u;
+            bad |= (by[i] & 0x7Fu) == 0x7Fu;
         }
-        float part[32] = {};
+        load(t0 + 4 * kStep);                               // (past the end the last row again)
+        float part[16] = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bool in = t0 + kStep * i + lane / kLanes < size;
-            bad |= (((s[i] & 0x7F7Fu) + 0x0101u) & 0x8080u) != 0;
-            const f16x2 f = e4m3_pair(in ? s[i] : 0u, false);
-            const uint32_t p[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            const f16 f = e4m3_pair(by[i], false).x;
+            const f16x8 lo = e2m1_8(x[i].x), hi = e2m1_8(x[i].y);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const f16x8 e = e2m1_8(p[c]);
-                const f16 by = c < 2 ? f.x : f.y;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) part[8 * c + j] = __builtin_fmaf((float)e[j], (float)by, part[8 * c + j]);
+            for (int j = 0; j < 8; ++j) {
+                part[j] = __builtin_fmaf((float)lo[j], (float)f, part[j]);
+                part[8 + j] = __builtin_fmaf((float)hi[j], (float)f, part[8 + j]);
             }
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sum[e] += (int)(part[e] * 1024.0f);
+        for (int e = 0; e < 16; ++e) sum[e] += (int)(part[e] * 1024.0f);
     }
     // over the lanes of the same elements, half of the elements handed over at each step
-    int first = 32 * (lane % kLanes);
+    int first = 16 * (lane % kLanes);
 #pragma unroll
-    for (int bit = 32, n = 16; bit >= kLanes; bit >>= 1, n >>= 1) {
+    for (int e = 0; e < 8; ++e) {
+        const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)sum[e], (uint32_t)sum[e + 8], false, false);
+        sum[e] = (int)(r[0] + r[1]);
+    }
+    first += lane & 32 ? 8 : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const auto r = __builtin_amdgcn_permlane16_swap((uint32_t)sum[e], (uint32_t)sum[e + 4], false, false);
+        sum[e] = (int)(r[0] + r[1]);
+    }
+    first += lane & 16 ? 4 : 0;
+#pragma unroll
+    for (int bit = 8, n = 2; bit >= kLanes; bit >>= 1, n >>= 1) {
         const bool upper = lane & bit;
 #pragma unroll
         for (int e = 0; e < n; ++e) {
@@ -73,8 +113,7 @@ __device__ __forceinline__ void page_key(const PageKeysArgs& a, int page, int he
     int top = 0;
 #pragma unroll
     for (int e = 0; e < kMine; ++e) top = max(top, abs(sum[e]));
-#pragma unroll
-    for (int bit = 1; bit < 64; bit <<= 1) top = max(top, __shfl_xor(top, bit, 64));
+    top = (int)wave_max((uint32_t)top);
     bad = __any(bad);
     const int64_t at = (int64_t)page * a.c.kv_heads + head;
     uint32_t out = 0;
@@ -128,24 +167,6 @@ __device__ __forceinline__ uint32_t order_of(float score) {
 }
 __device__ __forceinline__ float value_of(uint32_t order) {
     return __builtin_bit_cast(float, order & 0x80000000u ? order ^ 0x80000000u : ~order);
-}
-
-// The maximum over aligned sets of N lanes (8 or 16), in all of them.
-template <int N>
-__device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
-    static_assert(N == 8 || N == 16, "");
-    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));            // lane ^ 1
-    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));            // lane ^ 2
-    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));           // mirrored halves of 16
-    if constexpr (N == 16) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));
-    return v;
-}
-// The maximum over a wave (uniform).
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = max_lanes<16>(v);
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, true));     // the row before, rows 1 and 3
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, true));     // lane 31, rows 2 and 3
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // Rows of 16 lanes: a's maxima over rows 0, 1 and 2, 3 in rows 0 and 2, b's in rows 1 and 3.

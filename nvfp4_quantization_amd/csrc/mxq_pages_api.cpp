@@ -106,8 +106,19 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
 
 // How attention with shared prefixes splits its work.  A group's rows over its prefix, and a
 // sequence's over its own tokens, come in tiles of 16, 32 or 128: the first two by the waves'
-// own tiles (both in one launch, of one size), 128 by the form for many rows.  Pieces of both
-// until the launch fills the chip.
+// own tiles, 128 by the form for many rows, all in one launch.  Pieces of both until it fills the
+// chip.  Of the prefixes, in the form for many rows, a work-group a CU, where two would have few tiles
+// each (their rows' parts have to be written, read and joined) or the sequences' own tokens are as
+// much work, which then runs beside them.  Measured, one a CU / two, us (64 query heads over 8 of 128,
+// own tokens 50 to 400, the last row 500 to 4000):
+//   sequences  shared tokens                         taken
+//          16   16384    30.9 / 36.4                  one
+//          64    4096    32.8 / 39.7                  one
+//          64   16384    60.4 / 64.4                  one
+//          32   32768    59.9 / 58.9                  one
+//          32   65536   101.4 / 95.0                  two
+//          64   65536   186.1 / 161.3                 two
+//          64   32768   112.8 / 124.3 (much of own)   one
 constexpr int64_t kMaxGroups = 4096;
 constexpr int64_t kGroups = 512;               // work-groups that the chip holds at once
 constexpr int64_t kMaxBlocks = 1 << 24;        // of 256 threads
@@ -140,8 +151,11 @@ bool plan_prefix(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, in
     const int64_t prefix_units = (total_q * group / p->prefix_rows + groups) * kv_heads;        // at most
     const int64_t usual = (per_group + p->prefix_rows - 1) / p->prefix_rows * groups * kv_heads;
     if (own_units >= kMaxBlocks || prefix_units >= kMaxBlocks) return false;
-    p->prefix_splits = (int32_t)pieces(usual, (max_prefix + 63) / 64, 4, 256);
-    p->own_splits = (int32_t)pieces(own_units, (max_own + 63) / 64 + 1, 8, 128);
+    const int64_t tiles = (max_prefix + 63) / 64, own_tiles = (max_own + 63) / 64 + 1;
+    const bool half = p->prefix_rows == 128 && (!product_below(usual, tiles, 1ll << 60) || usual * tiles < 80 * d ||
+                                                own_units * own_tiles > usual * tiles);
+    p->prefix_splits = (int32_t)pieces(half ? 2 * usual : usual, tiles, 4, 256);
+    p->own_splits = (int32_t)pieces(own_units, own_tiles, 8, 128);
     p->prefix_blocks = prefix_units * p->prefix_splits;
     p->own_blocks = own_units * p->own_splits;
     if (p->prefix_blocks + p->own_blocks >= kMaxBlocks) return false;
@@ -376,17 +390,8 @@ mxq_status mxq_attention_prefix_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q
     a.own_blocks = (int32_t)p.own_blocks;
     a.tile_rows = p.own_rows;
     hipStream_t const hs = static_cast<hipStream_t>(stream);
-    if (p.own_rows == p.prefix_rows) {
-        if ((p.own_rows == 128 ? mxq::launch_attention_ranges_prompt(a, hs) : mxq::launch_attention_ranges_rows(a, hs)) != hipSuccess)
-            return MXQ_ERR_HIP;
-    } else {
-        mxq::PrefixAttnArgs part = a;
-        part.own_blocks = 0;
-        if (mxq::launch_attention_ranges_prompt(part, hs) != hipSuccess) return MXQ_ERR_HIP;
-        part = a;
-        part.prefix_blocks = 0;
-        if (mxq::launch_attention_ranges_rows(part, hs) != hipSuccess) return MXQ_ERR_HIP;
-    }
+    if ((p.prefix_rows == 128 ? mxq::launch_attention_ranges_prompt(a, hs) : mxq::launch_attention_ranges_rows(a, hs)) != hipSuccess)
+        return MXQ_ERR_HIP;
     return mxq::launch_attention_join_rows(a, hs) == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
 }
 
