@@ -43,47 +43,41 @@ template <int D>
 __device__ __forceinline__ void page_key(const PageKeysArgs& a, int page, int head, int lane) {
     constexpr int kLanes = D / 16, kStep = 64 / kLanes;     // lanes of a token, tokens of a load
     const int size = 1 << a.c.page_shift;
-    const uint8_t* const codes = a.c.kc + page * a.c.cs_page + head * a.c.cs_head + 8 * (lane % kLanes);
-    const uint8_t* const scales = a.c.ks + page * a.c.ss_page + head * a.c.ss_head + lane % kLanes;
+    const uint8_t* const codes = a.c.kc + page * a.c.cs_page + head * a.c.cs_head;
+    const uint8_t* const scales = a.c.ks + page * a.c.ss_page + head * a.c.ss_head;
+    const uint32_t code_at = (uint32_t)(lane / kLanes) * (uint32_t)a.c.cs_tok + 8 * (lane % kLanes);
+    const uint32_t scale_at = (uint32_t)(lane / kLanes) * (uint32_t)a.c.ss_tok + lane % kLanes;
     const float g = a.c.kg[head];
-    const uint32_t code_step = (uint32_t)a.c.cs_tok, scale_step = (uint32_t)a.c.ss_tok;
-    // four tokens a lane at a time, the next four on their way
-    u32x2v w[4];
-    uint32_t s[4];
-    const auto load = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t t = (uint32_t)min(t0 + kStep * i + lane / kLanes, size - 1);
-            w[i] = *reinterpret_cast<const u32x2v*>(codes + t * (uint64_t)code_step);
-            s[i] = scales[t * (uint64_t)scale_step];
-        }
-    };
-    load(0);
     int sum[16] = {};
-    bool bad = false;
-    for (int t0 = 0; t0 < size; t0 += 4 * kStep) {
-        u32x2v x[4];
-        uint32_t by[4];
+    float scale_sum = 0.0f;
+    // eight tokens a lane at a time, all of their loads at once (a page holds whole multiples of
+    // kStep tokens; past its end the last ones again, with zero scales)
+    for (int t0 = 0; t0 < size; t0 += 8 * kStep) {
+        u32x2v w[8];
+        uint32_t s[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = w[i];
-            by[i] = t0 + kStep * i + lane / kLanes < size ? s[i] : 0u;
-            bad |= (by[i] & 0x7Fu) == 0x7Fu;
+        for (int i = 0; i < 8; ++i) {
+            const int64_t t = min(t0 + kStep * i, size - kStep);
+            w[i] = *reinterpret_cast<const u32x2v*>(codes + t * a.c.cs_tok + code_at);
+            s[i] = (scales + t * a.c.ss_tok)[scale_at];
         }
-        load(t0 + 4 * kStep);                               // (past the end the last row again)
-        float part[16] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f16 f = e4m3_pair(by[i], false).x;
-            const f16x8 lo = e2m1_8(x[i].x), hi = e2m1_8(x[i].y);
+        for (int half = 0; half < 2; ++half) {
+            float part[16] = {};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                part[j] = __builtin_fmaf((float)lo[j], (float)f, part[j]);
-                part[8 + j] = __builtin_fmaf((float)hi[j], (float)f, part[8 + j]);
+            for (int i = 4 * half; i < 4 * half + 4; ++i) {
+                const float f = (float)e4m3_pair(t0 + kStep * i < size ? s[i] : 0u, false).x * 1024.0f;
+                scale_sum += f;                             // (NaN with any of them)
+                const f16x8 lo = e2m1_8(w[i].x), hi = e2m1_8(w[i].y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    part[j] = __builtin_fmaf((float)lo[j], f, part[j]);
+                    part[8 + j] = __builtin_fmaf((float)hi[j], f, part[8 + j]);
+                }
             }
-        }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] += (int)(part[e] * 1024.0f);
+            for (int e = 0; e < 16; ++e) sum[e] += (int)part[e];
+        }
     }
     // over the lanes of the same elements, half of the elements handed over at each step
     int first = 16 * (lane % kLanes);
@@ -99,22 +93,25 @@ __device__ __forceinline__ void page_key(const PageKeysArgs& a, int page, int he
         sum[e] = (int)(r[0] + r[1]);
     }
     first += lane & 16 ? 4 : 0;
-#pragma unroll
-    for (int bit = 8, n = 2; bit >= kLanes; bit >>= 1, n >>= 1) {
+    // (two steps written out: a loop over them would index the sums by a variable)
+    const auto hand_over = [&](int bit, int& a0, int& b0) {
         const bool upper = lane & bit;
-#pragma unroll
-        for (int e = 0; e < n; ++e) {
-            const int mine = upper ? sum[e + n] : sum[e], other = upper ? sum[e] : sum[e + n];
-            sum[e] = mine + __shfl_xor(other, bit, 64);
-        }
-        first += upper ? n : 0;
+        const int mine = upper ? b0 : a0, other = upper ? a0 : b0;
+        a0 = mine + __shfl_xor(other, bit, 64);
+    };
+    hand_over(8, sum[0], sum[2]);
+    hand_over(8, sum[1], sum[3]);
+    first += lane & 8 ? 2 : 0;
+    if constexpr (kLanes == 4) {
+        hand_over(4, sum[0], sum[1]);
+        first += lane & 4 ? 1 : 0;
     }
     constexpr int kMine = D / 64;
     int top = 0;
 #pragma unroll
     for (int e = 0; e < kMine; ++e) top = max(top, abs(sum[e]));
     top = (int)wave_max((uint32_t)top);
-    bad = __any(bad);
+    const bool bad = __any(scale_sum != scale_sum);
     const int64_t at = (int64_t)page * a.c.kv_heads + head;
     uint32_t out = 0;
 #pragma unroll
@@ -126,7 +123,7 @@ __device__ __forceinline__ void page_key(const PageKeysArgs& a, int page, int he
         *reinterpret_cast<uint16_t*>(a.codes + at * D + first) = (uint16_t)out;
     else
         a.codes[at * D + first] = (int8_t)out;
-    if (lane == 0) a.scales[at] = bad ? __builtin_nanf("") : (float)((double)top * (double)g * (1.0 / (130048.0 * size)));
+    if (lane == 0) a.scales[at] = bad ? __builtin_nanf("") : (float)((double)top * (double)g * a.inverse);
 }
 
 }  // namespace
@@ -135,9 +132,10 @@ __device__ __forceinline__ void page_key(const PageKeysArgs& a, int page, int he
 template <int D>
 __global__ __launch_bounds__(256) void k_page_keys(const PageKeysArgs a) {
     const int lane = (int)threadIdx.x & 63;
-    const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int64_t first = item / a.c.kv_heads * a.chunk;
-    const int head = (int)(item % a.c.kv_heads);
+    const unsigned item = blockIdx.x * 4 + (unsigned)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);      // (below 2^26)
+    const unsigned part = item / (unsigned)a.c.kv_heads;
+    const int64_t first = (int64_t)part * a.chunk;
+    const int head = (int)(item - part * (unsigned)a.c.kv_heads);
     if (first >= a.tokens) return;
     const int64_t slot = lane < a.chunk && first + lane < a.tokens ? a.slots[first + lane] : -1;
     const int64_t last_row = ((int64_t)1 << a.c.page_shift) - 1;

@@ -186,7 +186,7 @@ mxq_status mxq_page_keys_nvfp4(const mxq_nvfp4_kv* cache, const int64_t* slots, 
     const int64_t chunk = few ? 1 : keys->page_size < 64 ? keys->page_size : 64;
     if (tokens > kMaxRows || !product_below((tokens + chunk - 1) / chunk, 64ll * c.kv_heads, kMaxGridThreads - 255))
         return MXQ_ERR_UNSUPPORTED;
-    mxq::PageKeysArgs a{c, slots, tokens, keys->codes, keys->scales, (int32_t)chunk};
+    mxq::PageKeysArgs a{c, slots, tokens, keys->codes, keys->scales, (int32_t)chunk, 1.0 / (130048.0 * keys->page_size)};
     return mxq::launch_page_keys(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
 }
 

@@ -100,6 +100,7 @@ struct PageKeysArgs {
     int8_t* codes;                    // [num_pages][kv_heads][head_dim]
     float* scales;                    // [num_pages][kv_heads]
     int32_t chunk;                    // slots a wave looks at, 1 .. 64
+    double inverse;                   // of 130048 page_size
 };
 hipError_t launch_page_keys(const PageKeysArgs& a, hipStream_t stream);
 
