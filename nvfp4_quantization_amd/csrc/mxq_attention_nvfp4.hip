@@ -393,6 +393,86 @@ __global__ __launch_bounds__(64 * W, 8 / W) void k_attention_rows(const AttnArgs
     }
 }
 
+// Joins a query row's parts: W waves per row (a work-group has four).  Lanes first turn the
+// parts' maxima and sums into weights (LDS), then each wave adds every W-th part, all of a
+// lane's loads independent of one another.  parts: at most kMaxParts; part 0 at `first`, the
+// others `step` apart from `rest` on (rows).
+template <int D, int W>
+__device__ __forceinline__ void join_row(const AttnArgs& a, const Seq& seq, int kvh, int64_t r, int parts, int64_t first,
+                                         int64_t rest, int64_t step) {
+    constexpr int kRows = 4 / W;                             // rows of a work-group
+    __shared__ float weight[kRows][kMaxParts];
+    __shared__ float wave_sum[4], wave_top[4];
+    __shared__ float part[4][D];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int mine = tid / (64 * W), t = tid % (64 * W), w0 = wave % W;
+    const auto row_of = [&](int s) { return s == 0 ? first : rest + (s - 1) * step; };
+    // (the first parts' rows are on their way while the weights are made)
+    constexpr int kAhead = 8;
+    float ahead[kAhead][D / 64];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        const float* src = a.part_o + row_of(min(w0 + W * j, parts - 1)) * D + lane * (D / 64);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) ahead[j][e] = src[e];
+    }
+    const float vg = a.c.vg[kvh];
+    float2 ml[kMaxParts / (64 * W)];
+    float top = kFloor;
+#pragma unroll
+    for (int j = 0; j < kMaxParts / (64 * W); ++j) {
+        const int s = t + 64 * W * j;
+        ml[j] = s < parts ? a.part_ml[row_of(s)] : make_float2(kFloor, 0.0f);
+        top = __builtin_fmaxf(top, ml[j].x);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = __builtin_fmaxf(top, shfl_xor_f32(top, o));
+    if (W > 1) {
+        if (lane == 0) wave_top[wave] = top;
+        __syncthreads();
+        top = __builtin_fmaxf(__builtin_fmaxf(wave_top[0], wave_top[1]), __builtin_fmaxf(wave_top[2], wave_top[3]));
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMaxParts / (64 * W); ++j) {
+        const float f = __builtin_amdgcn_exp2f(ml[j].x - top);
+        weight[mine][t + 64 * W * j] = f;
+        sum += ml[j].y * f;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += shfl_xor_f32(sum, o);
+    if (W > 1) {
+        if (lane == 0) wave_sum[wave] = sum;
+        __syncthreads();
+        sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+    }
+    float v[D / 64] = {};
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        const float w = w0 + W * j < parts ? weight[mine][w0 + W * j] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) v[e] += w0 + W * j < parts ? ahead[j][e] * w : 0.0f;
+    }
+#pragma unroll 8
+    for (int s = w0 + W * kAhead; s < parts; s += W) {
+        const float w = weight[mine][s];
+        const float* src = a.part_o + row_of(s) * D + lane * (D / 64);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) v[j] += src[j] * w;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) part[wave][lane * (D / 64) + j] = v[j];
+    if (W > 1) __syncthreads();
+    if (t >= D / 4) return;
+    f32x4 y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int d = 4 * t + j;
+        y[j] = W > 1 ? (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]) : part[wave][d];
+    }
+    store_finished<D>(a, seq, kvh, r, 4 * t, y, top, sum, vg);
+}
+
 // Rows of a unit on the line that can hold queries, a multiple of 4.
 __host__ __device__ __forceinline__ int join_rows(const AttnArgs& a) {
     const int64_t rows = ((int64_t)a.max_q_len * a.group + 3) / 4 * 4;
@@ -416,8 +496,7 @@ __global__ __launch_bounds__(256) void k_attention_join_units(const AttnArgs a) 
     if (d.y == 0) return;                                    // finished by its work-group
     const int64_t at = 2 * (int64_t)d.x;
     const int parts = d.y;
-    join_row<D, W>(a, seq, kvh, r, parts, (at + 1) * a.tile_rows + r, (at + 2) * a.tile_rows + r, 2 * (int64_t)a.tile_rows,
-                   [] { return true; });
+    join_row<D, W>(a, seq, kvh, r, parts, (at + 1) * a.tile_rows + r, (at + 2) * a.tile_rows + r, 2 * (int64_t)a.tile_rows);
 }
 
 // The units that the form for many rows split.  W as above.
@@ -437,7 +516,7 @@ __global__ __launch_bounds__(256) void k_attention_join_splits(const AttnArgs a)
     const int used = splits_used(a, tile_span(a, seq, (int)(r0 / a.group), (int)(r1 / a.group)).n);
     if (used <= 1) return;                                   // written by the first kernel
     const int64_t at = unit * a.splits * a.tile_rows + r;
-    join_row<D, W>(a, seq, kvh, r0 + r, used, at, at + a.tile_rows, a.tile_rows, [] { return true; });
+    join_row<D, W>(a, seq, kvh, r0 + r, used, at, at + a.tile_rows, a.tile_rows);
 }
 
 // Units of their own get eight waves each while there is a CU for each: 256 units of 96

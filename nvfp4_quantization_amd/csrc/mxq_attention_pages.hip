@@ -186,39 +186,83 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 8 / W) void k_attention_pages(
         if (a.splits == 1)
             store_finished<D>(a, seq, kvh, in_group, d0, y, top, total, vg);
         else
-            store_part<D>(a, ((int64_t)split * a.total_q + token) * a.q_heads + kvh * a.group + in_group, d0, y, top, total);
+            store_row_part<D>(a, ((int64_t)split * a.total_q + token) * a.q_heads + kvh * a.group + in_group, d0, y, top, total);
     });
 }
 
-// W waves a row; W = 4: a work-group.
-template <int D, int W>
+// The parts of a query row and head, by a wave: D / 8 lanes a part, kPer parts a load, BLOCK such loads
+// on their way at once.
+template <int D, int BLOCK>
 __global__ __launch_bounds__(256) void k_attention_join_rows(const AttnArgs a) {
-    const int64_t row = (int64_t)blockIdx.x * (4 / W) + (threadIdx.x >> 6) / W, all = (int64_t)a.total_q * a.q_heads;
+    constexpr int kLanes = D / 8, kPer = 64 / kLanes;
+    const int lane = (int)threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t all = (int64_t)a.total_q * a.q_heads;
     if (row >= all) return;
-    const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads);
-    const int kvh = head / a.group;
-    join_row<D, W>(a, Seq{0, token, 1}, kvh, head - kvh * a.group, a.splits, row, row + all, all, [&] {
-        const Query at = query_of(a, a.c.page_shift, token);
-        return at.b >= 0 && at.index < a.max_q_len;
-    });
+    const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads), kvh = head / a.group;
+    const float vg = a.c.vg[kvh];
+    f16x8 o[BLOCK];
+    float2 ml[BLOCK];
+    const auto load = [&](int s0) {                          // parts s0 .. (past the last it again)
+#pragma unroll
+        for (int j = 0; j < BLOCK; ++j) {
+            const int64_t at = min(s0 + kPer * j + lane / kLanes, a.splits - 1) * all + row;
+            ml[j] = a.part_ml[at];
+            o[j] = *reinterpret_cast<const f16x8*>(reinterpret_cast<const f16*>(a.part_o) + at * D + 8 * (lane % kLanes));
+        }
+    };
+    load(0);
+    const Query at = query_of(a, a.c.page_shift, token);
+    if (at.b < 0 || at.index >= a.max_q_len) return;
+    float top = kFloor, sum = 0.0f;
+    float y[8] = {};
+    for (int s0 = 0; s0 < a.splits; s0 += BLOCK * kPer) {
+        if (s0 > 0) load(s0);
+        float most = top;
+#pragma unroll
+        for (int j = 0; j < BLOCK; ++j) most = __builtin_fmaxf(most, ml[j].x);
+#pragma unroll
+        for (int bit = kLanes; bit < 64; bit <<= 1) most = __builtin_fmaxf(most, shfl_xor_f32(most, bit));
+        const float f = __builtin_amdgcn_exp2f(top - most);
+        top = most;
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= f;
+#pragma unroll
+        for (int j = 0; j < BLOCK; ++j) {
+            const bool there = s0 + kPer * j + lane / kLanes < a.splits;
+            const float w = ml[j].y * __builtin_amdgcn_exp2f(ml[j].x - top);
+            sum += there ? w : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = there ? __builtin_fmaf((float)o[j][e], w, y[e]) : y[e];
+        }
+    }
+#pragma unroll
+    for (int bit = kLanes; bit < 64; bit <<= 1) {
+        sum += shfl_xor_f32(sum, bit);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += shfl_xor_f32(y[e], bit);
+    }
+    if (lane >= kLanes) return;
+    const Seq seq{0, token, 1};
+    const float scale = vg * (1.0f / kPartScale);            // (exact)
+    store_finished<D>(a, seq, kvh, head - kvh * a.group, 8 * lane, f32x4{y[0], y[1], y[2], y[3]}, top, sum, scale);
+    store_finished<D>(a, seq, kvh, head - kvh * a.group, 8 * lane + 4, f32x4{y[4], y[5], y[6], y[7]}, top, sum, scale);
 }
 
+template <int D>
+static void launch_join_rows(const AttnArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(((int64_t)a.total_q * a.q_heads + 3) / 4));
+    if (a.splits <= 4 * (64 / (D / 8)))
+        hipLaunchKernelGGL((k_attention_join_rows<D, 4>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_attention_join_rows<D, 12>), grid, dim3(256), 0, stream, a);
+}
 hipError_t launch_attention_join_rows(const AttnArgs& a, hipStream_t stream) {
-    const int64_t rows = (int64_t)a.total_q * a.q_heads;
-    const dim3 each((unsigned)rows), four((unsigned)((rows + 3) / 4));
-    // few rows get four waves each (128 of 10 parts 20.8 us in all against 19.9), many a wave (4096 of
-    // 17: 62.8 against 59.3)
-    if (a.c.head_dim == 128) {
-        if (a.splits > 64 || (a.splits > 4 && rows < 1024))
-            hipLaunchKernelGGL((k_attention_join_rows<128, 4>), each, dim3(256), 0, stream, a);
-        else
-            hipLaunchKernelGGL((k_attention_join_rows<128, 1>), four, dim3(256), 0, stream, a);
-    } else {
-        if (a.splits > 64 || (a.splits > 4 && rows < 1024))
-            hipLaunchKernelGGL((k_attention_join_rows<64, 4>), each, dim3(256), 0, stream, a);
-        else
-            hipLaunchKernelGGL((k_attention_join_rows<64, 1>), four, dim3(256), 0, stream, a);
-    }
+    if (a.c.head_dim == 128)
+        launch_join_rows<128>(a, stream);
+    else
+        launch_join_rows<64>(a, stream);
     return hipGetLastError();
 }
 

@@ -98,7 +98,7 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
     p->ml_offset = p->bytes = 0;
     if (p->splits > 1) {
         const int64_t parts = total_q * q_heads * p->splits;
-        p->ml_offset = (size_t)(parts * d * 4);
+        p->ml_offset = (size_t)(parts * d * 2);
         p->bytes = (size_t)round256((int64_t)p->ml_offset + parts * 8);
     }
     return true;
@@ -160,7 +160,7 @@ bool plan_prefix(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, in
     p->own_blocks = own_units * p->own_splits;
     if (p->prefix_blocks + p->own_blocks >= kMaxBlocks) return false;
     const int64_t parts = total_q * q_heads * (p->prefix_splits + p->own_splits);
-    p->ml_offset = (size_t)(parts * d * 4);
+    p->ml_offset = (size_t)(parts * d * 2);
     p->bytes = (size_t)round256((int64_t)p->ml_offset + parts * 8);
     return true;
 }

@@ -215,12 +215,12 @@ def test_attention_prefix_errors(L):
 def test_attention_prefix_workspace_size(L):
     size = mxq.mxq_attention_prefix_nvfp4_workspace_size
     base = (8, 2, 128, 3, 2, 4, 2, 40, 40)
-    assert size(*base) >= 2 * 4 * 8 * (128 * 4 + 8)                      # a part of each kind at least
+    assert size(*base) >= 2 * 4 * 8 * (128 * 2 + 8)                      # a part of each kind at least
     for i, v in ((0, 0), (1, 3), (2, 96), (3, 0), (3, 65536), (4, 0), (4, 4097), (5, 0), (5, 1 << 30), (6, 0), (7, -1), (8, -1)):
         assert size(*base[:i], v, *base[i + 1:]) == 0
     # no estimate, however large, plans more parts than a row's join takes
     for tokens in (1, 1 << 20, 1 << 40, (1 << 63) - 1):
-        assert size(8, 2, 64, 1, 1, 1, 1, tokens, tokens) <= 512 * 8 * (64 * 4 + 8) + 255
+        assert size(8, 2, 64, 1, 1, 1, 1, tokens, tokens) <= 512 * 8 * (64 * 2 + 8) + 255
 
 
 def test_prefix_binding_checks():
