@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kGroups = 512;               // work-groups that the chip holds at once
 constexpr int64_t kMaxPageTokens = 512;        // whose exact sums stay below 2^31
 constexpr int64_t kMaxTop = 1 << 16;
 constexpr int64_t kMaxListed = 1 << 30;        // tokens of a list's pages
@@ -76,7 +77,10 @@ SelectPlan plan_select(int64_t group, int64_t kv_heads, int64_t page_size, int64
 }
 
 // How attention over listed pages splits its work: a unit is (query, cached head, 16 or 32 rows
-// of its group).
+// of its group).  Few units go over several work-groups, a tile a wave where a CU each is enough
+// for them, else two (4 sequences, 8 cached heads, 64 pages of 64 in 8 pieces 11.0 us, in 16
+// 11.8; one sequence in 16 9.0, in 8 10.5).  From 2048 units on a wave takes one alone: 8000 of
+// 24 tiles 241 us against 267 by four waves each, which have to meet.
 struct PagesPlan {
     int32_t tile_rows, row_tiles, waves, splits;
     size_t ml_offset, bytes;
@@ -91,8 +95,9 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
     p->row_tiles = (int32_t)((group + p->tile_rows - 1) / p->tile_rows);
     const int64_t units = total_q * kv_heads * p->row_tiles, tiles = (top * page_size + 63) / 64;
     p->waves = units >= 2048 ? 1 : 4;
-    int64_t splits = 512 / units;
-    if (splits > (tiles + 7) / 8) splits = (tiles + 7) / 8;
+    int64_t splits = (tiles + 3) / 4;
+    if (units * splits > 256) splits = (tiles + 7) / 8;
+    if (splits > kGroups / units) splits = kGroups / units;
     p->splits = (int32_t)(splits < 1 ? 1 : splits);
     if (!product_below(units * p->splits, 64 * p->waves, kMaxGridThreads)) return false;
     p->ml_offset = p->bytes = 0;
@@ -120,7 +125,6 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
 //          64   65536   186.1 / 161.3                 two
 //          64   32768   112.8 / 124.3 (much of own)   one
 constexpr int64_t kMaxGroups = 4096;
-constexpr int64_t kGroups = 512;               // work-groups that the chip holds at once
 constexpr int64_t kMaxBlocks = 1 << 24;        // of 256 threads
 struct PrefixPlan {
     int32_t prefix_rows, own_rows, row_tiles, prefix_splits, own_splits;
@@ -155,7 +159,7 @@ bool plan_prefix(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, in
     const bool half = p->prefix_rows == 128 && (!product_below(usual, tiles, 1ll << 60) || usual * tiles < 80 * d ||
                                                 own_units * own_tiles > usual * tiles);
     p->prefix_splits = (int32_t)pieces(half ? 2 * usual : usual, tiles, 4, 256);
-    p->own_splits = (int32_t)pieces(own_units, own_tiles, 8, 128);
+    p->own_splits = (int32_t)pieces(own_units, own_tiles, 4, 128);
     p->prefix_blocks = prefix_units * p->prefix_splits;
     p->own_blocks = own_units * p->own_splits;
     if (p->prefix_blocks + p->own_blocks >= kMaxBlocks) return false;
