@@ -13,23 +13,23 @@ namespace {
 
 constexpr int kAbsent = 0x7FFFFFC0;   // the first token of a tile's group that no entry names: past every position
 
-// First tokens of a tile's groups (uniform) from the lanes' own (group lane % 4).
+// First tokens of a tile's groups (uniform) from the lanes' own (group lane % 4).  (Named members:
+// an array indexed by a lane's group would end up in scratch.)
 template <int G>
 struct Starts {
-    int t[G];
+    int t0, t1, t2, t3;
     __device__ __forceinline__ explicit Starts(int mine) {
-#pragma unroll
-        for (int i = 0; i < G; ++i) t[i] = __builtin_amdgcn_readlane(mine, i);
+        t0 = __builtin_amdgcn_readlane(mine, 0);
+        t1 = G == 1 ? t0 + 16 : __builtin_amdgcn_readlane(mine, 1);
+        t2 = G == 1 ? t0 + 32 : __builtin_amdgcn_readlane(mine, 2);
+        t3 = G == 1 ? t0 + 48 : __builtin_amdgcn_readlane(mine, 3);
     }
     __device__ __forceinline__ int of(int group) const {     // of a lane's group
-        if constexpr (G == 1) return t[0] + 16 * group;
-        const int lo = group & 1 ? t[1] : t[0], hi = group & 1 ? t[3] : t[2];
+        if constexpr (G == 1) return t0 + 16 * group;
+        const int lo = group & 1 ? t1 : t0, hi = group & 1 ? t3 : t2;
         return group & 2 ? hi : lo;
     }
-    __device__ __forceinline__ int last() const {            // the tile's last token
-        if constexpr (G == 1) return t[0] + 63;
-        return max(max(t[0], t[1]), max(t[2], t[3])) + 15;
-    }
+    __device__ __forceinline__ int last() const { return max(max(t0, t1), max(t2, t3)) + 15; }           // the tile's last token
 };
 
 }  // namespace
@@ -169,13 +169,14 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 8 / W) void k_attention_pages(
                     for (int t = 0; t < 4; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const bool seen = from.t[G == 1 ? 0 : t] + (G == 1 ? 16 * t : 0) + 4 * L.g + e <= at.pos;
+                            const int start = t == 0 ? from.t0 : t == 1 ? from.t1 : t == 2 ? from.t2 : from.t3;
+                            const bool seen = start + 4 * L.g + e <= at.pos;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) x[n][t][e] = seen ? x[n][t][e] : -__builtin_inff();
                         }
                 }
             },
-            [&](int, int tok) { return from.of(tok >> 4) + (tok & 15) <= at.pos; });
+            [&](int, int t, int i) { return (t == 0 ? from.t0 : t == 1 ? from.t1 : t == 2 ? from.t2 : from.t3) + i <= at.pos; });
     }
 
     waves_meet<D, NT, W>(wave, L, m, l, o, nan_blocks, join);

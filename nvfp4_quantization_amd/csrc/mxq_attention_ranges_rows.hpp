@@ -112,7 +112,7 @@ __device__ __forceinline__ void range_rows(const PrefixAttnArgs& a, const RangeU
                     }
                 }
             },
-            [&](int n, int tok) { return in_range(hi[n], count[n], t0 + tok); });
+            [&](int n, int t, int i) { return in_range(hi[n], count[n], t0 + 16 * t + i); });
     }
 
     waves_meet<D, NT, W>(wave, L, m, l, o, nan_blocks, join);

@@ -205,7 +205,7 @@ __device__ __forceinline__ void stage_scales(uint8_t* lds, const uint32_t (&vs)[
 // Adds the loaded tile (k, v; bit t of unread: group t's page may not be read; valid: this
 // lane's token of V's scales is one of the sequence) to the rows' running softmax.  next_v and
 // next_k load the following tile when V's and K's registers are free; mask(x) hides what rows
-// do not see (token 16 t + 4 g + e of the tile in x[n][t][e]); sees_token(n, token of the tile).
+// do not see (token 16 t + 4 g + e of the tile in x[n][t][e]); sees_token(n, t, i): token 16 t + i.
 template <int D, int NT, int G, typename NextV, typename NextK, typename Mask, typename Sees>
 __device__ __forceinline__ void rows_step(uint8_t* mine, const Lane& L, uint32_t unread, bool valid, int scale_shift,
                                           KRegs<D>& k, VRegs<D>& v, const f16x8 (&q)[NT][D / 32], const float (&factor)[NT],
@@ -225,13 +225,14 @@ __device__ __forceinline__ void rows_step(uint8_t* mine, const Lane& L, uint32_t
             blocks |= ((hit | hit >> 7 | hit >> 14 | hit >> 21) & 0xFu) << (4 * w);
         }
         mine[WaveLds<D>::kNan + L.lane] = (uint8_t)(valid ? blocks : 0u);
-#pragma unroll 1
-        for (int j = 0; j < 16; ++j) {
-            const int tok = 16 * (j >> 2) + 4 * L.g + (j & 3);
-            const uint32_t x = mine[WaveLds<D>::kNan + tok];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) nan_blocks[n] |= sees_token(n, tok) ? x : 0u;
-        }
+        for (int t = 0; t < 4; ++t)
+#pragma unroll 1
+            for (int i = 4 * L.g; i < 4 * L.g + 4; ++i) {
+                const uint32_t x = mine[WaveLds<D>::kNan + 16 * t + i];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) nan_blocks[n] |= sees_token(n, t, i) ? x : 0u;
+            }
     }
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) *reinterpret_cast<u32x4v*>(mine + j * kVJ + L.lane * 16) = v.w[j];

@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxBlocks = 1 << 24;        // of 256 threads
 constexpr int64_t kGroups = 512;               // work-groups that the chip holds at once
 constexpr int64_t kMaxPageTokens = 512;        // whose exact sums stay below 2^31
 constexpr int64_t kMaxTop = 1 << 16;
@@ -99,7 +100,7 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
     if (units * splits > 256) splits = (tiles + 7) / 8;
     if (splits > kGroups / units) splits = kGroups / units;
     p->splits = (int32_t)(splits < 1 ? 1 : splits);
-    if (!product_below(units * p->splits, 64 * p->waves, kMaxGridThreads)) return false;
+    if (units >= kMaxBlocks) return false;
     p->ml_offset = p->bytes = 0;
     if (p->splits > 1) {
         const int64_t parts = total_q * q_heads * p->splits;
@@ -125,7 +126,6 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
 //          64   65536   186.1 / 161.3                 two
 //          64   32768   112.8 / 124.3 (much of own)   one
 constexpr int64_t kMaxGroups = 4096;
-constexpr int64_t kMaxBlocks = 1 << 24;        // of 256 threads
 struct PrefixPlan {
     int32_t prefix_rows, own_rows, row_tiles, prefix_splits, own_splits;
     int64_t prefix_blocks, own_blocks;

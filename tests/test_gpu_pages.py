@@ -469,3 +469,19 @@ def test_select_long_runs(lens, nq, hq, hk, d, page, top, first, last):
     c.table[:, ::7] = c.pages
     scales[::5] = np.nan
     run_select(c, codes, scales, top, first, last, dev)
+
+
+@pytest.mark.parametrize("lens,nq,hq,hk,d,page,top", [
+    ([20000], [1], 8, 1, 64, 16, 500),                                   # more than the shortlist takes: 16 waves
+    ([9000, 8000], [150, 150], 8, 2, 64, 16, 300),                       # four waves a query
+    ([8000], [600], 4, 1, 64, 16, 230),                                  # a wave a query
+    ([9000], [2], 40, 1, 128, 16, 256),
+])
+def test_select_many_pages(lens, nq, hq, hk, d, page, top):
+    dev = device()
+    announce(f"many pages lens={lens} nq={nq} hq={hq} hk={hk} d={d} top={top}")
+    c = cu.Sequences(lens, nq, hq, hk, d, page, seed=top)
+    codes, scales = random_keys(c, 1)
+    run_select(c, codes, scales, top, 1, 2, dev)
+    scales = np.round(scales * 3)                                        # ties, zeros
+    run_select(c, np.sign(codes), scales, top, 1, 2, dev)

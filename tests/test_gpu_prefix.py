@@ -282,3 +282,42 @@ def test_graph():
         cu.check_attention(su.f32_of_bf16(call.out.out), host(call.out.lse), c.want())
         call.out.out.fill_(9.0)
         call.workspace.fill_(0xFF)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_decoding_behind_a_shared_prompt(graph):
+    """Steps of a server: each sequence of two groups appends a token to pages of its own, then all
+    attend over prompt and tokens; captured once and replayed too."""
+    dev = device()
+    hk, hq, d, page, batch = 2, 8, 64, 16, 5
+    starts, prefix = [0, 3, 5], [100, 100, 100, 64, 64]
+    own = [3, 17, 1, 30, 2]
+    c = Case(starts, prefix, [p + n + 12 for p, n in zip(prefix, own)], [1] * batch, hq, hk, d, page, seed=2)
+    cache = c.device_cache(dev)
+    table, seq_lens, q_starts = c.device_sequences(dev)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    gen = torch.Generator(device=dev).manual_seed(5)
+    qkv = torch.empty((batch, hq + 2 * hk, d), dtype=torch.bfloat16, device=dev)
+    positions, slots = i32([0] * batch), torch.zeros(batch, dtype=torch.int64, device=dev)
+    append = mxq.RopeAppendNVFP4(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], positions, slots, mxq.rope_plan(d), cache)
+    attend = mxq.AttentionPrefixNVFP4(append.out.q, cache, table, seq_lens, q_starts, i32(starts), i32(prefix), 1, lse=True)
+    recorded = None
+    for i in range(6):
+        now = torch.tensor([p + n + i for p, n in zip(prefix, own)], device=dev)
+        qkv.copy_(torch.randn(qkv.shape, generator=gen, device=dev))
+        positions.copy_(now)
+        slots.copy_(table[torch.arange(batch, device=dev), now // page].long() * page + now % page)
+        seq_lens.copy_(now + 1)
+        if graph and recorded is None:
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                recorded = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(recorded, stream=side):
+                    append(), attend()
+            torch.cuda.current_stream().wait_stream(side)
+        recorded.replay() if graph else (append(), attend())
+        torch.cuda.synchronize()
+        c.kc, c.ks, c.vc, c.vs = (host(t) for t in cache.tensors()[:4])
+        c.lens, c.q = [int(v) + 1 for v in now], su.f32_of_bf16(append.out.q)
+        cu.check_attention(su.f32_of_bf16(attend.out.out), host(attend.out.lse), c.want())
