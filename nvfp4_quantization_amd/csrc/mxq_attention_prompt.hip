@@ -281,11 +281,15 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
 
     // The queries are asked for ahead of the first tile, which has to wait for its page table
     // entry: loads come back in order, and so they are made ready while the tile is on its way.
-    Part<D> kr, vr;
+    // Ranges: tiles come from memory a step earlier, since often one work-group has a CU to itself and
+    // its steps are short (a second set of registers, staged from in turn).
+    constexpr int kLead = RANGES ? 3 : 2;
+    Part<D> kr, vr, kr2, vr2;
     int32_t entry = 0;
     if (first < last) {
         const int32_t e0 = entry_of(first), e1 = entry_of(first + 1);
-        entry = entry_of(first + 2);
+        const int32_t e2 = RANGES ? entry_of(first + 2) : 0;
+        entry = entry_of(first + kLead);
         const uint16_t* src = a.q + (int64_t)(seq.start + qi) * a.ld_q + (int64_t)head * D + h * 8;
         u32x4v w[D / 16];
 #pragma unroll
@@ -295,6 +299,12 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
         Spot at = spot_of(e0, first);
         load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
         load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
+        if constexpr (RANGES) {
+            kr2 = kr, vr2 = vr;
+            at = spot_of(e1, first + 1);
+            load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
+            load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
+        }
         __builtin_amdgcn_sched_barrier(0);
         uint32_t top = 0;
 #pragma unroll
@@ -306,17 +316,26 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
         factor = score_factor(a, factor, kg);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) q[c] = q_operand(w[c], up);
-        store_k<D>(k0, kr, my_tok, part);
-        store_v<D>(v0, vr, my_tok, valid(first), part);
-        at = spot_of(e1, first + 1);
-        load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
-        load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
+        if constexpr (RANGES) {
+            store_k<D>(k0, kr2, my_tok, part);
+            store_v<D>(v0, vr2, my_tok, valid(first), part);
+            at = spot_of(e2, first + 2);
+            load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr2);
+            load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr2);
+        } else {
+            store_k<D>(k0, kr, my_tok, part);
+            store_v<D>(v0, vr, my_tok, valid(first), part);
+            at = spot_of(e1, first + 1);
+            load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
+            load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
+        }
     }
 
     // One tile: kn, vn its images; kf, vf the next one's (the last tile's again at the end).
     // The order of the products and what stands between them is fixed by hand: left alone,
     // the compiler forms all weights first and reads each operand right before its product.
-    const auto step = [&](int i, const KImage<D>& kn, KImage<D>& kf, const VImage<D>& vn, VImage<D>& vf) {
+    const auto step = [&](int i, const KImage<D>& kn, KImage<D>& kf, const VImage<D>& vn, VImage<D>& vf, Part<D>& kr,
+                          Part<D>& vr) {
         __syncthreads();                               // kn and vn are whole; kf and vf are free
         const int t0 = span.tile(i) * 64;
         const u32x4v noted = *reinterpret_cast<const u32x4v*>(vn.any_nan);
@@ -348,10 +367,10 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
             __builtin_amdgcn_sched_barrier(0);
         }
         {
-            const Spot at = spot_of(entry, i + 2);
+            const Spot at = spot_of(entry, i + kLead);
             load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
             load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
-            entry = entry_of(i + 3);
+            entry = entry_of(i + kLead + 1);
         }
         // masks only where an edge crosses the tile for this wave's rows
         if constexpr (RANGES) {
@@ -431,24 +450,26 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
     // A wave without rows only stages its share of the next tile (64 ragged sequences of up to
     // 8192 tokens with 40 rows a unit: 211 us against 257).  The other two of four waves then do
     // all products, so that these 336 MB take four times as long as their bytes.
-    const auto stage = [&](int i, KImage<D>& kf, VImage<D>& vf) {
+    const auto stage = [&](int i, KImage<D>& kf, VImage<D>& vf, Part<D>& kr, Part<D>& vr) {
         __syncthreads();
         store_k<D>(kf, kr, my_tok, part);
         store_v<D>(vf, vr, my_tok, valid(i + 1), part);
-        const Spot at = spot_of(entry, i + 2);
+        const Spot at = spot_of(entry, i + kLead);
         load_part<D>(a.c.kc, a.c.ks, at, code_at, scale_at, kr);
         load_part<D>(a.c.vc, a.c.vs, at, code_at, scale_at, vr);
-        entry = entry_of(i + 3);
+        entry = entry_of(i + kLead + 1);
     };
+    Part<D>& k_odd = RANGES ? kr2 : kr;               // of every second step
+    Part<D>& v_odd = RANGES ? vr2 : vr;
     if (wave * kWaveRows < rows) {
         for (int i = first; i < last; i += 2) {
-            step(i, k0, k1, v0, v1);
-            if (i + 1 < last) step(i + 1, k1, k0, v1, v0);
+            step(i, k0, k1, v0, v1, kr, vr);
+            if (i + 1 < last) step(i + 1, k1, k0, v1, v0, k_odd, v_odd);
         }
     } else {
         for (int i = first; i < last; i += 2) {
-            stage(i, k1, v1);
-            if (i + 1 < last) stage(i + 1, k0, v0);
+            stage(i, k1, v1, kr, vr);
+            if (i + 1 < last) stage(i + 1, k0, v0, k_odd, v_odd);
         }
     }
 

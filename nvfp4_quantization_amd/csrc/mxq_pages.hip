@@ -374,31 +374,40 @@ __device__ __forceinline__ int sum_waves(int v, int wave, int (&shared)[16]) {
     return sum;
 }
 
-// Of a wave's 256 orders, none above `top` and at least `wanted` from `from` on: the largest that
+// Of a wave's 64 N orders, none above `top` and at least `wanted` from `from` on: the largest that
 // `wanted` reach, or any that at most `enough` do as well; two bits at a time.
+template <int N>
 __device__ __forceinline__ int count_reach(const uint32_t (&x)[4], uint32_t t) {
-    return __popcll(__ballot(x[0] >= t)) + __popcll(__ballot(x[1] >= t)) + __popcll(__ballot(x[2] >= t)) +
-           __popcll(__ballot(x[3] >= t));
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popcll(__ballot(x[i] >= t));
+    return n;
 }
+template <int N>
 __device__ __forceinline__ uint32_t edge_of(const uint32_t (&x)[4], int wanted, int enough, uint32_t from, uint32_t top) {
     const int bits = from == top ? 0 : (33 - __builtin_clz(from ^ top)) & ~1;                // even
     uint32_t edge = bits == 32 ? 0u : from >> bits << bits;
     for (int bit = bits - 2; bit >= 0; bit -= 2) {
         const uint32_t one = 1u << bit;
-        const int n1 = count_reach(x, edge + one), n2 = count_reach(x, edge + 2 * one), n3 = count_reach(x, edge + 3 * one);
+        const int n1 = count_reach<N>(x, edge + one), n2 = count_reach<N>(x, edge + 2 * one), n3 = count_reach<N>(x, edge + 3 * one);
         const int n = n3 >= wanted ? n3 : n2 >= wanted ? n2 : n1;
         edge += n3 >= wanted ? 3 * one : n2 >= wanted ? 2 * one : n1 >= wanted ? one : 0u;
         if (n >= wanted && n <= enough) break;
     }
     return edge;
 }
-// A bound of them to start from: a half, a quarter or an eighth of the largest score, if it is a
-// number above zero and that is low enough (most of an order's upper bits are the exponent).
-__device__ __forceinline__ uint32_t edge_start(const uint32_t (&x)[4], int wanted, uint32_t top) {
+// The edge of a row's columns, a little more than `wanted` of them from it on.  From a half, a
+// quarter or an eighth of the largest score, if that is a number above zero and one of them is low
+// enough (most of an order's upper bits are the exponent).
+template <int N>
+__device__ __forceinline__ uint32_t column_edge(const uint32_t (&x)[4], int wanted, uint32_t top) {
     constexpr uint32_t kOne = 1u << 23;
-    if (top < 0x80000000u + 4 * kOne) return 0;
-    const int n1 = count_reach(x, top - kOne), n2 = count_reach(x, top - 2 * kOne), n3 = count_reach(x, top - 3 * kOne);
-    return n1 >= wanted ? top - kOne : n2 >= wanted ? top - 2 * kOne : n3 >= wanted ? top - 3 * kOne : 0;
+    uint32_t from = 0;
+    if (top >= 0x80000000u + 4 * kOne) {
+        const int n1 = count_reach<N>(x, top - kOne), n2 = count_reach<N>(x, top - 2 * kOne), n3 = count_reach<N>(x, top - 3 * kOne);
+        from = n1 >= wanted ? top - kOne : n2 >= wanted ? top - 2 * kOne : n3 >= wanted ? top - 3 * kOne : 0;
+    }
+    return edge_of<N>(x, wanted, wanted + wanted / 8 + 4, from, top);
 }
 
 // The `wanted` largest of n orders (n > wanted >= 1), lower places first among equal ones, by NW
@@ -409,9 +418,9 @@ template <int NW, typename Prepare, typename Shared>
 __device__ __forceinline__ void select_row(const uint32_t* keys, int n, int wanted, int window, Prepare&& prepare, int32_t* out,
                                            int add, int wave, Shared& shared) {
     const int lane = (int)threadIdx.x & 63;
-    // The wanted-th largest of 256 columns' largest orders is reached by that many orders at
-    // least, and by few more (about 70 for 64), unless many are equal: those are put on a list, in
-    // their places' order, and one wave finishes there.
+    // The wanted-th largest of 64 to 256 columns' largest orders is reached by that many orders at
+    // least, and by few more (about 80 for 59 with 128 columns), unless many are equal: those are put
+    // on a list, in their places' order, and one wave finishes there.
     if (wanted <= 200 && n <= window) {
         uint16_t* const list = shared.list + (NW == 1 ? (int)(threadIdx.x >> 6) * kShort : 0);
         uint32_t column[4] = {0, 0, 0, 0};
@@ -433,8 +442,17 @@ __device__ __forceinline__ void select_row(const uint32_t* keys, int n, int want
         const uint32_t top = wave_max(max(max(column[0], column[1]), max(column[2], column[3])));
         // (1 at least: not the zeros behind n.  Those of NaN scores then are too few)
         uint32_t least = 1;
-        if (NW <= 4 || wave == 0)
-            least = max(edge_of(column, wanted, wanted + wanted / 8 + 4, edge_start(column, wanted, top), top), 1u);
+        if (NW <= 4 || wave == 0) {                          // (64 columns of several candidates do for few)
+            if (n > 256 && wanted <= 40) {
+                column[0] = max(max(column[0], column[1]), max(column[2], column[3]));
+                least = max(column_edge<1>(column, wanted, top), 1u);
+            } else if (n > 256 && wanted <= 100) {
+                column[0] = max(column[0], column[1]), column[1] = max(column[2], column[3]);
+                least = max(column_edge<2>(column, wanted, top), 1u);
+            } else {
+                least = max(column_edge<4>(column, wanted, top), 1u);
+            }
+        }
         if constexpr (NW > 4) {                              // (the others would only be in its way)
             if (wave == 0 && lane == 0) shared.least = least;
             __syncthreads();
@@ -482,7 +500,7 @@ __device__ __forceinline__ void select_row(const uint32_t* keys, int n, int want
                 place[e] = list[min(64 * e + lane, m - 1)];
                 k[e] = 64 * e + lane < m ? keys[place[e]] : 0u;          // (those of the list are 1 and more)
             }
-            const uint32_t edge = edge_of(k, wanted, wanted, least, top);
+            const uint32_t edge = m <= 128 ? edge_of<2>(k, wanted, wanted, least, top) : edge_of<4>(k, wanted, wanted, least, top);
             int ties = wanted;
 #pragma unroll
             for (int e = 0; e < 4; ++e) ties -= __popcll(__ballot(k[e] > edge));
