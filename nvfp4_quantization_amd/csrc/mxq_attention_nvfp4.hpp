@@ -279,7 +279,7 @@ __device__ __forceinline__ void store_part(const AttnArgs& a, int64_t at, int d0
 
 // A part of a row whose parts lie by query row (mxq_attention_pages.hip): finished but for the
 // tensor scale and times kPartScale, in FP16.  Half the bytes to write and read of FP32, for one more
-// rounding: of V's values 2^-12 at most, which the weights' own rounding costs too; elements
+// rounding: of the part 2^-11 at most, which the weights' own rounding costs too; elements
 // below 2^-14 / kPartScale (in units of V's tensor scale, whose steps are 2^-10 and more) by 2^-29.
 constexpr float kPartScale = 16.0f;                          // (V's values are at most 2688)
 template <int D>

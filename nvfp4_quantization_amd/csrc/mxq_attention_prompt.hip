@@ -31,6 +31,9 @@
 // card); two prompts of 4096 tokens 300 to 308 us, 892 to 916 TFLOP/s, and a quarter more when
 // the tiles of a sequence ran together, so that the last sequence's longest rows started last.
 // 64 rows a wave (half the operand reads, one wave a SIMD) were slower.
+//
+// The same body takes the rows of groups of sequences over shared prefixes, with a range of tokens
+// a row, beside sequences' own rows in the same launch (mxq_attention_ranges.hpp, figures there).
 #include <type_traits>
 
 #include "mxq_attention_ranges_rows.hpp"
