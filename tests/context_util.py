@@ -136,7 +136,14 @@ def attend_tokens(q, k, v, scale):
 
 def attention_over(c, tokens_of, scale):
     """out, lse and their bounds of every row and head; tokens_of(row, b, pos, kv head) gives the
-    physical rows (page, row) that it sees.  Rows of no sequence come back NaN."""
+    physical rows (page, row) that it sees.  Rows of no sequence come back NaN.
+
+    attention_bounds counts everything but the rounding of a cut row's parts.  A part's output is
+    rounded to FP16, divided by V's tensor scale and times 16: half a step is 2^-11 of it, or 2^-25
+    / 16 of the tensor scale below FP16's normal range.  The join weighs parts by shares that add
+    up to one, so the row is off by at most 2^-11 of the weighted mean of |part|, which is at most
+    mean |v| and what the part itself is off by (its error times 2^-11: the factor 1.05), and by 2^-29
+    of the tensor scale; then by as much of the rounding to BF16."""
     d, group = c.d, c.hq // c.hk
     out, lse = np.full((c.total, c.hq, d), np.nan), np.full((c.total, c.hq), np.nan)
     mean_v, sum_v, big = np.zeros((c.total, c.hq, d)), np.zeros((c.total, c.hq, d)), np.zeros((c.total, c.hq))
@@ -149,7 +156,9 @@ def attention_over(c, tokens_of, scale):
             for j in range(h * group, (h + 1) * group):
                 out[row, j], lse[row, j], mean_v[row, j], sum_v[row, j], big[row, j] = attend_tokens(
                     c.q[row, j].astype(np.float64), kk, vv, scale)
-    return (out, lse, *su.attention_bounds(out, lse, mean_v, sum_v, big, d))
+    o, l = su.attention_bounds(out, lse, mean_v, sum_v, big, d)
+    vg = np.repeat(np.abs(c.vg.astype(np.float64)), group)[None, :, None]
+    return out, lse, o + (1 + 2.0 ** -8) * (1.05 * 2.0 ** -11 * mean_v + 2.0 ** -29 * vg), l
 
 
 def listed_tokens(c, pages):

@@ -1,6 +1,6 @@
 """Mean keys, page selection and attention over listed pages on the GPU against plain forms
 (tests/context_util.py): keys and selections bit for bit, attention within bounds counted from
-its roundings (serve_util.attention_bounds)."""
+its roundings (context_util.attention_over)."""
 import math
 
 import numpy as np

@@ -1,5 +1,5 @@
 """Attention with shared prefixes on the GPU against the plain form of tests/context_util.py,
-within bounds counted from its roundings (serve_util.attention_bounds)."""
+within bounds counted from its roundings (context_util.attention_over)."""
 import math
 
 import numpy as np
