@@ -606,9 +606,8 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
  *                behind one, which size the split (longer ones are still right)
  * workspace: device memory of mxq_attention_prefix_nvfp4_workspace_size(...) bytes, as
  * there (never 0 but for calls that do nothing or are refused).
- * Requirements: as there; 1 <= groups <= 4096; in total fewer than 2^24 work-groups (two
- * pieces of all rows: about total_q * q_heads / 128 + batch * kv_heads; else
- * MXQ_ERR_UNSUPPORTED).  total_q == 0 or max_q_len == 0 is a successful no-op.
+ * Requirements: as there; 1 <= groups <= 4096; total_q * q_heads <= 2^26 - 4 and in total fewer
+ * than 2^24 work-groups (the pieces of all rows; else MXQ_ERR_UNSUPPORTED).  total_q == 0 or max_q_len == 0 is a successful no-op.
  * ------------------------------------------------------------------------- */
 size_t mxq_attention_prefix_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,
                                                  int64_t groups, int64_t total_q, int64_t max_q_len,

@@ -140,7 +140,7 @@ bool plan_prefix(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, in
                  int64_t max_prefix, int64_t max_own, PrefixPlan* p) {
     if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (d != 64 && d != 128) || batch < 1 || batch > kMaxBatch ||
         groups < 1 || groups > kMaxGroups || total_q < 1 || max_q < 1 || max_prefix < 0 || max_own < 0 ||
-        !product_below(total_q, q_heads, 1ll << 31))
+        !product_below(total_q, q_heads, 4 * kMaxBlocks - 3))           // (the launch that joins: a wave a row)
         return false;
     if (max_q > total_q) max_q = total_q;
     if (max_prefix > (1ll << 31)) max_prefix = 1ll << 31;

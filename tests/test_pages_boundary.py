@@ -235,3 +235,19 @@ def test_prefix_binding_checks():
             mxq.AttentionPrefixNVFP4(q, cache, *seqs, *bad)
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         mxq.AttentionPrefixNVFP4(q, cache, *seqs, *good, workspace=torch.zeros(512, dtype=torch.uint8)[::2])
+
+
+@no_gpu
+def test_prefix_rows_that_no_launch_joins(L):
+    """A wave joins a query row and head, four a work-group: 2^26 of them are more threads than a
+    launch holds, and the call is refused before anything is enqueued."""
+    size = mxq.mxq_attention_prefix_nvfp4_workspace_size
+    shape = dict(hq=64, ld_q=64 * 128, ld_out=64 * 128, c=kv(kv_heads=8, code_stride_page=8 * 16 * 64, scale_stride_page=8 * 16 * 8),
+                 batch=1, groups=1, max_q=1)
+    assert size(64, 8, 128, 1, 1, 1 << 20, 1, 40, 40) == 0
+    assert size(64, 8, 128, 1, 1, (1 << 20) - 1, 1, 40, 40) > 0
+    assert prefix(L, total=1 << 20, **shape) == UNSUPPORTED
+    # one query head each, so every count can be had: 2^26 - 4 rows are 2^32 - 256 threads
+    assert size(1, 1, 64, 1, 1, (1 << 26) - 4, 1, 40, 40) > 0
+    for rows in range((1 << 26) - 3, (1 << 26) + 1):
+        assert size(1, 1, 64, 1, 1, rows, 1, 40, 40) == 0
