@@ -375,10 +375,12 @@ template <int W>
 struct RowShared {
     int count[16];
     int2 pair[16];
-    uint32_t column[256];
+    __attribute__((aligned(16))) uint32_t column[256];
     uint32_t least;
     uint16_t list[W * kShort];        // places, ascending
 };
+static_assert(alignof(RowShared<1>) % 16 == 0 && __builtin_offsetof(RowShared<1>, column) % 16 == 0,
+              "column is cleared 16 bytes at a time");
 template <int NW>
 __device__ __forceinline__ int sum_waves(int v, int wave, int (&shared)[16]) {
     if constexpr (NW == 1) return v;
