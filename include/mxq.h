@@ -595,10 +595,9 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
  * than the sequence's own seq_lens[b] (the query at position p then sees its first p + 1
  * tokens), and what a sequence's own row of block_table says of shared tokens is not read.
  * Arithmetic, roundings, NaN scales, unreadable pages and the other arguments as in
- * mxq_attention_nvfp4, and one rounding more: a row's work is cut into parts, over the
- * prefix and its own tokens, and each part's output is rounded to FP16 before they are
- * joined (off by at most 2^-11 of it, or by 2^-29 of V's tensor scale where that is more).
- * The order of the sums depends on the lengths, the groups and the estimates.
+ * mxq_attention_nvfp4.  A row's work is cut into parts, over the prefix and its own tokens,
+ * which are held and joined in FP32; the order of the sums depends on the lengths, the
+ * groups and the estimates.
  *   group_starts device int32[groups + 1], ascending; the first counts as 0 and the last
  *                as batch
  *   prefix_lens  device int32[batch]; held to [0, table_pages * page_size]
@@ -699,9 +698,8 @@ mxq_status mxq_select_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_hea
  * them); out = 0 and lse = -inf where there is none.  Entries that are negative or above
  * p / page_size add nothing, in any place; a page that is listed twice counts twice.  The
  * arithmetic, its roundings, what NaN scales and unreadable pages do, and the other
- * arguments are those of mxq_attention_nvfp4; where few queries' lists are cut into parts,
- * each part's output is rounded to FP16 before they are joined, as in
- * mxq_attention_prefix_nvfp4.  Entries after the last that counts cost nothing.
+ * arguments are those of mxq_attention_nvfp4 (few queries' lists are cut into parts, held
+ * and joined in FP32).  Entries after the last that counts cost nothing.
  *   pages    device int32 [total_q][kv_heads][top], 4-byte aligned
  * workspace: device memory of mxq_attention_pages_nvfp4_workspace_size(...) bytes, as there.
  * Requirements: those of mxq_attention_nvfp4 on q, out, the cache, the sequences and the

@@ -277,20 +277,6 @@ __device__ __forceinline__ void store_part(const AttnArgs& a, int64_t at, int d0
     if (d0 == 0) a.part_ml[at] = make_float2(m, sum);
 }
 
-// A part of a row whose parts lie by query row (mxq_attention_pages.hip): finished but for the
-// tensor scale and times kPartScale, in FP16.  Half the bytes to write and read of FP32, for one more
-// rounding: of the part 2^-11 at most, which the weights' own rounding costs too; elements
-// below 2^-14 / kPartScale (in units of V's tensor scale, whose steps are 2^-10 and more) by 2^-29.
-constexpr float kPartScale = 16.0f;                          // (V's values are at most 2688)
-template <int D>
-__device__ __forceinline__ void store_row_part(const AttnArgs& a, int64_t at, int d0, const f32x4& o, float m, float sum) {
-    const float inv = sum == 0.0f ? 0.0f : kPartScale / sum;
-    const f32x4 y = o * inv;
-    typedef f16 f16x4 __attribute__((ext_vector_type(4)));
-    *reinterpret_cast<f16x4*>(reinterpret_cast<f16*>(a.part_o) + at * D + d0) = __builtin_convertvector(y, f16x4);
-    if (d0 == 0) a.part_ml[at] = make_float2(m, sum);
-}
-
 }  // namespace
 
 }  // namespace mxq

@@ -197,12 +197,12 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 8 / W) void k_attention_pages(
         if (a.splits == 1)
             store_finished<D>(a, seq, kvh, in_group, d0, y, top, total, vg);
         else
-            store_row_part<D>(a, ((int64_t)split * a.total_q + token) * a.q_heads + kvh * a.group + in_group, d0, y, top, total);
+            store_part<D>(a, ((int64_t)split * a.total_q + token) * a.q_heads + kvh * a.group + in_group, d0, y, top, total);
     });
 }
 
-// The parts of a query row and head, by a wave: D / 8 lanes a part, kPer parts a load, BLOCK such loads
-// on their way at once.
+// The parts of a query row and head, by a wave: D / 8 lanes a part (elements 4 l .. and D / 2 + 4 l .. of
+// it), kPer parts a load, BLOCK such loads on their way at once (9: as many as 128 registers hold).
 template <int D, int BLOCK>
 __global__ __launch_bounds__(256) void k_attention_join_rows(const AttnArgs a) {
     constexpr int kLanes = D / 8, kPer = 64 / kLanes;
@@ -212,21 +212,23 @@ __global__ __launch_bounds__(256) void k_attention_join_rows(const AttnArgs a) {
     if (row >= all) return;
     const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads), kvh = head / a.group;
     const float vg = a.c.vg[kvh];
-    f16x8 o[BLOCK];
+    f32x4 o[BLOCK][2];
     float2 ml[BLOCK];
     const auto load = [&](int s0) {                          // parts s0 .. (past the last it again)
 #pragma unroll
         for (int j = 0; j < BLOCK; ++j) {
             const int64_t at = min(s0 + kPer * j + lane / kLanes, a.splits - 1) * all + row;
+            const float* const src = a.part_o + at * D + 4 * (lane % kLanes);
             ml[j] = a.part_ml[at];
-            o[j] = *reinterpret_cast<const f16x8*>(reinterpret_cast<const f16*>(a.part_o) + at * D + 8 * (lane % kLanes));
+            o[j][0] = *reinterpret_cast<const f32x4*>(src);
+            o[j][1] = *reinterpret_cast<const f32x4*>(src + D / 2);
         }
     };
     load(0);
     const Query at = query_of(a, a.c.page_shift, token);
     if (at.b < 0 || at.index >= a.max_q_len) return;
     float top = kFloor, sum = 0.0f;
-    float y[8] = {};
+    f32x4 y[2] = {};
     for (int s0 = 0; s0 < a.splits; s0 += BLOCK * kPer) {
         if (s0 > 0) load(s0);
         float most = top;
@@ -237,28 +239,27 @@ __global__ __launch_bounds__(256) void k_attention_join_rows(const AttnArgs a) {
         const float f = __builtin_amdgcn_exp2f(top - most);
         top = most;
         sum *= f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= f;
+        y[0] *= f;
+        y[1] *= f;
 #pragma unroll
         for (int j = 0; j < BLOCK; ++j) {
             const bool there = s0 + kPer * j + lane / kLanes < a.splits;
-            const float w = ml[j].y * __builtin_amdgcn_exp2f(ml[j].x - top);
-            sum += there ? w : 0.0f;
+            const float w = __builtin_amdgcn_exp2f(ml[j].x - top);
+            sum = there ? __builtin_fmaf(ml[j].y, w, sum) : sum;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = there ? __builtin_fmaf((float)o[j][e], w, y[e]) : y[e];
+            for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = there ? __builtin_fmaf(o[j][e >> 2][e & 3], w, y[e >> 2][e & 3]) : y[e >> 2][e & 3];
         }
     }
 #pragma unroll
     for (int bit = kLanes; bit < 64; bit <<= 1) {
         sum += shfl_xor_f32(sum, bit);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] += shfl_xor_f32(y[e], bit);
+        for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] += shfl_xor_f32(y[e >> 2][e & 3], bit);
     }
     if (lane >= kLanes) return;
     const Seq seq{0, token, 1};
-    const float scale = vg * (1.0f / kPartScale);            // (exact)
-    store_finished<D>(a, seq, kvh, head - kvh * a.group, 8 * lane, f32x4{y[0], y[1], y[2], y[3]}, top, sum, scale);
-    store_finished<D>(a, seq, kvh, head - kvh * a.group, 8 * lane + 4, f32x4{y[4], y[5], y[6], y[7]}, top, sum, scale);
+    store_finished<D>(a, seq, kvh, head - kvh * a.group, 4 * lane, y[0], top, sum, vg);
+    store_finished<D>(a, seq, kvh, head - kvh * a.group, D / 2 + 4 * lane, y[1], top, sum, vg);
 }
 
 template <int D>
@@ -267,7 +268,7 @@ static void launch_join_rows(const AttnArgs& a, hipStream_t stream) {
     if (a.splits <= 4 * (64 / (D / 8)))
         hipLaunchKernelGGL((k_attention_join_rows<D, 4>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_attention_join_rows<D, 12>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_join_rows<D, 9>), grid, dim3(256), 0, stream, a);
 }
 hipError_t launch_attention_join_rows(const AttnArgs& a, hipStream_t stream) {
     if (a.c.head_dim == 128)

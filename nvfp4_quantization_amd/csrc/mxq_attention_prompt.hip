@@ -493,7 +493,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_prompt(const std::conditio
         for (int e = 0; e < 16; e += 4) {
             const f32x4 y = {o[dt][e], o[dt][e + 1], o[dt][e + 2], o[dt][e + 3]};
             if constexpr (RANGES)
-                store_row_part<D>(a, ((int64_t)range.part * a.total_q + seq.start + qi) * a.q_heads + head, 32 * dt + 2 * e + 4 * h, y, m, l);
+                store_part<D>(a, ((int64_t)range.part * a.total_q + seq.start + qi) * a.q_heads + head, 32 * dt + 2 * e + 4 * h, y, m, l);
             else if (used == 1)
                 store_finished<D>(a, seq, kvh, r0 + row, 32 * dt + 2 * e + 4 * h, y, m, l, vg);
             else

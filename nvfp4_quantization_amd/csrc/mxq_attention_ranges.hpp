@@ -5,12 +5,12 @@
 // min(P, p + 1) - 1 in the prefix's unit, through the pages of its group's first sequence, and
 // P .. p in its sequence's own.  In both a row's tokens are hi - count + 1 .. hi.
 //
-// What bounds it: 32 sequences, 64 query heads over 8 of 128, on 65536 shared tokens take 89 us,
-// 776 TFLOP/s: the vector and matrix instructions of the form for many rows (66 k cycles of
-// products a SIMD, 91 k of vector ones), 7 us the join of the parts, 5 the start.  64 sequences on 8192
-// tokens with 200 to 1500 of their own take 43 us: each of 256 work-groups has 16 tiles of the
-// prefix, 22 us, between a start of 5 (groups, runs, lengths, page table, queries and first tile, one
-// after another) and 2 for its parts, while the sequences' own tokens (60 MB) pass beside them.
+// What bounds it: 32 sequences, 64 query heads over 8 of 128, on 65536 shared tokens take 95 us,
+// 731 TFLOP/s: the vector and matrix instructions of the form for many rows (66 k cycles of
+// products a SIMD, 91 k of vector ones), then the parts, written and joined in FP32 (36 MB each way). 64
+// sequences on 8192 tokens with 200 to 1500 of their own take 45 us: each of 256 work-groups has 16
+// tiles of the prefix, 22 us, between a start of 5 (groups, runs, lengths, page table, queries and first
+// tile, one after another) and its parts, while the sequences' own tokens (60 MB) pass beside them.
 // Four sequences on 2048 tokens take 10.8 us: 7.8 the units, 3.3 to 4 of them until the first tile, and
 // a launch that joins.
 #pragma once

@@ -118,7 +118,7 @@ __device__ __forceinline__ void range_rows(const PrefixAttnArgs& a, const RangeU
     waves_meet<D, NT, W>(wave, L, m, l, o, nan_blocks, join);
     waves_join<D, NT, W>(area, wave, L, u.rows, o, join, [&](int r, int d0, const f32x4& y, float top, float total) {
         const RangeRow row = range_row(a, u, limits, r);
-        store_row_part<D>(a, ((int64_t)u.part * a.total_q + row.query) * a.q_heads + row.head, d0, y, top, total);
+        store_part<D>(a, ((int64_t)u.part * a.total_q + row.query) * a.q_heads + row.head, d0, y, top, total);
     });
 }
 

@@ -104,7 +104,7 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
     p->ml_offset = p->bytes = 0;
     if (p->splits > 1) {
         const int64_t parts = total_q * q_heads * p->splits;
-        p->ml_offset = (size_t)(parts * d * 2);
+        p->ml_offset = (size_t)(parts * d * 4);
         p->bytes = (size_t)round256((int64_t)p->ml_offset + parts * 8);
     }
     return true;
@@ -118,14 +118,15 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
 // much work, which then runs beside them.  Measured, one a CU / two, us (64 query heads over 8 of 128,
 // own tokens 50 to 400, the last row 500 to 4000):
 //   sequences  shared tokens                         taken
-//          16   16384    30.9 / 36.4                  one
-//          64    4096    32.8 / 39.7                  one
-//          64   16384    60.4 / 64.4                  one
-//          32   32768    59.9 / 58.9                  one
-//          32   65536   101.4 / 95.0                  two
-//          64   65536   186.1 / 161.3                 two
-//          64   32768   112.8 / 124.3 (much of own)   one
+//          16   16384    31.3 / 35.0                  one
+//          64    4096    33.0 / 39.6                  one
+//          64   16384    59.6 / 64.0                  one
+//          32   32768    58.6 / 61.2                  one
+//          32   65536   100.4 / 94.5                  two
+//          64   65536   179.5 / 161.6                 two
+//          64   32768   115.0 / 126.7 (much of own)   one
 constexpr int64_t kMaxGroups = 4096;
+constexpr int64_t kMaxRowParts = 256;          // of a prefix and of a sequence's own tokens together
 struct PrefixPlan {
     int32_t prefix_rows, own_rows, row_tiles, prefix_splits, own_splits;
     int64_t prefix_blocks, own_blocks;
@@ -158,13 +159,13 @@ bool plan_prefix(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t batch, in
     const int64_t tiles = (max_prefix + 63) / 64, own_tiles = (max_own + 63) / 64 + 1;
     const bool half = p->prefix_rows == 128 && (!product_below(usual, tiles, 1ll << 60) || usual * tiles < 80 * d ||
                                                 own_units * own_tiles > usual * tiles);
-    p->prefix_splits = (int32_t)pieces(half ? 2 * usual : usual, tiles, 4, 256);
-    p->own_splits = (int32_t)pieces(own_units, own_tiles, 4, 128);
+    p->own_splits = (int32_t)pieces(own_units, own_tiles, 4, kMaxRowParts / 2);
+    p->prefix_splits = (int32_t)pieces(half ? 2 * usual : usual, tiles, 4, kMaxRowParts - p->own_splits);
     p->prefix_blocks = prefix_units * p->prefix_splits;
     p->own_blocks = own_units * p->own_splits;
     if (p->prefix_blocks + p->own_blocks >= kMaxBlocks) return false;
     const int64_t parts = total_q * q_heads * (p->prefix_splits + p->own_splits);
-    p->ml_offset = (size_t)(parts * d * 2);
+    p->ml_offset = (size_t)(parts * d * 4);
     p->bytes = (size_t)round256((int64_t)p->ml_offset + parts * 8);
     return true;
 }
