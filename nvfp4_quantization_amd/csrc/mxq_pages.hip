@@ -375,12 +375,10 @@ template <int W>
 struct RowShared {
     int count[16];
     int2 pair[16];
-    __attribute__((aligned(16))) uint32_t column[256];
+    uint32_t column[256];
     uint32_t least;
     uint16_t list[W * kShort];        // places, ascending
 };
-static_assert(alignof(RowShared<1>) % 16 == 0 && __builtin_offsetof(RowShared<1>, column) % 16 == 0,
-              "column is cleared 16 bytes at a time");
 template <int NW>
 __device__ __forceinline__ int sum_waves(int v, int wave, int (&shared)[16]) {
     if constexpr (NW == 1) return v;
@@ -449,7 +447,9 @@ __device__ __forceinline__ void select_row(const uint32_t* keys, int n, int want
             column[2] = max(column[2], k.z), column[3] = max(column[3], k.w);
         }
         if constexpr (NW > 1) {
-            if (wave == 0) *reinterpret_cast<u32x4v*>(shared.column + 4 * lane) = u32x4v{0, 0, 0, 0};
+            if (wave == 0)                                   // (words: the columns lie on no 16-byte boundary)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) shared.column[64 * e + lane] = 0;
             __syncthreads();
             if (256 * wave < n)
 #pragma unroll
