@@ -598,6 +598,11 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
  * mxq_attention_nvfp4.  A row's work is cut into parts, over the prefix and its own tokens,
  * which are held and joined in FP32; the order of the sums depends on the lengths, the
  * groups and the estimates.
+ * The split is planned for groups of about as many queries each, and for sequences of about
+ * as many tokens of their own; others are right, but wait for the largest.  Sequences that
+ * share nothing belong in one group with prefix_lens 0, or in another's, not in groups of
+ * one.  A sequence with far more tokens of its own than the rest is better off in a call of
+ * its own.
  *   group_starts device int32[groups + 1], ascending; the first counts as 0 and the last
  *                as batch
  *   prefix_lens  device int32[batch]; held to [0, table_pages * page_size]
@@ -605,8 +610,9 @@ mxq_status mxq_attention_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_heads,
  *                behind one, which size the split (longer ones are still right)
  * workspace: device memory of mxq_attention_prefix_nvfp4_workspace_size(...) bytes, as
  * there (never 0 but for calls that do nothing or are refused).
- * Requirements: as there; 1 <= groups <= 4096; total_q * q_heads <= 2^26 - 4 and in total fewer
- * than 2^24 work-groups (the pieces of all rows; else MXQ_ERR_UNSUPPORTED).  total_q == 0 or max_q_len == 0 is a successful no-op.
+ * Requirements: as there; 1 <= groups <= 4096; total_q * q_heads <= 2^26 - 4 and in total
+ * fewer than 2^24 work-groups (the pieces of all rows; else MXQ_ERR_UNSUPPORTED).
+ * total_q == 0 or max_q_len == 0 is a successful no-op.
  * ------------------------------------------------------------------------- */
 size_t mxq_attention_prefix_nvfp4_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t batch,
                                                  int64_t groups, int64_t total_q, int64_t max_q_len,
@@ -692,14 +698,15 @@ mxq_status mxq_select_pages_nvfp4(const uint16_t* q, int64_t ld_q, int32_t q_hea
                                   int32_t* pages, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Causal attention over listed pages: the query at position p and the query heads of
- * cached head k attend the tokens t <= p of the pages pages[query][k][0 .. top - 1] of
- * their sequence (counted along its row of block_table, as mxq_select_pages_nvfp4 writes
- * them); out = 0 and lse = -inf where there is none.  Entries that are negative or above
- * p / page_size add nothing, in any place; a page that is listed twice counts twice.  The
- * arithmetic, its roundings, what NaN scales and unreadable pages do, and the other
- * arguments are those of mxq_attention_nvfp4 (few queries' lists are cut into parts, held
- * and joined in FP32).  Entries after the last that counts cost nothing.
+ * Causal attention over listed pages (without a window): the query at position p and the
+ * query heads of cached head k attend the tokens t <= p of the pages pages[query][k][0 ..
+ * top - 1] of their sequence (counted along its row of block_table, as
+ * mxq_select_pages_nvfp4 writes them); out = 0 and lse = -inf where there is none.  Entries
+ * that are negative or above p / page_size add nothing, in any place; a page that is listed
+ * twice counts twice.  The arithmetic, its roundings, what NaN scales and unreadable pages
+ * do, and the other arguments are those of mxq_attention_nvfp4 (few queries' lists are cut
+ * into parts, held and joined in FP32).  Lists are read to their end by every work-group
+ * before its first page; entries after the last that counts load nothing of the cache.
  *   pages    device int32 [total_q][kv_heads][top], 4-byte aligned
  * workspace: device memory of mxq_attention_pages_nvfp4_workspace_size(...) bytes, as there.
  * Requirements: those of mxq_attention_nvfp4 on q, out, the cache, the sequences and the

@@ -12,8 +12,8 @@
 // What bounds it: 64 queries of 64 pages of 64, 64 query heads over 8 of 128 (304 MB) take 53 us,
 // 5.8 TB/s: memory, and 4 us until the first tile (sequence, list, page table, tile: four memory
 // latencies).  1000 queries of 48 pages of 32, 32 query heads over 8 (1.8 GB by way of the L2, 0.6 of
-// it from beyond) take 238 us: a tile costs a wave some 430 vector instructions, 256 of them to
-// dequantize it for the group's four rows alone, 168 of the 238 us on every SIMD, and 40 of matrix
+// it from beyond) take 239 us: a tile costs a wave some 430 vector instructions, 256 of them to
+// dequantize it for the group's four rows alone, 168 of the 239 us on every SIMD, and 40 of matrix
 // ones beside them.  Sharing a dequantized tile takes queries that list the same pages.
 #include "mxq_attention_tile.hpp"
 

@@ -5,8 +5,8 @@
 // min(P, p + 1) - 1 in the prefix's unit, through the pages of its group's first sequence, and
 // P .. p in its sequence's own.  In both a row's tokens are hi - count + 1 .. hi.
 //
-// What bounds it: 32 sequences, 64 query heads over 8 of 128, on 65536 shared tokens take 95 us,
-// 731 TFLOP/s: the vector and matrix instructions of the form for many rows (66 k cycles of
+// What bounds it: 32 sequences, 64 query heads over 8 of 128, on 65536 shared tokens take 94 to 96
+// us, 719 to 740 TFLOP/s: the vector and matrix instructions of the form for many rows (66 k cycles of
 // products a SIMD, 91 k of vector ones), then the parts, written and joined in FP32 (36 MB each way). 64
 // sequences on 8192 tokens with 200 to 1500 of their own take 45 us: each of 256 work-groups has 16
 // tiles of the prefix, 22 us, between a start of 5 (groups, runs, lengths, page table, queries and first

@@ -23,10 +23,10 @@
 // and one wave finishes with them in registers (64 candidates a pass over LDS until then, two passes
 // in all).  Long selections and heaps of equal scores are halved by value instead.
 //
-// What bounds it: latency, mostly.  One query of 8 cached heads over 2048 pages takes 12.5 us, in two
+// What bounds it: latency, mostly.  One query of 8 cached heads over 2048 pages takes 12.2 us, in two
 // launches (4 and 8): lengths, page numbers, keys and scores come one after another, then the
-// search's ballots.  64 queries over up to 512 pages, 64 query heads over 8 (21 MB), 12.5 us in
-// one launch.  2000 queries of 24 heads of 64 over 1250 short pages 34 us: 48 of some 80 k cycles
+// search's ballots (16 waves of 128 registers a work-group, of which heads of 128 spill up to 33).  64
+// queries over up to 512 pages, 64 query heads over 8 (21 MB), 12.4 us in one launch.  2000 queries of 24 heads of 64 over 1250 short pages 34 us: 48 of some 80 k cycles
 // of a SIMD are vector instructions.
 #include "mxq_attention_nvfp4.hpp"
 

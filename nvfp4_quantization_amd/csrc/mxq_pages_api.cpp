@@ -1,6 +1,6 @@
 // mxq_pages_api.cpp -- the C ABI of the calls of include/mxq.h around long and shared
-// contexts (mean keys of pages, page selection, attention over listed pages): argument
-// checks, launch planning and kernel launches.  Host code only; nothing here allocates,
+// contexts (mean keys of pages, page selection, attention over listed pages, attention with
+// shared prefixes): argument checks, launch planning and kernel launches.  Host code only; nothing here allocates,
 // synchronizes, memsets or reads the environment.
 #include <cmath>
 
@@ -46,10 +46,11 @@ int32_t log2_of(int32_t page_size) {
 // How the selection spreads its work: queries of a work-group (for one cached head), and what is
 // held of their scores in LDS.  Several where sequences have long runs of queries, which then
 // share the mean keys that are read: two tiles of 16 rows, four of groups of more than 8 heads
-// (a query a wave then: 2000 queries of 8 heads of 128 over 1024 pages 63 us against 79 with four
-// tiles and 86 with eight; of 16 heads over 938 pages 34 with four, 58 with two).  Few queries with
-// many candidates: their scores are made by more work-groups, through the workspace (one query, 8
-// cached heads: 2048 candidates 13.5 us against 17.9, 8192 16 against 41).
+// (a query a wave then: 2000 queries over 1024 pages, 16 heads over 2 of 128, 28.4 us against 30.4
+// with four tiles, 16 over 4 of 64 22.9 against 30.3; 32 over 2 of 64 over 938 pages 19.8 with four,
+// 32.9 with two).  Few queries with many candidates: their scores are made by more work-groups,
+// through the workspace (one query, 8 cached heads: 2048 candidates 12.2 us against 17.0, 8192 15.4
+// against 45.5).
 constexpr int64_t kHeldScores = 14336;         // 56 KB, of one query
 constexpr int64_t kHeldScoresRun = 12288;      // 48 KB, of several (whose waves need more beside them)
 struct SelectPlan {
@@ -79,9 +80,9 @@ SelectPlan plan_select(int64_t group, int64_t kv_heads, int64_t page_size, int64
 
 // How attention over listed pages splits its work: a unit is (query, cached head, 16 or 32 rows
 // of its group).  Few units go over several work-groups, a tile a wave where a CU each is enough
-// for them, else two (4 sequences, 8 cached heads, 64 pages of 64 in 8 pieces 11.0 us, in 16
-// 11.8; one sequence in 16 9.0, in 8 10.5).  From 2048 units on a wave takes one alone: 8000 of
-// 24 tiles 241 us against 267 by four waves each, which have to meet.
+// for them, else two (4 sequences, 8 cached heads, 64 pages of 64 in 8 pieces 12.0 us, in 16
+// 13.7; one sequence's 32 pages in 8 pieces 9.9, in 4 11.3).  From 2048 units on a wave takes one
+// alone: 8000 of 24 tiles 241 us against 267 by four waves each, which have to meet.
 struct PagesPlan {
     int32_t tile_rows, row_tiles, waves, splits;
     size_t ml_offset, bytes;
@@ -113,9 +114,11 @@ bool plan_pages(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
 // How attention with shared prefixes splits its work.  A group's rows over its prefix, and a
 // sequence's over its own tokens, come in tiles of 16, 32 or 128: the first two by the waves'
 // own tiles, 128 by the form for many rows, all in one launch.  Pieces of both until it fills the
-// chip.  Of the prefixes, in the form for many rows, a work-group a CU, where two would have few tiles
-// each (their rows' parts have to be written, read and joined) or the sequences' own tokens are as
-// much work, which then runs beside them.  Measured, one a CU / two, us (64 query heads over 8 of 128,
+// chip, all by the mean group and the longest estimates (32 sequences on 65536 tokens beside 32
+// without a prefix, 64 query heads over 8 of 128: 110 us in two groups, 350 in 33).  Of the
+// prefixes, in the form for many rows, a work-group a CU, where two would have few tiles each
+// (their rows' parts have to be written, read and joined) or the sequences' own tokens are as much
+// work, which then runs beside them.  Measured, one a CU / two, us (64 query heads over 8 of 128,
 // own tokens 50 to 400, the last row 500 to 4000):
 //   sequences  shared tokens                         taken
 //          16   16384    31.3 / 35.0                  one

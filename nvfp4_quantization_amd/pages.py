@@ -1,6 +1,6 @@
 """The serving calls for long and shared contexts: attention with shared prefixes; mean keys
-of a cache's pages, the pages each query attends, and attention over those alone.  Prepared calls (classes) and the functions
-of the C names, as in serve.py."""
+of a cache's pages, the pages each query attends, and attention over those alone.  Prepared
+calls (classes) and the functions of the C names, as in serve.py."""
 from __future__ import annotations
 
 import ctypes
@@ -70,8 +70,9 @@ class AttentionPrefixNVFP4(_Prepared):
     int32 [groups + 1], the first sequence of each group and batch; prefix_lens: int32
     [batch], the tokens of each sequence that are read through the pages of its group's
     first.  max_prefix_len, max_own_len (default: what the table can hold) bound the longest
-    prefix and the most tokens behind one, to plan the split for.  The rest as
-    AttentionNVFP4, without a window."""
+    prefix and the most tokens behind one, to plan the split for.  Sequences that share
+    nothing belong in one group with prefix_lens 0, not in groups of one (the split is planned
+    for groups of about the same size).  The rest as AttentionNVFP4, without a window."""
 
     def __init__(self, q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
                  q_starts: torch.Tensor, group_starts: torch.Tensor, prefix_lens: torch.Tensor, max_q_len: int,
@@ -225,7 +226,8 @@ def mxq_attention_pages_nvfp4_workspace_size(q_heads: int, kv_heads: int, head_d
 
 class AttentionPagesNVFP4(_Prepared):
     """A prepared attention call over listed pages of an NVFP4KVCache.  pages: int32
-    [total_q][kv_heads][top], as SelectPagesNVFP4 writes them; the rest as AttentionNVFP4."""
+    [total_q][kv_heads][top], as SelectPagesNVFP4 writes them; the rest as AttentionNVFP4,
+    without a window."""
 
     def __init__(self, q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
                  q_starts: torch.Tensor, pages: torch.Tensor, scale: Optional[float] = None, lse: bool = False,
