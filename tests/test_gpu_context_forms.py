@@ -181,6 +181,36 @@ def test_more_parts_than_tokens():
         assert parts_of(c.prepared(dev, max_prefix_len=1 << 24, max_own_len=1 << 24), c) == 256
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("d,page,batch,nq,group", [(64, 16, 4, 1, 3), (128, 64, 3, 3, 7), (128, 16, 14, 1, 3), (64, 64, 2, 150, 1)])
+def test_rows_beside_one_that_is_no_number(batch, nq, group, page, d, what):
+    """NaN, infinities or the largest numbers in one query and head: every other row's bits stay."""
+    dev = device()
+    announce(f"one row of {what} batch={batch} nq={nq} group={group} page={page} d={d}")
+    c = Case([0, batch], [4 * page + 3] * batch, [5 * page + nq + 9 * b for b in range(batch)], [nq] * batch, 2 * group, 2, d, page,
+             seed=page + d)
+    c.table[1:, :4] = c.table[0, :4]                                     # (for the lists: a row of its own for each)
+    lists = torch.from_numpy(cu.random_lists(c, 4, seed=d)).to(dev)
+
+    def results():
+        shared = c.prepared(dev, lse=True)()
+        listed = mxq.mxq_attention_pages_nvfp4(c.device_q(dev), c.device_cache(dev), *c.device_sequences(dev), lists, lse=True)
+        torch.cuda.synchronize()
+        return [su.f32_of_bf16(shared.out), host(shared.lse), su.f32_of_bf16(listed.out), host(listed.lse)]
+
+    clean = results()
+    assert all(np.isfinite(x).all() for x in clean)
+    row, head = c.total // 2, c.hq - 1
+    c.q[row, head, ::3] = su.to_bf16(np.full(c.d, what, np.float32))[::3]
+    got = results()
+    for x, y in zip(got, clean):
+        if what != 3e38:
+            assert np.isnan(x[row, head]).all()
+        x, y = x.copy(), y.copy()
+        x[row, head] = y[row, head] = 0
+        assert_same("the other rows", x, y)
+
+
 # ------------------------------------------------------------------ mean keys on two streams
 def test_mean_keys_and_selection_on_two_streams():
     """Two servers' steps at once: each updates mean keys and selects by them, on a stream of its own."""
